@@ -300,6 +300,75 @@ moe_status moe_router_topk_noalloc(const moe_config* cfg, const void* x, const f
                                    int32_t* ids, float* gates, float* probs, int32_t* slot, int32_t* row_of,
                                    int32_t* src_token, int32_t* counts, int32_t* offsets, moe_stream_t stream);
 
+/* ---- Operators around the layer in a transformer block ----
+ * The block is out = x + dropout(layer(norm(x))): moe_norm_fwd in front of the
+ * layer, moe_dropout_add behind it, their backward passes, and the whole layer
+ * for the few tokens of a serving step.  (The pages have no counterpart.)
+ * Rows are dense; x, y, dy, dx, out and the residuals use `dtype` (moe_dtype)
+ * and are 16-byte aligned, gamma, beta, the statistics and dgamma, dbeta are
+ * float32.  1 <= d <= 65536, of any parity; rows * d <= 2^40. */
+
+/* Most tokens of one moe_layer_decode call. */
+#define MOE_DECODE_MAX_T 64
+
+/* Bytes of workspace that moe_layer_decode needs for cfg.  Host only; it
+ * scales with the SM count of the current device, so ask with the device that
+ * will run the layer current. */
+moe_status moe_decode_workspace_size(const moe_config* cfg, size_t* bytes);
+
+/* The whole layer for a few tokens (T <= MOE_DECODE_MAX_T) in one kernel:
+ *   y[t] = residual[t] + sum over kept j of gates[t,j] * (silu(x_t W1_e) * (x_t W3_e)) W2_e,
+ * e = ids[t, j].  Routing, ties, gates, capacity and dropped assignments are
+ * those of moe_router_topk; residual (NULL: none), ids and gates (NULL: not
+ * wanted) as there.  Only the weights of experts with kept rows are read.  a
+ * and b are fp32 sums and are not rounded to the activations' type, so y
+ * carries one rounding to it.
+ * Deterministic.  It is a cooperative launch of one block an SM: on a GPU that
+ * other streams keep busy it starts when all its blocks fit.  residual may
+ * be y; x must not overlap y. */
+moe_status moe_layer_decode(const moe_config* cfg, const moe_weights* w, const void* x, const void* residual, void* y,
+                            int32_t* ids, float* gates, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Layer norm of each row:
+ *   mean = sum(x) / d;  rstd = 1 / sqrt(sum((x - mean)^2) / d + eps)
+ *   y = (x - mean) * rstd * gamma + beta
+ * with fp32 statistics.  mean and rstd [rows] may be NULL (inference).  y may
+ * be x.  eps >= 0. */
+moe_status moe_norm_fwd(int64_t rows, int32_t d, int32_t dtype, const void* x, const float* gamma, const float* beta,
+                        float eps, void* y, float* mean, float* rstd, moe_stream_t stream);
+
+/* Bytes of workspace that moe_norm_bwd needs: partial sums of dgamma and
+ * dbeta, at most two rows of d an SM.  Host only; device as above. */
+moe_status moe_norm_workspace_size(int64_t rows, int32_t d, size_t* bytes);
+
+/* Backward of moe_norm_fwd, n = (x - mean) * rstd, v = dy * gamma:
+ *   dx = rstd * (v - sum(v) / d - n * sum(v n) / d) + dres
+ *   dgamma (+)= sum over rows of dy * n;  dbeta (+)= sum over rows of dy
+ * dres (NULL: none) is the gradient that reaches x past the norm, on the
+ * residual branch; dx may be x, dy or dres.  accumulate as in moe_layer_bwd.
+ * Sums run in an order fixed by the sizes and the device. */
+moe_status moe_norm_bwd(int64_t rows, int32_t d, int32_t dtype, const void* x, const void* dy, const float* gamma,
+                        const float* mean, const float* rstd, const void* dres, void* dx, float* dgamma, float* dbeta,
+                        int accumulate, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Dropout of n elements behind the layer, with the residual added:
+ *   out[i] = residual[i] + (u_i >= cut ? y[i] * 65536 / (65536 - cut) : 0)
+ * cut = floor(65536 p + 1/2); 0 <= p < 1 and cut < 65536.  u_i are 16-bit
+ * draws of Philox-4x32-10: element i takes 16-bit part i % 8 (low half of a
+ * 32-bit word first) of the block whose counter is the 64-bit pair
+ * (i / 8, offset) and whose key is seed.  The mask depends on (seed, offset, i)
+ * alone and is never stored: give each layer and step its own offset.  A
+ * dropped element contributes 0 whatever y[i] is.  residual may be NULL; out
+ * may be y or residual. */
+moe_status moe_dropout_add(int64_t n, int32_t dtype, const void* y, const void* residual, void* out, float p,
+                           uint64_t seed, uint64_t offset, moe_stream_t stream);
+
+/* Its gradient, with the mask drawn again from the same seed and offset:
+ *   dy[i] = u_i >= cut ? dout[i] * 65536 / (65536 - cut) : 0
+ * (the residual's gradient is dout itself).  dy may be dout. */
+moe_status moe_dropout_bwd(int64_t n, int32_t dtype, const void* dout, void* dy, float p, uint64_t seed,
+                           uint64_t offset, moe_stream_t stream);
+
 /* Waits for the current device to finish, then reads the device error word:
  * *code is MOE_OK, MOE_ERR_DEVICE_CHECK or MOE_ERR_TIMEOUT, *detail says which
  * kernel and check; clear != 0 resets the word.  Either output may be NULL. */

@@ -6,8 +6,9 @@ current stream to the C ABI of ``libmoe_gb300.so``.  All arithmetic runs in
 the library's CUDA kernels.  If the library has not been built the import of
 any entry point raises; there is no fallback.
 
-Helpers ``allocate_saved``, ``allocate_grads`` and ``workspace`` size buffers
-with ``moe_max_rows`` / ``moe_workspace_size`` and allocate them with torch.
+Helpers ``allocate_saved``, ``allocate_grads``, ``workspace``, ``decode_workspace``
+and ``norm_workspace`` size buffers with ``moe_max_rows`` and the
+``moe_*workspace_size`` calls and allocate them with torch.
 """
 from __future__ import annotations
 
@@ -55,6 +56,8 @@ class MoeGrads(ctypes.Structure):
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
+_U = ctypes.c_uint64
 _CFG = ctypes.POINTER(MoeConfig)
 
 # name -> argtypes (all return int status unless listed in _RESTYPES)
@@ -74,6 +77,13 @@ _SIGNATURES = {
     "moe_aux_loss": [_CFG, _P, _P, _P, _P, _P, _Z, _P],
     "moe_layer_bwd": [_CFG, ctypes.POINTER(MoeWeights), _P, _P, ctypes.POINTER(MoeSaved), _P,
                       ctypes.POINTER(MoeGrads), _I, _P, _Z, _P],
+    "moe_decode_workspace_size": [_CFG, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_layer_decode": [_CFG, ctypes.POINTER(MoeWeights), _P, _P, _P, _P, _P, _P, _Z, _P],
+    "moe_norm_fwd": [_L, _I, _I, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P],
+    "moe_norm_workspace_size": [_L, _I, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_norm_bwd": [_L, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _Z, _P],
+    "moe_dropout_add": [_L, _I, _P, _P, _P, ctypes.c_float, _U, _U, _P],
+    "moe_dropout_bwd": [_L, _I, _P, _P, ctypes.c_float, _U, _U, _P],
     "moe_get_device_error": [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32), _I],
     "moe_launch_count": [],
     "moe_selftest_bounded_wait": [ctypes.c_int64, _I, _P],
@@ -161,6 +171,18 @@ def moe_max_rows(cfg: MoeConfig) -> int:
 def moe_workspace_size(cfg: MoeConfig, training: int) -> int:
     b = ctypes.c_size_t()
     _check("moe_workspace_size", lib().moe_workspace_size(ctypes.byref(cfg), int(training), ctypes.byref(b)))
+    return b.value
+
+
+def moe_decode_workspace_size(cfg: MoeConfig) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_decode_workspace_size", lib().moe_decode_workspace_size(ctypes.byref(cfg), ctypes.byref(b)))
+    return b.value
+
+
+def moe_norm_workspace_size(rows: int, d: int) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_norm_workspace_size", lib().moe_norm_workspace_size(rows, d, ctypes.byref(b)))
     return b.value
 
 
@@ -258,6 +280,94 @@ def moe_layer_bwd(cfg, weights: dict, x, dy, saved: dict, dx, grads: dict, accum
         int(accumulate), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
 
 
+# ----------------------------- around the layer -------------------------- #
+def _same(name: str, t, like, dtype=None) -> Optional[int]:
+    """Pointer of ``t`` (or None), which has to be as large as ``like`` and of its (or the given) type."""
+    if t is None:
+        return None
+    if t.dtype != (like.dtype if dtype is None else dtype):
+        raise TypeError(f"{name} has type {t.dtype}")
+    if t.numel() != like.numel():
+        raise ValueError(f"{name} has {t.numel()} elements, not {like.numel()}")
+    return _ptr(t)
+
+
+def _vec(name: str, t, n: int, dtype=None) -> Optional[int]:
+    """Pointer of ``t`` (or None), which has to have ``n`` elements of float32 (or the given type)."""
+    if t is None:
+        return None
+    import torch
+
+    if t.dtype != (torch.float32 if dtype is None else dtype):
+        raise TypeError(f"{name} has type {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+    return _ptr(t)
+
+
+def _dtype(t) -> int:
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return MOE_BF16
+    if t.dtype == torch.float32:
+        return MOE_F32
+    raise TypeError(f"expected a bfloat16 or float32 tensor, not {t.dtype}")
+
+
+def _rows(x):
+    """(rows, d) of [..., d]."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError("expected rows of at least one element")
+    return x.numel() // x.shape[-1], x.shape[-1]
+
+
+def moe_layer_decode(cfg: MoeConfig, weights: dict, x, residual, y, ids, gates, ws, stream=None) -> None:
+    """The whole layer for at most 64 tokens in one kernel: y = layer(x) [+ residual].
+
+    ``residual``, ``ids`` [T, k] int32 and ``gates`` [T, k] float32 may be None.
+    """
+    import torch
+
+    n, Tk = cfg.T * cfg.d_model, cfg.T * cfg.k
+    act = torch.bfloat16 if cfg.dtype == MOE_BF16 else torch.float32
+    w = _weights(weights)
+    _check("moe_layer_decode", lib().moe_layer_decode(
+        ctypes.byref(cfg), ctypes.byref(w), _vec("x", x, n, act), _vec("residual", residual, n, act),
+        _vec("y", y, n, act), _vec("ids", ids, Tk, torch.int32), _vec("gates", gates, Tk), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_norm_fwd(x, gamma, beta, eps: float, y, mean=None, rstd=None, stream=None) -> None:
+    """Layer norm of the rows of x [..., d]; ``mean`` and ``rstd`` [rows] float32 are kept for the backward."""
+    rows, d = _rows(x)
+    _check("moe_norm_fwd", lib().moe_norm_fwd(
+        rows, d, _dtype(x), _ptr(x), _vec("gamma", gamma, d), _vec("beta", beta, d), eps, _same("y", y, x),
+        _vec("mean", mean, rows), _vec("rstd", rstd, rows), _stream(stream)))
+
+
+def moe_norm_bwd(x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, accumulate: bool, ws, stream=None) -> None:
+    """dx (+ dres), dgamma and dbeta of the layer norm; ``dres`` may be None."""
+    rows, d = _rows(x)
+    _check("moe_norm_bwd", lib().moe_norm_bwd(
+        rows, d, _dtype(x), _ptr(x), _same("dy", dy, x), _vec("gamma", gamma, d), _vec("mean", mean, rows),
+        _vec("rstd", rstd, rows), _same("dres", dres, x), _same("dx", dx, x), _vec("dgamma", dgamma, d),
+        _vec("dbeta", dbeta, d), int(accumulate), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def moe_dropout_add(y, residual, out, p: float, seed: int, offset: int, stream=None) -> None:
+    """out = residual + dropout(y), the mask drawn from (seed, offset, element); ``residual`` may be None."""
+    _check("moe_dropout_add", lib().moe_dropout_add(
+        y.numel(), _dtype(y), _ptr(y), _same("residual", residual, y), _same("out", out, y), p, seed, offset,
+        _stream(stream)))
+
+
+def moe_dropout_bwd(dout, dy, p: float, seed: int, offset: int, stream=None) -> None:
+    """dy = the gradient of dropout(y), with the mask of the same seed and offset."""
+    _check("moe_dropout_bwd", lib().moe_dropout_bwd(
+        dout.numel(), _dtype(dout), _ptr(dout), _same("dy", dy, dout), p, seed, offset, _stream(stream)))
+
+
 def moe_get_device_error(clear: bool = True):
     """(code, detail) from the device error word; waits for the device."""
     c, d = ctypes.c_int32(), ctypes.c_int32()
@@ -350,3 +460,17 @@ def workspace(cfg: MoeConfig, training: int, device="cuda"):
     import torch
 
     return torch.empty(moe_workspace_size(cfg, training), dtype=torch.uint8, device=device)
+
+
+def decode_workspace(cfg: MoeConfig, device="cuda"):
+    """Workspace of ``moe_layer_decode``, kept from call to call."""
+    import torch
+
+    return torch.empty(moe_decode_workspace_size(cfg), dtype=torch.uint8, device=device)
+
+
+def norm_workspace(rows: int, d: int, device="cuda"):
+    """Workspace of ``moe_norm_bwd``, kept from call to call."""
+    import torch
+
+    return torch.empty(moe_norm_workspace_size(rows, d), dtype=torch.uint8, device=device)

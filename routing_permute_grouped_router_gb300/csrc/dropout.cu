@@ -1,0 +1,127 @@
+// Dropout whose mask is drawn from a counter and never stored, with the
+// residual added in the same pass; the backward draws the same mask again.
+//
+// The generator is Philox-4x32-10 (J. Salmon, M. Moraes, R. Dror, D. Shaw,
+// "Parallel random numbers: as easy as 1, 2, 3", SC 2011).  The block
+// b = i / 8 of element i has the counter (b, offset), two 64-bit numbers, and
+// the key is the seed; the 128 bits of a block are eight draws of 16 bits, low
+// half of a word first.  Element i is kept when its draw is at least
+// cut = round(65536 p), and scaled by 65536 / (65536 - cut).
+//
+// A draw has 16 bits rather than 32 so that one block serves eight elements, a
+// 16-byte vector of bf16: half the integer work an element.  p is then
+// realised to within 2^-17, and the scale is the inverse of the realised rate,
+// so the expectation of the output is exact.
+#include "block.h"
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int DROP_THREADS = 256;
+
+struct DropArgs {
+  const void* y;
+  const void* residual;
+  void* out;
+  int64_t n;
+  uint64_t seed, offset;
+  uint32_t cut;
+  float scale;
+};
+
+__device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
+  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p0 = (uint64_t)0xD2511F53u * c0, p1 = (uint64_t)0xCD9E8D57u * c2;
+    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)p1;
+    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)p0;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// keep or drop the eight values of a block; a dropped value is 0 whatever it was (infinities and NaN too)
+__device__ __forceinline__ void drop8(float (&v)[8], const uint4& u, uint32_t cut, float scale) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t r = (i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+    v[i] = r >= cut ? v[i] * scale : 0.f;
+  }
+}
+
+// plain loads, not the read-only path: out may be y or the residual
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8 / Vec<T>::N; ++q) {
+    float w[Vec<T>::N];
+    unpack(*reinterpret_cast<const uint4*>(p + q * Vec<T>::N), w);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) v[q * Vec<T>::N + i] = w[i];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8 / Vec<T>::N; ++q) {
+    float w[Vec<T>::N];
+#pragma unroll
+    for (int i = 0; i < Vec<T>::N; ++i) w[i] = v[q * Vec<T>::N + i];
+    stg16(p + q * Vec<T>::N, pack(w));
+  }
+}
+
+template <typename T, bool RES>
+__global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const DropArgs a) {
+  pdl_enter();  // see pdl_wait: no global access before this
+  const T* y = static_cast<const T*>(a.y);
+  const T* res = static_cast<const T*>(a.residual);
+  T* out = static_cast<T*>(a.out);
+  const int64_t blocks = (a.n + 7) / 8, step = (int64_t)gridDim.x * DROP_THREADS;
+  for (int64_t b = (int64_t)blockIdx.x * DROP_THREADS + threadIdx.x; b < blocks; b += step) {
+    const int64_t i0 = b * 8;
+    float v[8], r[8];
+    if (i0 + 8 <= a.n) {
+      load8(y + i0, v);
+      if (RES) load8(res + i0, r);
+      drop8(v, philox((uint64_t)b, a.offset, a.seed), a.cut, a.scale);
+      if (RES) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += r[i];
+      }
+      store8(out + i0, v);
+    } else {  // the last, short block
+      const int m = (int)(a.n - i0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < m ? to_f32(y[i0 + i]) : 0.f;
+      drop8(v, philox((uint64_t)b, a.offset, a.seed), a.cut, a.scale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < m) out[i0 + i] = from_f32<T>(RES ? v[i] + to_f32(res[i0 + i]) : v[i]);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_dropout(int kind, int64_t n, bool bf16, const void* y, const void* residual, void* out,
+                           uint32_t cut, uint64_t seed, uint64_t offset, cudaStream_t st) {
+  const DropArgs a{y, residual, out, n, seed, offset, cut, (float)(65536.0 / (65536.0 - cut))};
+  const int64_t need = ((n + 7) / 8 + DROP_THREADS - 1) / DROP_THREADS, most = (int64_t)sm_count() * 8;
+  const dim3 grid((unsigned)(need < most ? need : most)), block(DROP_THREADS);
+  LaunchScope ls(kind, st);
+  if (bf16)
+    return residual ? launch_pdl(dropout_kernel<__nv_bfloat16, true>, grid, block, 0, st, a)
+                    : launch_pdl(dropout_kernel<__nv_bfloat16, false>, grid, block, 0, st, a);
+  return residual ? launch_pdl(dropout_kernel<float, true>, grid, block, 0, st, a)
+                  : launch_pdl(dropout_kernel<float, false>, grid, block, 0, st, a);
+}
+
+}  // namespace moe

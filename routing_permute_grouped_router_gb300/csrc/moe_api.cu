@@ -11,7 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/moe.h"
-#include "internal.h"
+#include "block.h"
 
 namespace moe {
 
@@ -79,11 +79,12 @@ cudaEvent_t pool_event() {
   return e;
 }
 
-const char* const kKernelNames[KK_COUNT] = {
+const char* const kKernelNames[KK_ALL] = {
     "router_topk",  "slot_scan",  "slot_assign",     "permute",      "gemm_up_swiglu", "gemm_down",
     "unpermute_combine", "combine_bwd", "gemm_dgrad_h_swiglu_bwd", "gemm_wgrad", "gemm_dgrad_x",
     "transpose_wr", "dx_router",  "dwr",     "dwr_reduce",   "zero", "split_wr", "selftest_bounded_wait",
-    "split_dl", "aux_loss", "aux_grad", "router_logit_grad"};
+    "split_dl", "aux_loss", "aux_grad", "router_logit_grad", "layer_decode", "norm_fwd", "norm_bwd", "norm_bwd_reduce",
+    "dropout_add", "dropout_bwd"};
 
 }  // namespace
 
@@ -764,22 +765,22 @@ moe_status moe_nvtx_enable(int on) {
   return MOE_OK;
 }
 
-int32_t moe_kernel_kinds(void) { return KK_COUNT; }
+int32_t moe_kernel_kinds(void) { return KK_ALL; }
 
 moe_status moe_profiler_filter(int32_t id) {
-  if (id >= KK_COUNT) return MOE_ERR_INVALID_ARG;
+  if (id >= KK_ALL) return MOE_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lk(g_prof_mu);
   g_prof_filter = id < 0 ? -1 : id;
   return MOE_OK;
 }
 
 const char* moe_kernel_name(int32_t id) {
-  if (id < 0 || id >= KK_COUNT) return nullptr;
+  if (id < 0 || id >= KK_ALL) return nullptr;
   return kKernelNames[id];
 }
 
 moe_status moe_profiler_read(int32_t id, int64_t* launches, double* total_ms) {
-  if (id < 0 || id >= KK_COUNT) return MOE_ERR_INVALID_ARG;
+  if (id < 0 || id >= KK_ALL) return MOE_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lk(g_prof_mu);
   int64_t n = 0;
   double ms = 0.0;

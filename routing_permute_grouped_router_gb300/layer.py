@@ -1,8 +1,11 @@
-"""A mixture-of-experts layer held on one GPU, driven through the C ABI.
+"""A mixture-of-experts layer, and the transformer sub-block around it, held on one GPU.
 
 ``MoELayer`` owns the device copies of the weights, the saved routing state,
 the float32 gradient buffers and the workspace (allocated with torch), and
-calls ``moe_layer_fwd`` / ``moe_layer_bwd``.  It does no arithmetic itself.
+calls ``moe_layer_fwd`` / ``moe_layer_bwd``.  ``MoEBlock`` puts the layer norm in
+front of it and the residual dropout behind it, for training, and runs the
+serving step of a few tokens with ``moe_layer_decode``.  Neither does arithmetic
+itself.
 """
 from __future__ import annotations
 
@@ -10,8 +13,9 @@ from typing import Optional
 
 import torch
 
-from . import (MOE_BF16, MoeConfig, allocate_grads, allocate_saved, moe_layer_bwd, moe_layer_fwd, moe_max_rows,
-               workspace)
+from . import (MOE_BF16, MoeConfig, allocate_grads, allocate_saved, decode_workspace, moe_dropout_add,
+               moe_dropout_bwd, moe_layer_bwd, moe_layer_decode, moe_layer_fwd, moe_max_rows, moe_norm_bwd,
+               moe_norm_fwd, norm_workspace, workspace)
 
 
 class MoELayer:
@@ -42,6 +46,63 @@ class MoELayer:
         moe_layer_bwd(self.cfg, self.weights, x, dy, self.saved, self.dx, self.grads, int(accumulate), self.ws,
                       stream)
         return self.dx
+
+
+class MoEBlock:
+    """out = x + dropout(layer(norm(x))), its backward, and the same for a few tokens without dropout.
+
+    ``layer`` is a ``MoELayer``; gamma and beta [d] float32 are the norm's weights, whose gradients are in
+    ``dgamma`` and ``dbeta``.  The dropout's mask is a function of (seed, offset): the backward is given the
+    forward's.  Give each layer and step its own offset.
+    """
+
+    def __init__(self, layer: MoELayer, gamma: torch.Tensor, beta: torch.Tensor, p: float = 0.0, eps: float = 1e-5):
+        self.layer, self.p, self.eps = layer, p, eps
+        self.gamma, self.beta = gamma.contiguous(), beta.contiguous()
+        cfg, dev = layer.cfg, layer.device
+        T, d = max(cfg.T, 1), cfg.d_model
+        self.h = torch.empty(T, d, dtype=layer.act_dtype, device=dev)
+        self.out = torch.empty_like(self.h)
+        self._decode = {}  # tokens -> config and buffers
+        self._decode_ws = None
+        if layer.training:
+            f32 = dict(dtype=torch.float32, device=dev)
+            self.mean, self.rstd = torch.empty(T, **f32), torch.empty(T, **f32)
+            self.dgamma, self.dbeta = torch.zeros(d, **f32), torch.zeros(d, **f32)
+            self.dy = torch.empty_like(self.h)
+            self.dx = torch.empty_like(self.h)
+            self.ws = norm_workspace(T, d, dev)
+        else:
+            self.mean = self.rstd = None
+
+    def forward(self, x: torch.Tensor, seed: int = 0, offset: int = 0, stream=None) -> torch.Tensor:
+        moe_norm_fwd(x, self.gamma, self.beta, self.eps, self.h, self.mean, self.rstd, stream)
+        y = self.layer.forward(self.h, stream)
+        moe_dropout_add(y, x, self.out, self.p if self.layer.training else 0.0, seed, offset, stream)
+        return self.out
+
+    def backward(self, x: torch.Tensor, dout: torch.Tensor, accumulate: bool, seed: int = 0, offset: int = 0,
+                 stream=None) -> torch.Tensor:
+        moe_dropout_bwd(dout, self.dy, self.p, seed, offset, stream)
+        dh = self.layer.backward(self.h, self.dy, accumulate, stream)
+        moe_norm_bwd(x, dh, self.gamma, self.mean, self.rstd, dout, self.dx, self.dgamma, self.dbeta, accumulate,
+                     self.ws, stream)
+        return self.dx
+
+    def decode(self, x: torch.Tensor, stream=None) -> torch.Tensor:
+        """x + layer(norm(x)) for at most 64 tokens, in two kernels."""
+        T = x.shape[0]
+        if T not in self._decode:
+            c = self.layer.cfg
+            cfg = MoeConfig(T, c.d_model, c.d_ff, c.E, c.k, c.capacity_factor, c.capacity, c.dtype, 0.0)
+            ws = decode_workspace(cfg, self.layer.device)
+            if self._decode_ws is None or ws.numel() > self._decode_ws.numel():
+                self._decode_ws = ws
+            self._decode[T] = (cfg, torch.empty_like(x), torch.empty_like(x))
+        cfg, h, out = self._decode[T]
+        moe_norm_fwd(x, self.gamma, self.beta, self.eps, h, None, None, stream)
+        moe_layer_decode(cfg, self.layer.weights, h, x, out, None, None, self._decode_ws, stream)
+        return out
 
 
 def from_workload(wl, device="cuda", training: bool = True, T: Optional[int] = None,
