@@ -42,23 +42,12 @@ struct SimtSmem {
   };
 };
 
-__device__ __forceinline__ void ld4(const float* p, float (&v)[4]) { unpack(ldg16(p), v); }
-__device__ __forceinline__ void ld4(const __nv_bfloat16* p, float (&v)[4]) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  const float2 a = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(u.x));
-  const float2 b = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(u.y));
-  v[0] = a.x;
-  v[1] = a.y;
-  v[2] = b.x;
-  v[3] = b.y;
-}
-
 // out[m][c] = sum over rows k0..k1 of in(m, k) * W[k][c] for up to SM_TOK
 // inputs and the 128 columns at c0 (`width` columns wide); the warps take
 // rows in turn and add up through shared memory.  out(m, c, value) is called
 // once for each of the n x 128 sums.
-template <typename T, typename In, typename Out>
-__device__ __forceinline__ void thin_product(SimtSmem& S, const T* W, int width, int c0, int k0, int k1, int n, In in,
+template <typename In, typename Out>
+__device__ __forceinline__ void thin_product(SimtSmem& S, const float* W, int width, int c0, int k0, int k1, int n, In in,
                                              Out out) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = c0 + lane * 4;
   float acc[SM_TOK][4];
@@ -78,7 +67,7 @@ __device__ __forceinline__ void thin_product(SimtSmem& S, const T* W, int width,
 #pragma unroll 4
       for (int r = warp; r < nk; r += SM_WARPS) {
         float w[4];
-        ld4(W + (int64_t)(kc + r) * width + c, w);
+        unpack(ldg16(W + (int64_t)(kc + r) * width + c), w);
 #pragma unroll
         for (int m = 0; m < SM_TOK; ++m)
 #pragma unroll
@@ -101,14 +90,13 @@ __device__ __forceinline__ void thin_product(SimtSmem& S, const T* W, int width,
   }
 }
 
-template <typename T>
 __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant__ DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimtSmem& S = *reinterpret_cast<SimtSmem*>(smem_raw);
   Routing& R = S.R;
-  route<T, SM_NT>(a, S.score, R);
+  route<float, SM_NT>(a, S.score, R);
   const int G = gridDim.x, c = blockIdx.x, tid = threadIdx.x;
-  const T* x = static_cast<const T*>(a.io.x);
+  const float* x = static_cast<const float*>(a.io.x);
   float* h = static_cast<float*>(a.h);
   const int FT = (a.f + DEC_N - 1) / DEC_N, DT = (a.d + DEC_N - 1) / DEC_N;
   const int KU = (a.d + SM_KR - 1) / SM_KR, KD = (a.f + SM_KR - 1) / SM_KR;
@@ -138,12 +126,12 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
       const int e = R.act[tile / FT], f0 = (int)(tile % FT) * DEC_N, n = R.cnt[e], base = R.base[e];
       const int k0 = kb0 * SM_KR, k1 = kb1 * SM_KR < a.d ? kb1 * SM_KR : a.d;
       float* part = a.up_part + ((int64_t)c * 2 + (kb0 > 0 ? 0 : 1)) * pslot;
-      const T* W[2] = {static_cast<const T*>(a.io.W1) + (int64_t)e * a.d * a.f,
-                       static_cast<const T*>(a.io.W3) + (int64_t)e * a.d * a.f};
+      const float* W[2] = {static_cast<const float*>(a.io.W1) + (int64_t)e * a.d * a.f,
+                       static_cast<const float*>(a.io.W3) + (int64_t)e * a.d * a.f};
       for (int m0 = 0; m0 < n; m0 += SM_TOK)
         for (int q = 0; q < 2; ++q)
           thin_product(S, W[q], a.f, f0, k0, k1, n - m0 < SM_TOK ? n - m0 : SM_TOK,
-                       [&](int m, int k) { return to_f32(x[(int64_t)R.tok[base + m0 + m] * a.d + k]); },
+                       [&](int m, int k) { return x[(int64_t)R.tok[base + m0 + m] * a.d + k]; },
                        [&](int m, int col, float v) { part[(int64_t)(m0 + m) * 2 * DEC_N + q * DEC_N + col] = v; });
       if (kb0 > 0 || kb1 < KU) {  // shared: tell the others of the tile
         __threadfence();
@@ -175,11 +163,11 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
   const int64_t dslot = (int64_t)a.T * DEC_N;
   const int64_t per = (int64_t)R.nact * KD;  // units of a column tile: all experts' rows of W2
   const Split down(per * DT, G);
-  const T* res = static_cast<const T*>(a.io.residual);
-  T* y = static_cast<T*>(a.io.y);
+  const float* res = static_cast<const float*>(a.io.residual);
+  float* y = static_cast<float*>(a.io.y);
   if (down.U == 0) {  // every assignment was dropped
     for (int64_t i = (int64_t)c * SM_NT + tid; i < (int64_t)a.T * a.d; i += (int64_t)G * SM_NT)
-      y[i] = res ? res[i] : from_f32<T>(0.f);
+      y[i] = res ? res[i] : 0.f;
     return;
   }
   auto finish_down = [&](int dt, int first, int segs, int i0, int i1) {
@@ -189,7 +177,7 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
       for (int s = 0; s < segs; ++s) v += __ldcg(a.down_part + ((int64_t)(first + s) * 2 + (s > 0 ? 0 : 1)) * dslot + i);
       if (col < a.d) {
         const int64_t o = (int64_t)t * a.d + col;
-        y[o] = from_f32<T>(res ? v + to_f32(res[o]) : v);
+        y[o] = res ? v + res[o] : v;
       }
     }
   };
@@ -209,7 +197,7 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
       const int e = R.act[ai], n = R.cnt[e], base = R.base[e];
       const int k0 = kb0 * SM_KR, k1 = kb1 * SM_KR < a.f ? kb1 * SM_KR : a.f;
       for (int m0 = 0; m0 < n; m0 += SM_TOK)
-        thin_product(S, static_cast<const T*>(a.io.W2) + (int64_t)e * a.f * a.d, a.d, d0, k0, k1,
+        thin_product(S, static_cast<const float*>(a.io.W2) + (int64_t)e * a.f * a.d, a.d, d0, k0, k1,
                      n - m0 < SM_TOK ? n - m0 : SM_TOK,
                      [&](int m, int k) { return __ldcg(h + (int64_t)(base + m0 + m) * a.f + k); },
                      [&](int m, int col, float v) { S.yacc[R.tok[base + m0 + m]][col] += v; });
@@ -259,21 +247,20 @@ DecodeWs decode_ws(const Shape& s) {
   return w;
 }
 
-template <typename T>
 cudaError_t launch_simt(DecodeArgs a, int G, cudaStream_t st) {
   static bool attr_done[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
   if (!attr_done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)sizeof(SimtSmem));
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
   void* args[] = {&a};
   LaunchScope ls(KK_DECODE, st);
-  return cudaLaunchCooperativeKernel((const void*)decode_kernel<T>, dim3(G), dim3(SM_NT), args, sizeof(SimtSmem), st);
+  return cudaLaunchCooperativeKernel((const void*)decode_kernel, dim3(G), dim3(SM_NT), args, sizeof(SimtSmem), st);
 }
 
 }  // namespace
@@ -303,7 +290,7 @@ cudaError_t launch_decode(const Shape& s, const DecodeIo& io, void* ws, uint32_t
   a.slices = G / a.groups;
   const int most = (s.d + 31) / 32;
   if (a.slices > most) a.slices = most;
-  return s.bf16 ? launch_simt<__nv_bfloat16>(a, G, st) : launch_simt<float>(a, G, st);
+  return s.bf16 ? launch_decode_tc(s, a, G, st) : launch_simt(a, G, st);
 }
 
 }  // namespace moe

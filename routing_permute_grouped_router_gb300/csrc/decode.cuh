@@ -12,6 +12,21 @@
 #include "common.cuh"
 
 namespace moe {
+
+struct DecodeArgs {
+  DecodeIo io;
+  float* score_part;  // [groups][slices][DEC_TG][E] partial logits
+  uint32_t* ctr;      // [2 G + 1]: arrivals at the split tiles of the up and the down product, and of the whole grid
+  void* h;            // rows of the experts, gate * silu(a) * b: [T k][f] fp32, or [T k][hi f | lo f] bf16
+  float* up_part;     // [G][2][T][2 * DEC_N] a and b of a split tile
+  float* down_part;   // [G][2][T][DEC_N]
+  uint32_t* err;
+  int T, d, f, E, k, cap;
+  int groups, slices;  // of the scores: groups of DEC_TG tokens, slices of d
+};
+// decode_tc.cu: bf16 layers, G CTAs
+cudaError_t launch_decode_tc(const Shape& s, const DecodeArgs& args, int G, cudaStream_t st);
+
 namespace {
 
 constexpr int DEC_T = 64;          // most tokens (MOE_DECODE_MAX_T)
@@ -22,20 +37,8 @@ constexpr int DEC_N = 128;         // output columns of a weight tile
 constexpr int DEC_TG = 8;          // tokens scored together
 constexpr uint64_t DEC_WAIT_NS = 2000000000ull;  // a wait for another CTA gives up after 2 s
 
-struct DecodeArgs {
-  DecodeIo io;
-  float* score_part;  // [groups][slices][DEC_TG][E] partial logits
-  uint32_t* ctr;      // [2 G + 1]: arrivals at the split tiles of the up and the down product, and of the whole grid
-  void* h;            // rows of the experts: gate * silu(a) * b
-  float* up_part;     // [G][2][T][2 * DEC_N] a and b of a split tile
-  float* down_part;   // [G][2][T][DEC_N]
-  uint32_t* err;
-  int T, d, f, E, k, cap;
-  int groups, slices;  // of the scores: groups of DEC_TG tokens, slices of d
-};
-
 // What a CTA knows of the routing: every CTA derives the same.
-struct Routing {
+struct alignas(16) Routing {
   int ids[DEC_ROWS];     // [T, k]
   float gates[DEC_ROWS];  // [T, k]
   int slot[DEC_ROWS];    // in visiting order: choice-major, then token
