@@ -103,10 +103,10 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
 
   // ---- up product ----
   const int64_t pslot = (int64_t)a.T * 2 * DEC_N;
-  const Split up((int64_t)R.nact * FT * KU, G);
+  const Split up(R.nact * FT * KU, G);
   // h of the sums i0..i1 of a tile (row, column) from the parts of its `segs` CTAs
-  auto finish_up = [&](int64_t tile, int first, int segs, int i0, int i1) {
-    const int f0 = (int)(tile % FT) * DEC_N, base = R.base[R.act[tile / FT]];
+  auto finish_up = [&](int tile, int first, int segs, int i0, int i1) {
+    const int f0 = tile % FT * DEC_N, base = R.base[R.act[tile / FT]];
     for (int i = i0 + tid; i < i1; i += SM_NT) {
       const int m = i / DEC_N, col = i % DEC_N;
       float va = 0.f, vb = 0.f;
@@ -118,12 +118,12 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
       if (f0 + col < a.f) h[(int64_t)(base + m) * a.f + f0 + col] = R.gate[base + m] * dec_silu(va) * vb;
     }
   };
-  if (up.U > 0) {
-    const int64_t u0 = up.begin(c), u1 = up.begin(c + 1);
-    for (int64_t u = u0; u < u1;) {
-      const int64_t tile = u / KU;
-      const int kb0 = (int)(u - tile * KU), kb1 = (int)(u1 - tile * KU < KU ? u1 - tile * KU : KU);
-      const int e = R.act[tile / FT], f0 = (int)(tile % FT) * DEC_N, n = R.cnt[e], base = R.base[e];
+  if (R.nact > 0) {
+    const int u0 = up.begin(c), u1 = up.begin(c + 1);
+    for (int u = u0; u < u1;) {
+      const int tile = u / KU;
+      const int kb0 = u - tile * KU, kb1 = u1 - tile * KU < KU ? u1 - tile * KU : KU;
+      const int e = R.act[tile / FT], f0 = tile % FT * DEC_N, n = R.cnt[e], base = R.base[e];
       const int k0 = kb0 * SM_KR, k1 = kb1 * SM_KR < a.d ? kb1 * SM_KR : a.d;
       float* part = a.up_part + ((int64_t)c * 2 + (kb0 > 0 ? 0 : 1)) * pslot;
       const float* W[2] = {static_cast<const float*>(a.io.W1) + (int64_t)e * a.d * a.f,
@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
       u += kb1 - kb0;
     }
     // a share of each tile that other CTAs have a part of
-    for (int64_t u = u0; u < u1;) {
-      const int64_t tile = u / KU, end = (tile + 1) * KU;
+    for (int u = u0; u < u1;) {
+      const int tile = u / KU, end = (tile + 1) * KU;
       const int first = up.owner(tile * KU), segs = up.owner(end - 1) - first + 1;
       if (segs > 1) {
         __syncthreads();
@@ -161,11 +161,11 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
 
   // ---- down product ----
   const int64_t dslot = (int64_t)a.T * DEC_N;
-  const int64_t per = (int64_t)R.nact * KD;  // units of a column tile: all experts' rows of W2
+  const int per = R.nact * KD;  // units of a column tile: all experts' rows of W2
   const Split down(per * DT, G);
   const float* res = static_cast<const float*>(a.io.residual);
   float* y = static_cast<float*>(a.io.y);
-  if (down.U == 0) {  // every assignment was dropped
+  if (R.nact == 0) {  // every assignment was dropped
     for (int64_t i = (int64_t)c * SM_NT + tid; i < (int64_t)a.T * a.d; i += (int64_t)G * SM_NT)
       y[i] = res ? res[i] : 0.f;
     return;
@@ -174,26 +174,25 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
     for (int i = i0 + tid; i < i1; i += SM_NT) {
       const int t = i / DEC_N, col = dt * DEC_N + i % DEC_N;
       float v = 0.f;
-      for (int s = 0; s < segs; ++s) v += __ldcg(a.down_part + ((int64_t)(first + s) * 2 + (s > 0 ? 0 : 1)) * dslot + i);
+      for (int s = 0; s < segs; ++s) v += __ldcg(a.down_part + (int64_t)(first + s + dt) * dslot + i);
       if (col < a.d) {
         const int64_t o = (int64_t)t * a.d + col;
         y[o] = res ? v + res[o] : v;
       }
     }
   };
-  const int64_t u0 = down.begin(c), u1 = down.begin(c + 1);
-  for (int64_t u = u0; u < u1;) {
-    const int64_t dt = u / per, end = (dt + 1) * per < u1 ? (dt + 1) * per : u1;
-    const int d0 = (int)dt * DEC_N;
+  const int u0 = down.begin(c), u1 = down.begin(c + 1);
+  for (int u = u0; u < u1;) {
+    const int dt = u / per, end = (dt + 1) * per < u1 ? (dt + 1) * per : u1;
+    const int d0 = dt * DEC_N;
     __syncthreads();
     for (int i = tid; i < a.T * DEC_N; i += SM_NT) (&S.yacc[0][0])[i] = 0.f;
     __syncthreads();
-    float* part = a.down_part + ((int64_t)c * 2 + (u > dt * per ? 0 : 1)) * dslot;
+    float* part = a.down_part + (c + dt) * dslot;
     const bool whole = u == dt * per && end == (dt + 1) * per;
     while (u < end) {
-      const int64_t q = u - dt * per;
-      const int ai = (int)(q / KD), kb0 = (int)(q - (int64_t)ai * KD);
-      const int kb1 = end - u < KD - kb0 ? kb0 + (int)(end - u) : KD;
+      const int q = u - dt * per, ai = q / KD, kb0 = q - ai * KD;
+      const int kb1 = end - u < KD - kb0 ? kb0 + end - u : KD;
       const int e = R.act[ai], n = R.cnt[e], base = R.base[e];
       const int k0 = kb0 * SM_KR, k1 = kb1 * SM_KR < a.f ? kb1 * SM_KR : a.f;
       for (int m0 = 0; m0 < n; m0 += SM_TOK)
@@ -211,18 +210,18 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
       if (tid == 0) red_release(a.ctr + G + down.owner(dt * per));
     } else {
       __syncthreads();
-      finish_down((int)dt, c, 1, 0, a.T * DEC_N);
+      finish_down(dt, c, 1, 0, a.T * DEC_N);
     }
   }
-  for (int64_t u = u0; u < u1;) {
-    const int64_t dt = u / per, end = (dt + 1) * per;
+  for (int u = u0; u < u1;) {
+    const int dt = u / per, end = (dt + 1) * per;
     const int first = down.owner(dt * per), segs = down.owner(end - 1) - first + 1;
     if (segs > 1) {
       __syncthreads();
       if (tid == 0) wait_count(a.ctr + G + first, segs, a.err, 701);
       __syncthreads();
       const int N = a.T * DEC_N;
-      finish_down((int)dt, first, segs, (int)((int64_t)(c - first) * N / segs),
+      finish_down(dt, first, segs, (int)((int64_t)(c - first) * N / segs),
                   (int)((int64_t)(c - first + 1) * N / segs));
     }
     u = end < u1 ? end : u1;
@@ -233,17 +232,19 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct DecodeWs {
-  size_t score, ctr, h, up, down, total;
+  size_t score, ids, gates, ctr, h, up, down, total;
 };
 DecodeWs decode_ws(const Shape& s) {
-  const size_t G = sm_count(), T = s.T;
+  const size_t G = sm_count(), T = s.T, DT = (s.d + DEC_N - 1) / DEC_N;
   DecodeWs w{};
   w.score = 0;
-  w.ctr = w.score + up256(G * DEC_TG * s.E * 4);
-  w.h = w.ctr + up256((2 * G + 1) * 4);
+  w.ids = w.score + up256(G * DEC_TG * s.E * 4);
+  w.gates = w.ids + up256(T * s.k * 4);
+  w.ctr = w.gates + up256(T * s.k * 4);
+  w.h = w.ctr + up256((2 * G + 3) * 4);
   w.up = w.h + up256(T * s.k * s.f * 4);
-  w.down = w.up + up256(G * 2 * T * 2 * DEC_N * 4);
-  w.total = w.down + up256(G * 2 * T * DEC_N * 4);
+  w.down = w.up + up256(2 * G * 2 * T * 2 * DEC_N * 4);
+  w.total = w.down + up256(2 * (G + DT) * T * DEC_N * 4);
   return w;
 }
 
@@ -274,6 +275,8 @@ cudaError_t launch_decode(const Shape& s, const DecodeIo& io, void* ws, uint32_t
   DecodeArgs a{};
   a.io = io;
   a.score_part = reinterpret_cast<float*>(base + w.score);
+  a.ids = reinterpret_cast<int32_t*>(base + w.ids);
+  a.gates = reinterpret_cast<float*>(base + w.gates);
   a.ctr = reinterpret_cast<uint32_t*>(base + w.ctr);
   a.h = base + w.h;
   a.up_part = reinterpret_cast<float*>(base + w.up);
@@ -286,10 +289,10 @@ cudaError_t launch_decode(const Shape& s, const DecodeIo& io, void* ws, uint32_t
   a.k = s.k;
   a.cap = s.cap;
   a.groups = (s.T + DEC_TG - 1) / DEC_TG;
-  // slices of at least 32 rows of d
-  a.slices = G / a.groups;
-  const int most = (s.d + 31) / 32;
-  if (a.slices > most) a.slices = most;
+  // slices of one batch of W_r loads (eight a thread), of at least 32 rows, and no more of them than CTAs
+  const int rows = 2048 / s.E < 32 ? 32 : (2048 / s.E > 256 ? 256 : 2048 / s.E);
+  a.slices = (s.d + rows - 1) / rows;
+  if (a.slices > G / a.groups) a.slices = G / a.groups;
   return s.bf16 ? launch_decode_tc(s, a, G, st) : launch_simt(a, G, st);
 }
 

@@ -16,10 +16,12 @@ namespace moe {
 struct DecodeArgs {
   DecodeIo io;
   float* score_part;  // [groups][slices][DEC_TG][E] partial logits
-  uint32_t* ctr;      // [2 G + 1]: arrivals at the split tiles of the up and the down product, and of the whole grid
+  int32_t* ids;       // [T, k] picks and their gates, from the CTA that made them to the others
+  float* gates;
+  uint32_t* ctr;      // [2 G + 3]: arrivals at split tiles and grid barriers
   void* h;            // rows of the experts, gate * silu(a) * b: [T k][f] fp32, or [T k][hi f | lo f] bf16
-  float* up_part;     // [G][2][T][2 * DEC_N] a and b of a split tile
-  float* down_part;   // [G][2][T][DEC_N]
+  float* up_part;     // [2][G][2][T][2 * DEC_N] a and b of split tiles
+  float* down_part;   // [2][G + column tiles][T][DEC_N] sums of the CTAs over their part of a column tile
   uint32_t* err;
   int T, d, f, E, k, cap;
   int groups, slices;  // of the scores: groups of DEC_TG tokens, slices of d
@@ -39,14 +41,14 @@ constexpr uint64_t DEC_WAIT_NS = 2000000000ull;  // a wait for another CTA gives
 
 // What a CTA knows of the routing: every CTA derives the same.
 struct alignas(16) Routing {
-  int ids[DEC_ROWS];     // [T, k]
   float gates[DEC_ROWS];  // [T, k]
-  int slot[DEC_ROWS];    // in visiting order: choice-major, then token
-  int cnt[DEC_E];        // kept rows of each expert
-  int base[DEC_E];       // first row of each expert
-  int act[DEC_E];        // experts with rows
-  int tok[DEC_ROWS];     // token of each row
-  float gate[DEC_ROWS];  // gate of each row
+  float gate[DEC_ROWS];   // gate of each row
+  int16_t slot[DEC_ROWS];  // in visiting order: choice-major, then token
+  uint8_t ids[DEC_ROWS];   // [T, k]
+  uint8_t tok[DEC_ROWS];   // token of each row
+  int cnt[DEC_E];          // kept rows of each expert
+  int16_t base[DEC_E];     // first row of each expert
+  uint8_t act[DEC_E];      // experts with rows
   int nact;
 };
 
@@ -77,134 +79,175 @@ __device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t want, uin
 }
 
 // ---- the split of the weights ----
-// U equal units in order; the first G CTAs (all, or one a unit where there are
-// fewer units) take [c U / G, (c + 1) U / G), the others nothing.  A tile of
-// several units can begin in one CTA and end in another, so every CTA streams
-// the same bytes to within a unit whatever the number of tiles.
+// U equal units in order: the first U % G CTAs take one more than the others,
+// so with fewer units than CTAs the last ones take none.  A tile of several
+// units can begin in one CTA and end in another, so every CTA streams the same
+// bytes to within a unit whatever the number of tiles.  U < 2^26 by the limits
+// on d, f and E.
 struct Split {
-  int64_t U;
-  int G;
-  __device__ __forceinline__ Split(int64_t units, int ctas) : U(units), G((int)(units < ctas ? units : ctas)) {}
-  __device__ __forceinline__ int64_t begin(int c) const { return c < G ? c * U / G : U; }
-  __device__ __forceinline__ int owner(int64_t u) const { return (int)(((u + 1) * G + U - 1) / U) - 1; }
+  int base, more;
+  __device__ __forceinline__ Split(int U, int G) : base(U / G), more(U % G) {}
+  __device__ __forceinline__ int begin(int c) const { return c * base + (c < more ? c : more); }
+  __device__ __forceinline__ int owner(int u) const {
+    const int big = more * (base + 1);
+    return u < big ? u / (base + 1) : more + (u - big) / base;
+  }
 };
 
 // ---- scores ----
-// Partial logits of DEC_TG tokens over one slice of d: W_r's rows are read
-// once a group, the sum runs in a fixed order.
+// The kernel runs once through most of its code, and every 128-byte line of
+// it that is not yet in an SM's instruction cache costs an L2 or DRAM latency:
+// the loops from here on are kept rolled and the bodies short (the unrolled
+// forms of the score, pick and epilogue loops cost a one-token step 20 us).
 struct ScoreScratch {
-  float x[256][DEC_TG];
+  float w[4096];            // rows of W_r
+  float x[256 * DEC_TG];    // the same columns of the tokens
   float red[256 * DEC_TG];
 };
+__device__ __forceinline__ int pow2_at_least(int e) { return e <= 1 ? 1 : 1 << (32 - __clz(e - 1)); }
+
+// Partial logits of DEC_TG tokens over one slice of d, so W_r is read once a
+// group.  256 threads take `subs` rows at a time; the sums run in a fixed order.
 template <typename T, int NT>
 __device__ __forceinline__ void score_slice(const DecodeArgs& a, ScoreScratch& s) {
   const int unit = blockIdx.x;
   if (unit >= a.groups * a.slices) return;
-  const int grp = unit / a.slices, sl = unit % a.slices, t0 = grp * DEC_TG;
+  const int grp = unit / a.slices, sl = unit - grp * a.slices, t0 = grp * DEC_TG;
   const int r0 = (int)((int64_t)sl * a.d / a.slices), r1 = (int)((int64_t)(sl + 1) * a.d / a.slices);
-  const T* x = static_cast<const T*>(a.io.x);
-  int ep = 1;
-  while (ep < a.E) ep *= 2;
-  const int subs = 256 / ep, e = threadIdx.x % ep, sub = threadIdx.x / ep;  // sub rows at a time
+  const int ep = pow2_at_least(a.E), subs = 256 / ep;
+  const int e = threadIdx.x & (ep - 1), sub = threadIdx.x / ep, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const bool on = threadIdx.x < 256 && e < a.E;
+  const int most = 4096 / a.E < 256 ? 4096 / a.E : 256;
   float acc[DEC_TG];
 #pragma unroll
   for (int t = 0; t < DEC_TG; ++t) acc[t] = 0.f;
-  for (int c0 = r0; c0 < r1; c0 += 256) {
-    const int n = r1 - c0 < 256 ? r1 - c0 : 256;
+#pragma unroll 1
+  for (int c0 = r0; c0 < r1; c0 += most) {
+    const int n = r1 - c0 < most ? r1 - c0 : most;
     __syncthreads();
-    for (int i = threadIdx.x; i < n * DEC_TG; i += NT) {
-      const int t = i / n, r = i % n;
-      s.x[r][t] = t0 + t < a.T ? to_f32(x[(int64_t)(t0 + t) * a.d + c0 + r]) : 0.f;
+    const float* W = a.io.W_r + (int64_t)c0 * a.E;
+    const T* x = static_cast<const T*>(a.io.x) + (int64_t)(t0 + warp) * a.d + c0;
+    const bool live = warp < DEC_TG && t0 + warp < a.T;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n * a.E; i += NT) s.w[i] = __ldg(W + i);
+    if (warp < DEC_TG) {
+#pragma unroll 4
+      for (int r = lane; r < n; r += 32) s.x[r * DEC_TG + warp] = live ? to_f32(x[r]) : 0.f;
     }
     __syncthreads();
     if (on) {
-#pragma unroll 8
+#pragma unroll 2
       for (int r = sub; r < n; r += subs) {
-        const float w = __ldg(a.io.W_r + (int64_t)(c0 + r) * a.E + e);
-#pragma unroll
-        for (int t = 0; t < DEC_TG; ++t) acc[t] = fmaf(s.x[r][t], w, acc[t]);
+        const float w = s.w[r * a.E + e];
+        const float4 p = *reinterpret_cast<const float4*>(s.x + r * DEC_TG);
+        const float4 q = *reinterpret_cast<const float4*>(s.x + r * DEC_TG + 4);
+        acc[0] = fmaf(p.x, w, acc[0]);
+        acc[1] = fmaf(p.y, w, acc[1]);
+        acc[2] = fmaf(p.z, w, acc[2]);
+        acc[3] = fmaf(p.w, w, acc[3]);
+        acc[4] = fmaf(q.x, w, acc[4]);
+        acc[5] = fmaf(q.y, w, acc[5]);
+        acc[6] = fmaf(q.z, w, acc[6]);
+        acc[7] = fmaf(q.w, w, acc[7]);
       }
     }
   }
   if (on) {
 #pragma unroll
-    for (int t = 0; t < DEC_TG; ++t) s.red[(sub * DEC_TG + t) * ep + e] = acc[t];
+    for (int t = 0; t < DEC_TG; ++t) s.red[(t * subs + sub) * ep + e] = acc[t];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < DEC_TG * a.E; i += NT) {
-    const int t = i / a.E, ee = i % a.E;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < DEC_TG * ep; i += NT) {
+    const int t = i / ep, ee = i & (ep - 1);
+    if (ee >= a.E || t0 + t >= a.T) continue;
     float v = 0.f;
-    for (int q = 0; q < subs; ++q) v += s.red[(q * DEC_TG + t) * ep + ee];
-    a.score_part[(int64_t)unit * DEC_TG * a.E + i] = v;
+#pragma unroll 4
+    for (int q = 0; q < subs; ++q) v += s.red[(t * subs + q) * ep + ee];
+    a.score_part[((int64_t)unit * DEC_TG + t) * a.E + ee] = v;
   }
 }
 
-// Softmax and top-k of every token (a warp a token), as router_topk_kernel
-// does them: NaN scores count as -inf, ties go to the lower expert.
-template <int NT>
-__device__ __forceinline__ void pick_experts(const DecodeArgs& a, Routing& R) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  for (int t = warp; t < a.T; t += NT / 32) {
-    const float* part = a.score_part + ((int64_t)(t / DEC_TG) * a.slices * DEC_TG + t % DEC_TG) * a.E;
-    float v[DEC_E / 32];
-    float mx = -INFINITY;
+// Logits of `n` <= DEC_TG tokens of one group from token t0 on, added over the
+// slices; token t0 + i is then picked for by warp i, as router_topk_kernel
+// does it: NaN scores count as -inf, ties go to the lower expert.  put(t, j,
+// expert, gate) is called once for each pick.
+template <int NT, typename Put>
+__device__ __forceinline__ void pick_experts(const DecodeArgs& a, ScoreScratch& s, int t0, int n, Put put) {
+  const int ep = pow2_at_least(a.E), np = pow2_at_least(n), warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int pairs = np * ep, subs = pairs < 256 ? 256 / pairs : 1;  // threads that share a sum
+  const float* part = a.score_part + ((int64_t)(t0 / DEC_TG) * a.slices * DEC_TG + t0 % DEC_TG) * a.E;
+  const int step = DEC_TG * a.E;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < pairs * subs; i += NT) {
+    const int e = i & (ep - 1), t = (i / ep) & (np - 1), sub = i / pairs;
+    float v = 0.f;
+    if (e < a.E && t < n) {
+#pragma unroll 8
+      for (int q = sub; q < a.slices; q += subs) v += __ldcg(part + q * step + t * a.E + e);
+    }
+    s.red[(t * subs + sub) * ep + e] = v;
+  }
+  __syncthreads();
+  if (warp >= n) return;
+  float* lg = s.x + warp * DEC_E;  // the token's logits
+  float v[DEC_E / 32];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < DEC_E / 32; ++c) {
+    const int e = lane + 32 * c;
+    float sc = -INFINITY;
+    if (e < a.E) {
+      sc = a.io.bias ? __ldg(a.io.bias + e) : 0.f;
+#pragma unroll 1
+      for (int q = 0; q < subs; ++q) sc += s.red[(warp * subs + q) * ep + e];
+      if (isnan(sc)) sc = -INFINITY;
+    }
+    lg[e] = v[c] = sc;
+    mx = fmaxf(mx, sc);
+  }
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  uint32_t taken = 0;
+  float mine = -INFINITY;  // lane j keeps the j-th pick and its logit
+  int pick = 0;
+#pragma unroll 1
+  for (int j = 0; j < a.k; ++j) {
+    float bv = -INFINITY;
+    int be = 0x7fffffff;
 #pragma unroll
     for (int c = 0; c < DEC_E / 32; ++c) {
       const int e = lane + 32 * c;
-      float s = -INFINITY;
-      if (e < a.E) {
-        s = 0.f;
-#pragma unroll 8
-        for (int q = 0; q < a.slices; ++q) s += __ldcg(part + (int64_t)q * DEC_TG * a.E + e);
-        if (a.io.bias) s += __ldg(a.io.bias + e);
-        if (isnan(s)) s = -INFINITY;
-      }
-      v[c] = s;
-      mx = fmaxf(mx, s);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    uint32_t taken = 0;
-    float first = 0.f, den = 0.f, mine = 0.f;  // lane j keeps the j-th pick's exponential
-    for (int j = 0; j < a.k; ++j) {
-      float bv = -INFINITY;
-      int be = 0x7fffffff;
-#pragma unroll
-      for (int c = 0; c < DEC_E / 32; ++c) {
-        const int e = lane + 32 * c;
-        if (e < a.E && !((taken >> c) & 1u) && (v[c] > bv || (v[c] == bv && e < be))) {
-          bv = v[c];
-          be = e;
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-        const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-        if (ov > bv || (ov == bv && oe < be)) {
-          bv = ov;
-          be = oe;
-        }
-      }
-      if ((be & 31) == lane) taken |= 1u << (be >> 5);
-      if (j == 0) first = bv;
-      const float ex = a.k == 1 ? expf(bv - mx) : expf(bv - first);
-      den += ex;
-      if (lane == j) {
-        mine = ex;
-        R.ids[t * a.k + j] = be;
+      if (e < a.E && !((taken >> c) & 1u) && (v[c] > bv || (v[c] == bv && e < be))) {
+        bv = v[c];
+        be = e;
       }
     }
-    if (a.k == 1) {  // one pick: its probability over all experts
-      den = 0.f;
-#pragma unroll
-      for (int c = 0; c < DEC_E / 32; ++c)
-        if (lane + 32 * c < a.E) den += expf(v[c] - mx);
-      den = warp_sum(den);
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) {
+      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
+      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
+      if (ov > bv || (ov == bv && oe < be)) {
+        bv = ov;
+        be = oe;
+      }
     }
-    if (lane < a.k) R.gates[t * a.k + lane] = mine / den;
+    if ((be & 31) == lane) taken |= 1u << (be >> 5);
+    if (lane == j) {
+      mine = bv;
+      pick = be;
+    }
   }
+  // one pick: its probability over all experts; several: over the picks
+  float ex = lane < a.k ? expf(mine - mx) : 0.f, den = ex;
+  if (a.k == 1) {
+    den = 0.f;
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 32) den += expf(lg[e] - mx);
+  }
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  if (lane < a.k) put(t0 + warp, lane, pick, ex / den);
 }
 
 // Row lists of the experts: assignments are visited choice-major and then in
@@ -213,49 +256,52 @@ __device__ __forceinline__ void pick_experts(const DecodeArgs& a, Routing& R) {
 template <int NT>
 __device__ __forceinline__ void list_rows(const DecodeArgs& a, Routing& R) {
   const int Tk = a.T * a.k, lane = threadIdx.x % 32;
-  for (int e = threadIdx.x; e < DEC_E; e += NT) R.cnt[e] = 0;
-  __syncthreads();
   if (threadIdx.x < 32) {
+    reinterpret_cast<int4*>(R.cnt)[lane] = make_int4(0, 0, 0, 0);
+    __syncwarp();
+#pragma unroll 1
     for (int i0 = 0; i0 < Tk; i0 += 32) {
       const int i = i0 + lane;
       const bool on = i < Tk;
-      const int e = on ? R.ids[(i % a.T) * a.k + i / a.T] : -1;
+      const int j = i / a.T, e = on ? R.ids[(i - j * a.T) * a.k + j] : -1;
       const uint32_t same = __match_any_sync(0xffffffffu, e);
       const int rank = __popc(same & ((1u << lane) - 1u));
       const int before = on ? R.cnt[e] : 0;
-      if (on) R.slot[i] = before + rank;
+      if (on) R.slot[i] = (int16_t)(before + rank);
       __syncwarp();
       if (on && rank == 0) R.cnt[e] = before + __popc(same);
       __syncwarp();
     }
-    // kept rows, their first rows and the experts that have any
-    int rows = 0, nact = 0;
+    // kept rows, their first rows and the experts that have any: four experts a lane
+    const int4 c4 = reinterpret_cast<const int4*>(R.cnt)[lane];
+    const int c[4] = {min(c4.x, a.cap), min(c4.y, a.cap), min(c4.z, a.cap), min(c4.w, a.cap)};
+    reinterpret_cast<int4*>(R.cnt)[lane] = make_int4(c[0], c[1], c[2], c[3]);
+    int own = 0;  // rows, and experts in the upper half
 #pragma unroll
-    for (int c = 0; c < DEC_E / 32; ++c) {
-      const int e = c * 32 + lane;
-      int n = R.cnt[e];
-      n = n < a.cap ? n : a.cap;
-      int pre = n;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const int u = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += u;
-      }
-      const uint32_t live = __ballot_sync(0xffffffffu, n > 0);
-      R.cnt[e] = n;
-      R.base[e] = rows + pre - n;
-      if (n > 0) R.act[nact + __popc(live & ((1u << lane) - 1u))] = e;
-      rows += __shfl_sync(0xffffffffu, pre, 31);
-      nact += __popc(live);
+    for (int q = 0; q < 4; ++q) own += c[q] + (c[q] > 0 ? 1 << 16 : 0);
+    int pre = own;
+#pragma unroll 1
+    for (int o = 1; o < 32; o *= 2) {
+      const int u = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += u;
     }
-    if (lane == 0) R.nact = nact;
+    if (lane == 31) R.nact = pre >> 16;
+    pre -= own;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      R.base[lane * 4 + q] = (int16_t)(pre & 0xffff);
+      if (c[q] > 0) {
+        R.act[pre >> 16] = (uint8_t)(lane * 4 + q);
+        pre += c[q] + (1 << 16);
+      }
+    }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < Tk; i += NT) {
-    const int t = i % a.T, j = i / a.T, e = R.ids[t * a.k + j];
+    const int j = i / a.T, t = i - j * a.T, e = R.ids[t * a.k + j];
     if (R.slot[i] < R.cnt[e]) {
       const int row = R.base[e] + R.slot[i];
-      R.tok[row] = t;
+      R.tok[row] = (uint8_t)t;
       R.gate[row] = R.gates[t * a.k + j];
     }
   }
@@ -268,15 +314,36 @@ __device__ __forceinline__ void list_rows(const DecodeArgs& a, Routing& R) {
   __syncthreads();
 }
 
-// Scores, picks and row lists; every thread of every CTA takes part.
+// Scores, picks and row lists; every thread of every CTA takes part.  Up to
+// DEC_TG tokens every CTA adds the slices and picks for itself; for more, one
+// CTA a token does, and a second grid barrier hands the picks to the others.
 template <typename T, int NT>
 __device__ __forceinline__ void route(const DecodeArgs& a, ScoreScratch& s, Routing& R) {
   if (blockIdx.x == gridDim.x - 1)
-    for (int i = threadIdx.x; i < 2 * (int)gridDim.x + 1; i += NT) a.ctr[i] = 0;
+    for (int i = threadIdx.x; i < 2 * (int)gridDim.x + 3; i += NT) a.ctr[i] = 0;
   score_slice<T, NT>(a, s);
   cooperative_groups::this_grid().sync();
-  pick_experts<NT>(a, R);
-  __syncthreads();
+  if (a.T <= DEC_TG) {
+    pick_experts<NT>(a, s, 0, a.T, [&](int t, int j, int e, float g) {
+      R.ids[t * a.k + j] = (uint8_t)e;
+      R.gates[t * a.k + j] = g;
+    });
+    __syncthreads();
+  } else {
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+      __syncthreads();
+      pick_experts<NT>(a, s, t, 1, [&](int tt, int j, int e, float g) {
+        a.ids[tt * a.k + j] = e;
+        a.gates[tt * a.k + j] = g;
+      });
+    }
+    cooperative_groups::this_grid().sync();
+    for (int i = threadIdx.x; i < a.T * a.k; i += NT) {
+      R.ids[i] = (uint8_t)__ldcg(a.ids + i);
+      R.gates[i] = __ldcg(a.gates + i);
+    }
+    __syncthreads();
+  }
   list_rows<NT>(a, R);
 }
 

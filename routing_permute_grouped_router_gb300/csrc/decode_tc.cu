@@ -9,12 +9,14 @@
 // to an SM, so the kernel is a stream of TMA loads with everything else behind:
 //   warp 0, one lane: TMA producer.  A stage of the up product is 64 rows of d
 //     of a W1 and a W3 tile and the same columns of all tokens; one of the down
-//     product 64 rows of f of a W2 tile and those columns of the expert's rows
-//     of h.  It fills the ring with the first W2 tiles before it waits for the
-//     other CTAs' h, so HBM is busy across the grid barrier.
+//     product 64 or 128 rows of f of a W2 tile and those columns of the
+//     expert's rows of h.
 //   warp 1, one lane: MMAs.  Two accumulators in turn, so the next segment's
 //     products run under a segment's epilogue.
 //   warps 4-7: epilogue, one weight column a thread.
+// Both products are done in two halves of f, in the order up 0, up 1, down 0,
+// down 1: the exchange of the partial sums of one half and the grid barrier
+// behind its h (some 5 us) run under the stream of the next part's weights.
 // h is split into two bf16 parts, hi + lo, whose products go to the same
 // accumulator: 16 significant bits where one bf16 would round h to 8 and
 // double the error of y.  The second product is free here.
@@ -38,7 +40,6 @@ struct alignas(16) TcCtrl {
   uint64_t full[TC_MAX_ST], empty[TC_MAX_ST], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
-  int8_t row_of[4][DEC_T];  // a warp's map from token to the row of the segment's expert
 };
 
 struct TcMapsD {
@@ -70,39 +71,97 @@ struct Seg {
   int e, n, base;  // expert, its rows, the first of them
   int c0;          // first weight column
   int kb0, kb1;    // units
-  int64_t tile;    // up: the weight tile; down: the column tile of y
+  int tile;        // up: the weight tile; down: the column tile of y
 };
-__device__ __forceinline__ Seg up_seg(const Routing& R, int64_t u, int64_t u1, int FT, int KU) {
+// half: 0 or 1, FT and KD are those of a half
+__device__ __forceinline__ Seg up_seg(const Routing& R, int u, int u1, int half, int FT, int KU) {
   Seg s;
   s.tile = u / KU;
-  s.kb0 = (int)(u - s.tile * KU);
-  s.kb1 = (int)(u1 - s.tile * KU < KU ? u1 - s.tile * KU : KU);
-  s.e = R.act[s.tile / FT];
-  s.c0 = (int)(s.tile % FT) * DEC_N;
+  s.kb0 = u - s.tile * KU;
+  s.kb1 = u1 - s.tile * KU < KU ? u1 - s.tile * KU : KU;
+  const int ai = s.tile / FT;
+  s.e = R.act[ai];
+  s.c0 = (half * FT + s.tile - ai * FT) * DEC_N;
   s.n = R.cnt[s.e];
   s.base = R.base[s.e];
   return s;
 }
-__device__ __forceinline__ Seg down_seg(const Routing& R, int64_t u, int64_t u1, int64_t per, int KD) {
+__device__ __forceinline__ Seg down_seg(const Routing& R, int u, int u1, int half, int per, int KD) {
   Seg s;
   s.tile = u / per;
-  const int64_t q = u - s.tile * per;
-  const int ai = (int)(q / KD);
-  s.kb0 = (int)(q - (int64_t)ai * KD);
-  s.kb1 = u1 - u < KD - s.kb0 ? s.kb0 + (int)(u1 - u) : KD;
+  const int q = u - s.tile * per, ai = q / KD;
+  s.kb0 = q - ai * KD;
+  s.kb1 = u1 - u < KD - s.kb0 ? s.kb0 + u1 - u : KD;
+  s.kb0 += half * KD;
+  s.kb1 += half * KD;
   s.e = R.act[ai];
-  s.c0 = (int)s.tile * DEC_N;
+  s.c0 = s.tile * DEC_N;
   s.n = R.cnt[s.e];
   s.base = R.base[s.e];
   return s;
 }
+// a load of weights: they pass through L2 once, so they leave it before anything else does (code, tokens, partial sums)
+__device__ __forceinline__ void tma_load_once(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
+                                              uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
+// units of a stage of the down product: two where the rows are few enough for both to fit
+__device__ __forceinline__ int down_units(const Seg& s, int kb) { return s.n <= 16 && kb + 1 < s.kb1 ? 2 : 1; }
 
+// a and b of one token, four consecutive rows of y
+__device__ __forceinline__ float2 tmem_ld_ab(uint32_t at) {
+  float2 v;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%2];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%1}, [%3];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&f"(v.x), "=&f"(v.y)
+      : "r"(at), "r"(at + TC_B)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 tmem_ld4(uint32_t at) {
+  float4 v;
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w)
+      : "r"(at)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ void add4(float4& v, const float4& w) {
+  v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+}
+__device__ __forceinline__ void xor4(float4& v, int o) {
+  add4(v, make_float4(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o),
+                      __shfl_xor_sync(0xffffffffu, v.z, o), __shfl_xor_sync(0xffffffffu, v.w, o)));
+}
+// the fast divide and exponential, within 2^-20 for |z| < 64: h is held in 16 bits
+__device__ __forceinline__ float silu_bf16(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 __device__ __forceinline__ void put_h(__nv_bfloat16* h, int64_t row, int f, int col, float v) {
   const __nv_bfloat16 hi = __float2bfloat16_rn(v);
   const float r = v - __bfloat162float(hi);
   h[row * 2 * f + col] = hi;
   h[row * 2 * f + f + col] = __float2bfloat16_rn(isfinite(r) ? r : 0.f);  // hi of an infinite v carries it alone
+}
+
+__device__ __forceinline__ void put_h4(__nv_bfloat16* h, int64_t row, int f, int col, const float (&v)[4]) {
+  __nv_bfloat162 hi[2], lo[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    hi[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    const float2 w = __bfloat1622float2(hi[i]);
+    const float r0 = v[2 * i] - w.x, r1 = v[2 * i + 1] - w.y;
+    lo[i] = __floats2bfloat162_rn(isfinite(r0) ? r0 : 0.f, isfinite(r1) ? r1 : 0.f);
+  }
+  *reinterpret_cast<uint2*>(h + row * 2 * f + col) = *reinterpret_cast<const uint2*>(hi);
+  *reinterpret_cast<uint2*>(h + row * 2 * f + f + col) = *reinterpret_cast<const uint2*>(lo);
 }
 
 __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_constant__ TcMapsD maps,
@@ -145,16 +204,17 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
   const uint32_t tmem = C.tmem, ring = smem_addr(smem);
 
   const int G = gridDim.x, c = blockIdx.x;
-  const int FT = a.f / DEC_N, DT = a.d / DEC_N, KU = a.d / TC_KB, KD = a.f / TC_KB;
+  const int FT = a.f / DEC_N / 2, DT = a.d / DEC_N, KU = a.d / TC_KB, KD = a.f / TC_KB / 2;  // FT, KD: of a half of f
   const int NT = pad16(a.T);
-  const Split up((int64_t)R.nact * FT * KU, G);
-  const int64_t per = (int64_t)R.nact * KD;
-  const Split down(per * DT, G);
-  const int64_t u0 = R.nact ? up.begin(c) : 0, u1 = R.nact ? up.begin(c + 1) : 0;
-  const int64_t v0 = R.nact ? down.begin(c) : 0, v1 = R.nact ? down.begin(c + 1) : 0;
+  const int per = R.nact * KD;  // units of a column tile of y: all experts' rows of W2
+  const Split up(R.nact * FT * KU, G), down(per * DT, G);
+  const int u0 = up.begin(c), u1 = up.begin(c + 1), v0 = down.begin(c), v1 = down.begin(c + 1);
+  uint32_t* bar = a.ctr + 2 * G;  // h of half 0, of half 1, the partial sums of y
+  const int64_t dslot = (int64_t)a.T * DEC_N;
 
   if (warp == 0) {
     if (lane == 0) {
+      const uint64_t once = l2_evict_first_policy();
       int st = 0, issued = 0;
       uint32_t phase = 0;
       bool alive = true;
@@ -169,67 +229,80 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
           phase ^= 1u;
         }
       };
-      for (int64_t u = u0; u < u1 && alive;) {
-        const Seg s = up_seg(R, u, u1, FT, KU);
-        for (int kb = s.kb0; kb < s.kb1 && acquire(); ++kb) {
-          const uint32_t fb = smem_addr(&C.full[st]), sA = ring + st * slot;
-          mbar_expect_tx(fb, 2 * TC_TILE + NT * 128);
-          const int row = s.e * a.d + kb * TC_KB;
-          tma_load_2d(sA, &maps.W1, fb, s.c0, row);
-          tma_load_2d(sA + TC_TILE / 2, &maps.W1, fb, s.c0 + 64, row);
-          tma_load_2d(sA + TC_TILE, &maps.W3, fb, s.c0, row);
-          tma_load_2d(sA + TC_TILE + TC_TILE / 2, &maps.W3, fb, s.c0 + 64, row);
-          tma_load_2d(sA + 2 * TC_TILE, &maps.x, fb, kb * TC_KB, 0);
-          next();
+      for (int half = 0; half < 2; ++half)
+        for (int u = u0; u < u1 && alive;) {
+          const Seg s = up_seg(R, u, u1, half, FT, KU);
+          for (int kb = s.kb0; kb < s.kb1 && acquire(); ++kb) {
+            const uint32_t fb = smem_addr(&C.full[st]), sA = ring + st * slot;
+            mbar_expect_tx(fb, 2 * TC_TILE + NT * 128);
+            const int row = s.e * a.d + kb * TC_KB;
+            tma_load_once(sA, &maps.W1, fb, s.c0, row, once);
+            tma_load_once(sA + TC_TILE / 2, &maps.W1, fb, s.c0 + 64, row, once);
+            tma_load_once(sA + TC_TILE, &maps.W3, fb, s.c0, row, once);
+            tma_load_once(sA + TC_TILE + TC_TILE / 2, &maps.W3, fb, s.c0 + 64, row, once);
+            tma_load_2d(sA + 2 * TC_TILE, &maps.x, fb, kb * TC_KB, 0);
+            next();
+          }
+          u += s.kb1 - s.kb0;
         }
-        u += s.kb1 - s.kb0;
-      }
-      auto load_w2 = [&](const Seg& s, int kb) {
+      auto load_w2 = [&](const Seg& s, int kb, int nk) {
         const uint32_t fb = smem_addr(&C.full[st]), sA = ring + st * slot;
-        mbar_expect_tx(fb, TC_TILE + 2 * pad16(s.n) * 128);
-        const int row = s.e * a.f + kb * TC_KB;
-        tma_load_2d(sA, &maps.W2, fb, s.c0, row);
-        tma_load_2d(sA + TC_TILE / 2, &maps.W2, fb, s.c0 + 64, row);
+        mbar_expect_tx(fb, nk * (TC_TILE + 2 * pad16(s.n) * 128));
+        for (int i = 0; i < nk; ++i) {
+          const int row = s.e * a.f + (kb + i) * TC_KB;
+          tma_load_once(sA + i * TC_TILE, &maps.W2, fb, s.c0, row, once);
+          tma_load_once(sA + i * TC_TILE + TC_TILE / 2, &maps.W2, fb, s.c0 + 64, row, once);
+        }
       };
-      auto load_h = [&](const Seg& s, int kb, int stage) {
-        const uint32_t fb = smem_addr(&C.full[stage]), sB = ring + stage * slot + TC_TILE;
+      auto load_h = [&](const Seg& s, int kb, int nk, int stage) {
+        const uint32_t fb = smem_addr(&C.full[stage]);
         const int n16 = pad16(s.n);
-        for (int r = 0; r < n16; r += 16) {
-          tma_load_2d(sB + r * 128, &maps.h, fb, kb * TC_KB, s.base + r);
-          tma_load_2d(sB + (n16 + r) * 128, &maps.h, fb, a.f + kb * TC_KB, s.base + r);
-        }
+        uint32_t sB = ring + stage * slot + nk * TC_TILE;
+        for (int i = 0; i < nk; ++i)
+          for (int part = 0; part < 2; ++part)
+            for (int r = 0; r < n16; r += 16, sB += 2048)
+              tma_load_2d(sB, &maps.h, fb, part * a.f + (kb + i) * TC_KB, s.base + r);
       };
-      // the ring full of W2 tiles, then the wait for every CTA's h, then their h tiles
-      const int first = st;
-      int ahead = 0;
-      int64_t v = v0;
-      for (; v < v1 && ahead < nst && alive; ++v, ++ahead) {
-        if (!acquire()) break;
-        const Seg s = down_seg(R, v, v1, per, KD);
-        load_w2(s, s.kb0);
-        next();
-      }
-      if (v0 < v1) {
-        if (alive && !wait_count(a.ctr + 2 * G, G, a.err, 711)) {
-          *abort_flag = 1;
-          alive = false;
-        }
-        fence_async_all();
-        int stage = first;
-        for (int i = 0; i < ahead; ++i) {  // after a timeout too: every stage begun is completed
-          const Seg s = down_seg(R, v0 + i, v1, per, KD);
-          load_h(s, s.kb0, stage);
-          if (++stage == nst) stage = 0;
-        }
-      }
-      while (v < v1 && alive) {
-        const Seg s = down_seg(R, v, v1, per, KD);
-        for (int kb = s.kb0; kb < s.kb1 && acquire(); ++kb) {
-          load_w2(s, kb);
-          load_h(s, kb, st);
+      for (int half = 0; half < 2; ++half) {
+        // the ring full of W2 tiles, then the wait for every CTA's h, then their h tiles
+        const int first = st;
+        int ahead = 0;
+        int v = v0;
+        while (v < v1 && ahead < nst && alive && acquire()) {
+          const Seg s = down_seg(R, v, v1, half, per, KD);
+          const int nk = down_units(s, s.kb0);
+          load_w2(s, s.kb0, nk);
           next();
+          v += nk;
+          ++ahead;
         }
-        v += s.kb1 - s.kb0;
+        if (ahead > 0) {
+          if (!wait_count(bar + half, G, a.err, 711)) {
+            *abort_flag = 1;
+            alive = false;
+          }
+          fence_async_all();
+          int stage = first;
+          for (int w = v0; w < v;) {  // after a timeout too: every stage begun is completed
+            const Seg s = down_seg(R, w, v1, half, per, KD);
+            const int nk = down_units(s, s.kb0);
+            load_h(s, s.kb0, nk, stage);
+            if (++stage == nst) stage = 0;
+            w += nk;
+          }
+        }
+        while (v < v1 && alive) {
+          const Seg s = down_seg(R, v, v1, half, per, KD);
+          int kb = s.kb0;
+          while (kb < s.kb1 && acquire()) {
+            const int nk = down_units(s, kb);
+            load_w2(s, kb, nk);
+            load_h(s, kb, nk, st);
+            next();
+            kb += nk;
+          }
+          v += s.kb1 - s.kb0;
+        }
       }
       if (!alive) {  // wait for the copies in flight
         const int n = issued < nst ? issued : nst;
@@ -268,44 +341,51 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
         tc_fence_after();
         return alive;
       };
-      for (int64_t u = u0; u < u1 && open();) {
-        const Seg s = up_seg(R, u, u1, FT, KU);
-        const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(NT);
-        for (int kb = s.kb0; kb < s.kb1 && filled(); ++kb) {
-          const uint32_t sA = ring + st * slot, sB = sA + 2 * TC_TILE;
+      for (int half = 0; half < 2; ++half)
+        for (int u = u0; u < u1 && alive && open();) {
+          const Seg s = up_seg(R, u, u1, half, FT, KU);
+          const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(NT);
+          for (int kb = s.kb0; kb < s.kb1 && filled(); ++kb) {
+            const uint32_t sA = ring + st * slot, sB = sA + 2 * TC_TILE;
 #pragma unroll
-          for (int q = 0; q < TC_KB / 16; ++q) {
-            const uint64_t bd = sdesc(sB + q * 32, 16, 1024);
-            const uint32_t on = kb != s.kb0 || q != 0;
-            umma_bf16(acc, sdesc(sA + q * 2048, 8192, 1024), bd, id, on);
-            umma_bf16(acc + TC_B, sdesc(sA + TC_TILE + q * 2048, 8192, 1024), bd, id, on);
+            for (int q = 0; q < TC_KB / 16; ++q) {
+              const uint64_t bd = sdesc(sB + q * 32, 16, 1024);
+              const uint32_t on = kb != s.kb0 || q != 0;
+              umma_bf16(acc, sdesc(sA + q * 2048, 8192, 1024), bd, id, on);
+              umma_bf16(acc + TC_B, sdesc(sA + TC_TILE + q * 2048, 8192, 1024), bd, id, on);
+            }
+            advance();
           }
-          advance();
+          if (!alive) break;
+          umma_commit(smem_addr(&C.tfull[seg & 1]));
+          ++seg;
+          u += s.kb1 - s.kb0;
         }
-        if (!alive) break;
-        umma_commit(smem_addr(&C.tfull[seg & 1]));
-        ++seg;
-        u += s.kb1 - s.kb0;
-      }
-      for (int64_t v = v0; v < v1 && alive && open();) {
-        const Seg s = down_seg(R, v, v1, per, KD);
-        const int n16 = pad16(s.n);
-        const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(n16);
-        for (int kb = s.kb0; kb < s.kb1 && filled(); ++kb) {
-          const uint32_t sA = ring + st * slot, sB = sA + TC_TILE;
+      for (int half = 0; half < 2; ++half)
+        for (int v = v0; v < v1 && alive && open();) {
+          const Seg s = down_seg(R, v, v1, half, per, KD);
+          const int n16 = pad16(s.n);
+          const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(n16);
+          for (int kb = s.kb0; kb < s.kb1 && filled();) {
+            const int nk = down_units(s, kb);
+            for (int i = 0; i < nk; ++i) {
+              const uint32_t sA = ring + st * slot + i * TC_TILE;
+              const uint32_t sB = ring + st * slot + nk * TC_TILE + i * 2 * n16 * 128;
 #pragma unroll
-          for (int q = 0; q < TC_KB / 16; ++q) {
-            const uint64_t ad = sdesc(sA + q * 2048, 8192, 1024);
-            umma_bf16(acc, ad, sdesc(sB + q * 32, 16, 1024), id, kb != s.kb0 || q != 0);
-            umma_bf16(acc, ad, sdesc(sB + n16 * 128 + q * 32, 16, 1024), id, 1);
+              for (int q = 0; q < TC_KB / 16; ++q) {
+                const uint64_t ad = sdesc(sA + q * 2048, 8192, 1024);
+                umma_bf16(acc, ad, sdesc(sB + q * 32, 16, 1024), id, kb + i != s.kb0 || q != 0);
+                umma_bf16(acc, ad, sdesc(sB + n16 * 128 + q * 32, 16, 1024), id, 1);
+              }
+            }
+            advance();
+            kb += nk;
           }
-          advance();
+          if (!alive) break;
+          umma_commit(smem_addr(&C.tfull[seg & 1]));
+          ++seg;
+          v += s.kb1 - s.kb0;
         }
-        if (!alive) break;
-        umma_commit(smem_addr(&C.tfull[seg & 1]));
-        ++seg;
-        v += s.kb1 - s.kb0;
-      }
       umma_commit(smem_addr(&C.drain));
       for (uint32_t it = 0; it < (1u << 26) && !mbar_try_wait(smem_addr(&C.drain), 0); ++it) {
       }
@@ -341,121 +421,141 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
     // ---- up product ----
     __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.h);
     const int64_t pslot = (int64_t)a.T * 2 * DEC_N;
-    int8_t* row_of = C.row_of[q];
-    for (int64_t u = u0; u < u1 && ready();) {
-      const Seg s = up_seg(R, u, u1, FT, KU);
-      const bool whole = s.kb0 == 0 && s.kb1 == KU;
-      float* part = a.up_part + ((int64_t)c * 2 + (s.kb0 > 0 ? 0 : 1)) * pslot + col;
-      for (int t = lane; t < DEC_T; t += 32) row_of[t] = -1;
-      __syncwarp();
-      for (int m = lane; m < s.n; m += 32) row_of[R.tok[s.base + m]] = (int8_t)m;
-      __syncwarp();
-      for (int t0 = 0; t0 < NT; t0 += 16) {
-        uint32_t ra[16], rb[16];
-        const uint32_t at = tmem + lanes + (seg & 1) * TC_BUF + t0;
-        tmem_ld16(at, ra);
-        tmem_ld16(at + TC_B, rb);
-        tmem_ld_wait16(ra);
-        tmem_reg_fence16(rb);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int m = row_of[t0 + i];
-          if (m < 0) continue;
-          const float va = __uint_as_float(ra[i]), vb = __uint_as_float(rb[i]);
+    for (int half = 0; half < 2 && alive; ++half) {
+      float* parts = a.up_part + (int64_t)half * G * 2 * pslot;
+      uint32_t* ctr = a.ctr + half * G;
+      for (int u = u0; u < u1 && ready();) {
+        const Seg s = up_seg(R, u, u1, half, FT, KU);
+        const bool whole = s.kb0 == 0 && s.kb1 == KU;
+        float* part = parts + ((int64_t)c * 2 + (s.kb0 > 0 ? 0 : 1)) * pslot + col;
+#pragma unroll 1
+        for (int m = 0; m < s.n; ++m) {  // the row's token is its column
+          const int row = s.base + m;
+          const uint32_t at = tmem + lanes + (seg & 1) * TC_BUF + R.tok[row];
+          const float2 v = tmem_ld_ab(at);
           if (whole) {
-            put_h(h, s.base + m, a.f, s.c0 + col, R.gate[s.base + m] * dec_silu(va) * vb);
+            put_h(h, row, a.f, s.c0 + col, R.gate[row] * silu_bf16(v.x) * v.y);
           } else {
-            part[m * 2 * DEC_N] = va;
-            part[m * 2 * DEC_N + DEC_N] = vb;
+            part[m * 2 * DEC_N] = v.x;
+            part[m * 2 * DEC_N + DEC_N] = v.y;
           }
         }
+        release();
+        if (!whole) signal(ctr + up.owner(s.tile * KU));
+        u += s.kb1 - s.kb0;
       }
-      release();
-      if (!whole) signal(a.ctr + up.owner(s.tile * KU));
-      u += s.kb1 - s.kb0;
-    }
-    // a share of each tile that other CTAs have a part of
-    for (int64_t u = u0; u < u1 && alive;) {
-      const int64_t tile = u / KU, end = (tile + 1) * KU;
-      const int first = up.owner(tile * KU), segs = up.owner(end - 1) - first + 1;
-      if (segs > 1 && wait_all(a.ctr + first, segs, 731)) {
-        const int e = R.act[tile / FT], c0 = (int)(tile % FT) * DEC_N, N = R.cnt[e] * DEC_N;
-        const int i1 = (int)((int64_t)(c - first + 1) * N / segs);
-        for (int i = (int)((int64_t)(c - first) * N / segs) + tid; i < i1; i += 128) {
-          const int m = i / DEC_N, cc = i % DEC_N, row = R.base[e] + m;
-          float va = 0.f, vb = 0.f;
+      // a share of each tile that other CTAs have a part of
+      for (int u = u0; u < u1 && alive;) {
+        const int64_t tile = u / KU, end = (tile + 1) * KU;
+        const int first = up.owner(tile * KU), segs = up.owner(end - 1) - first + 1;
+        if (segs > 1 && wait_all(ctr + first, segs, 731)) {
+          const Seg s = up_seg(R, tile * KU, end, half, FT, KU);
+          const float* p0 = parts + ((int64_t)first * 2 + 1) * pslot;  // the first CTA's, then the others'
+          const int N4 = s.n * (DEC_N / 4), j0 = (c - first) * N4 / segs, j1 = (c - first + 1) * N4 / segs;
+          // four columns to `L` threads, each some of the parts
+          const int L = j1 - j0 <= 16 ? 8 : 1, sub = tid % L;
+#pragma unroll 1
+          for (int jb = j0; jb < j1; jb += 128 / L) {
+            const int j = jb + tid / L, m = j / (DEC_N / 4), cc = j % (DEC_N / 4) * 4;
+            float4 va = make_float4(0.f, 0.f, 0.f, 0.f), vb = va;
+            if (j < j1) {
 #pragma unroll 4
-          for (int g = 0; g < segs; ++g) {
-            const float* p = a.up_part + ((int64_t)(first + g) * 2 + (g > 0 ? 0 : 1)) * pslot + m * 2 * DEC_N + cc;
-            va += __ldcg(p);
-            vb += __ldcg(p + DEC_N);
+              for (int g = sub; g < segs; g += L) {
+                const float4* p = reinterpret_cast<const float4*>(p0 + (g == 0 ? 0 : g * 2 - 1) * pslot + m * 2 * DEC_N + cc);
+                add4(va, __ldcg(p));
+                add4(vb, __ldcg(p + DEC_N / 4));
+              }
+            }
+#pragma unroll 1
+            for (int o = 1; o < L; o *= 2) {
+              xor4(va, o);
+              xor4(vb, o);
+            }
+            if (sub == 0 && j < j1) {
+              const float gate = R.gate[s.base + m];
+              const float v[4] = {gate * silu_bf16(va.x) * vb.x, gate * silu_bf16(va.y) * vb.y,
+                                  gate * silu_bf16(va.z) * vb.z, gate * silu_bf16(va.w) * vb.w};
+              put_h4(h, s.base + m, a.f, s.c0 + cc, v);
+            }
           }
-          put_h(h, row, a.f, c0 + cc, R.gate[row] * dec_silu(va) * vb);
         }
+        u = end < u1 ? end : u1;
       }
-      u = end < u1 ? end : u1;
+      fence_async_all();  // h is read by the TMA
+      if (alive) signal(bar + half);
     }
-    fence_async_all();  // h is read by the TMA
-    if (alive) signal(a.ctr + 2 * G);
 
     // ---- down product ----
-    const int64_t dslot = (int64_t)a.T * DEC_N;
-    const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(a.io.residual);
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.io.y);
-    auto put_y = [&](int t, int column, float v) {
-      const int64_t o = (int64_t)t * a.d + column;
-      y[o] = __float2bfloat16_rn(res ? v + __bfloat162float(res[o]) : v);
-    };
-    if (R.nact == 0) {  // every assignment was dropped
-      for (int64_t i = (int64_t)c * 128 + tid; i < (int64_t)a.T * a.d; i += (int64_t)G * 128)
-        put_y((int)(i / a.d), (int)(i % a.d), 0.f);
-    }
     for (int t = 0; t < a.T; ++t) yacc[t * DEC_N + col] = 0.f;
-    for (int64_t v = v0; v < v1 && alive && ready();) {
-      const Seg s = down_seg(R, v, v1, per, KD);
-      for (int m0 = 0; m0 < s.n; m0 += 16) {
-        uint32_t r[16];
-        tmem_ld16(tmem + lanes + (seg & 1) * TC_BUF + m0, r);
-        tmem_ld_wait16(r);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (m0 + i < s.n) yacc[R.tok[s.base + m0 + i] * DEC_N + col] += __uint_as_float(r[i]);
-      }
-      release();
-      v += s.kb1 - s.kb0;
-      if (v == v1 || v == (s.tile + 1) * per) {  // the last of this column tile here
-        const bool head = v0 > s.tile * per, whole = !head && v == (s.tile + 1) * per;
-        float* part = a.down_part + ((int64_t)c * 2 + (head ? 0 : 1)) * dslot + col;
-        for (int t = 0; t < a.T; ++t) {
-          const float w = yacc[t * DEC_N + col];
-          yacc[t * DEC_N + col] = 0.f;
-          if (whole) put_y(t, s.c0 + col, w);
-          else part[t * DEC_N] = w;
+    for (int half = 0; half < 2; ++half)
+      for (int v = v0; v < v1 && alive && ready();) {
+        const Seg s = down_seg(R, v, v1, half, per, KD);
+#pragma unroll 1
+        for (int m0 = 0; m0 < s.n; m0 += 4) {
+          const float4 r = tmem_ld4(tmem + lanes + (seg & 1) * TC_BUF + m0);
+          const uint8_t* tok = R.tok + s.base + m0;
+          yacc[tok[0] * DEC_N + col] += r.x;
+          if (m0 + 1 < s.n) yacc[tok[1] * DEC_N + col] += r.y;
+          if (m0 + 2 < s.n) yacc[tok[2] * DEC_N + col] += r.z;
+          if (m0 + 3 < s.n) yacc[tok[3] * DEC_N + col] += r.w;
         }
-        if (!whole) signal(a.ctr + G + down.owner(s.tile * per));
-      }
-    }
-    for (int64_t v = v0; v < v1 && alive;) {
-      const int64_t tile = v / per, end = (tile + 1) * per;
-      const int first = down.owner(tile * per), segs = down.owner(end - 1) - first + 1;
-      if (segs > 1 && wait_all(a.ctr + G + first, segs, 732)) {
-        const int N = a.T * DEC_N, i1 = (int)((int64_t)(c - first + 1) * N / segs);
-        for (int i = (int)((int64_t)(c - first) * N / segs) + tid; i < i1; i += 128) {
-          float w = 0.f;
+        release();
+        v += s.kb1 - s.kb0;
+        if (v == v1 || v == (s.tile + 1) * per) {  // the last of this column tile here
+          float* part = a.down_part + ((int64_t)half * (G + DT) + c + s.tile) * dslot + col;
 #pragma unroll 4
-          for (int g = 0; g < segs; ++g)
-            w += __ldcg(a.down_part + ((int64_t)(first + g) * 2 + (g > 0 ? 0 : 1)) * dslot + i);
-          put_y(i / DEC_N, (int)tile * DEC_N + i % DEC_N, w);
+          for (int t = 0; t < a.T; ++t) {
+            part[t * DEC_N] = yacc[t * DEC_N + col];
+            yacc[t * DEC_N + col] = 0.f;
+          }
         }
       }
-      v = end < v1 ? end : v1;
-    }
+    if (alive) signal(bar + 2);
+    if (alive) wait_all(bar + 2, G, 732);
+    if (!alive) *abort_flag = 1;
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, TC_COLS);
+  if (*abort_flag) return;
+
+  // ---- y: the sums of a column tile's CTAs, half 0 and then half 1; `L` threads
+  // take every L-th of them for four columns ----
+  const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(a.io.residual);
+  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.io.y);
+  const int64_t items = (int64_t)a.T * a.d / 4;
+  const int i0 = (int)(c * items / G), i1 = (int)((c + 1) * items / G);
+  const int L = i1 - i0 <= TC_NT / 8 ? 8 : 1, sub = threadIdx.x % L;
+#pragma unroll 1
+  for (int ib = i0; ib < i1; ib += TC_NT / L) {
+    const int i = ib + threadIdx.x / L;
+    const bool on = i < i1;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int t = i / (a.d / 4), col = (i - t * (a.d / 4)) * 4;
+    if (on && R.nact > 0) {
+      const int dt = col / DEC_N, first = down.owner(dt * per), n = down.owner((dt + 1) * per - 1) - first + 1;
+      const float* p = a.down_part + (int64_t)(first + dt) * dslot + t * DEC_N + col % DEC_N;
+#pragma unroll 4
+      for (int g = sub; g < 2 * n; g += L) {
+        add4(v, __ldcg(reinterpret_cast<const float4*>(p + (int64_t)(g < n ? g : G + DT + g - n) * dslot)));
+      }
+    }
+#pragma unroll 1
+    for (int o = 1; o < L; o *= 2) xor4(v, o);
+    if (on && sub == 0) {
+      const int64_t o = (int64_t)t * a.d + col;
+      if (res) {
+        const uint2 u = *reinterpret_cast<const uint2*>(res + o);
+        const float2 r0 = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(u.x));
+        const float2 r1 = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(u.y));
+        v = make_float4(v.x + r0.x, v.y + r0.y, v.z + r1.x, v.w + r1.y);
+      }
+      __nv_bfloat162 w[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+      *reinterpret_cast<uint2*>(y + o) = *reinterpret_cast<const uint2*>(w);
+    }
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 dec_encode = nullptr;
@@ -490,7 +590,7 @@ cudaError_t launch_decode_tc(const Shape& s, const DecodeArgs& args, int G, cuda
   if (!dec_encode_ready()) return cudaErrorNotSupported;
   DecodeArgs a = args;
   const uint32_t NT = (uint32_t)(s.T + 15) / 16 * 16;
-  int slot = 2 * TC_TILE + (int)NT * 128;
+  int slot = 2 * TC_TILE + 8192;  // two weight tiles, and 64 tokens of x or two units' hi and lo of 16 rows of h
   const int fixed = 1024 + (int)sizeof(Routing) + (int)sizeof(TcCtrl) + s.T * DEC_N * 4;
   int nst = (TC_SMEM_MAX - fixed) / slot;
   if (nst > TC_MAX_ST) nst = TC_MAX_ST;
