@@ -242,7 +242,7 @@ DecodeWs decode_ws(const Shape& s) {
   w.gates = w.ids + up256(T * s.k * 4);
   w.ctr = w.gates + up256(T * s.k * 4);
   w.h = w.ctr + up256((2 * G + 3) * 4);
-  w.up = w.h + up256(T * s.k * s.f * 4);
+  w.up = w.h + up256(s.bf16 ? decode_tc_h_bytes(s) : T * s.k * s.f * 4);
   w.down = w.up + up256(2 * G * 2 * T * 2 * DEC_N * 4);
   w.total = w.down + up256(2 * (G + DT) * T * DEC_N * 4);
   return w;

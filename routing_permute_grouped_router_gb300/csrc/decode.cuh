@@ -19,7 +19,7 @@ struct DecodeArgs {
   int32_t* ids;       // [T, k] picks and their gates, from the CTA that made them to the others
   float* gates;
   uint32_t* ctr;      // [2 G + 3]: arrivals at split tiles and grid barriers
-  void* h;            // rows of the experts, gate * silu(a) * b: [T k][f] fp32, or [T k][hi f | lo f] bf16
+  void* h;            // rows of the experts, gate * silu(a) * b: [T k][f] fp32, or tiles of bf16 (decode_tc.cu)
   float* up_part;     // [2][G][2][T][2 * DEC_N] a and b of split tiles
   float* down_part;   // [2][G + column tiles][T][DEC_N] sums of the CTAs over their part of a column tile
   uint32_t* err;
@@ -27,6 +27,7 @@ struct DecodeArgs {
   int groups, slices;  // of the scores: groups of DEC_TG tokens, slices of d
 };
 // decode_tc.cu: bf16 layers, G CTAs
+size_t decode_tc_h_bytes(const Shape& s);
 cudaError_t launch_decode_tc(const Shape& s, const DecodeArgs& args, int G, cudaStream_t st);
 
 namespace {
@@ -48,6 +49,7 @@ struct alignas(16) Routing {
   uint8_t tok[DEC_ROWS];   // token of each row
   int cnt[DEC_E];          // kept rows of each expert
   int16_t base[DEC_E];     // first row of each expert
+  int16_t block[DEC_E];    // first block of 16 rows of each expert, where each begins a block (bf16: rows of h)
   uint8_t act[DEC_E];      // experts with rows
   int nact;
 };
@@ -287,8 +289,20 @@ __device__ __forceinline__ void list_rows(const DecodeArgs& a, Routing& R) {
     }
     if (lane == 31) R.nact = pre >> 16;
     pre -= own;
+    int blocks = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) blocks += (c[q] + 15) / 16;
+    int at = blocks;
+#pragma unroll 1
+    for (int o = 1; o < 32; o *= 2) {
+      const int u = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += u;
+    }
+    at -= blocks;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
+      R.block[lane * 4 + q] = (int16_t)at;
+      at += (c[q] + 15) / 16;
       R.base[lane * 4 + q] = (int16_t)(pre & 0xffff);
       if (c[q] > 0) {
         R.act[pre >> 16] = (uint8_t)(lane * 4 + q);

@@ -32,18 +32,20 @@ constexpr int TC_NT = 256;
 constexpr int TC_KB = 64;                 // rows of a unit: 128 bytes of a token's row
 constexpr int TC_TILE = DEC_N * TC_KB * 2;  // 16 KB: two boxes of 64 columns x 64 rows
 constexpr int TC_MAX_ST = 8;
+constexpr int TC_SLOT = 2 * TC_TILE + 8192;  // and 64 tokens of x, or two units' hi and lo of 16 rows of h
+constexpr int TC_QUEUE = 6;
 constexpr int TC_SMEM_MAX = 232448;       // 227 KB a CTA
 constexpr uint32_t TC_COLS = 256;         // TMEM: two accumulators of a and b, 64 tokens each
 constexpr uint32_t TC_BUF = 128, TC_B = 64;
 
 struct alignas(16) TcCtrl {
-  uint64_t full[TC_MAX_ST], empty[TC_MAX_ST], tfull[2], tempty[2], drain;
+  uint64_t wfull[TC_MAX_ST], bfull[TC_MAX_ST], empty[TC_MAX_ST], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
 };
 
 struct TcMapsD {
-  CUtensorMap x, W1, W3, W2, h;
+  CUtensorMap x, W1, W3, W2;
 };
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -68,7 +70,7 @@ __host__ __device__ constexpr uint32_t dec_idesc(int n) {  // fp32 D, bf16 A (MN
 
 // A CTA's consecutive units of one weight tile.
 struct Seg {
-  int e, n, base;  // expert, its rows, the first of them
+  int e, n, base, block;  // expert, its rows, the first of them, its first block of rows of h
   int c0;          // first weight column
   int kb0, kb1;    // units
   int tile;        // up: the weight tile; down: the column tile of y
@@ -84,6 +86,7 @@ __device__ __forceinline__ Seg up_seg(const Routing& R, int u, int u1, int half,
   s.c0 = (half * FT + s.tile - ai * FT) * DEC_N;
   s.n = R.cnt[s.e];
   s.base = R.base[s.e];
+  s.block = R.block[s.e];
   return s;
 }
 __device__ __forceinline__ Seg down_seg(const Routing& R, int u, int u1, int half, int per, int KD) {
@@ -98,16 +101,29 @@ __device__ __forceinline__ Seg down_seg(const Routing& R, int u, int u1, int hal
   s.c0 = s.tile * DEC_N;
   s.n = R.cnt[s.e];
   s.base = R.base[s.e];
+  s.block = R.block[s.e];
   return s;
 }
-// a load of weights: they pass through L2 once, so they leave it before anything else does (code, tokens, partial sums)
-__device__ __forceinline__ void tma_load_once(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1,
-                                              uint64_t policy) {
+// A 128-column weight tile: two boxes of 64 columns, [row][chunk of 64 columns].  Weights pass through L2 once, so
+// they leave it before anything else does (code, tokens, partial sums).
+__device__ __forceinline__ void load_weights(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row, int chunk,
+                                             uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
-      "[%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(row), "r"(chunk), "l"(policy)
       : "memory");
+}
+// bytes, a multiple of 16, between 16-byte boundaries
+__device__ __forceinline__ void load_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// wait, the call only where the phase is not complete yet
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
+                                          uint32_t where) {
+  return mbar_try_wait(smem_addr(bar), parity) || mbar_wait(smem_addr(bar), parity, abort_flag, err, where);
 }
 __device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
 // units of a stage of the down product: two where the rows are few enough for both to fit
@@ -144,28 +160,44 @@ __device__ __forceinline__ void xor4(float4& v, int o) {
 }
 // the fast divide and exponential, within 2^-20 for |z| < 64: h is held in 16 bits
 __device__ __forceinline__ float silu_bf16(float z) { return __fdividef(z, 1.f + __expf(-z)); }
-__device__ __forceinline__ void put_h(__nv_bfloat16* h, int64_t row, int f, int col, float v) {
-  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-  const float r = v - __bfloat162float(hi);
-  h[row * 2 * f + col] = hi;
-  h[row * 2 * f + f + col] = __float2bfloat16_rn(isfinite(r) ? r : 0.f);  // hi of an infinite v carries it alone
+// h is kept as the down product reads it: for every 64 columns an expert's
+// blocks of 16 rows, [hi rows | lo rows] of 128 bytes in the 128-byte swizzle
+// of the MMA operand, so one plain copy brings a unit's rows.
+__device__ __forceinline__ char* h_at(const DecodeArgs& a, int blocks, const Seg& s, int m, int col) {
+  const int64_t tile = (int64_t)(col / 64) * blocks + s.block;
+  return static_cast<char*>(a.h) + tile * 4096 + m * 128 + ((((col % 64) / 8) ^ (m & 7)) << 4) + (col % 8) * 2;
 }
-
-__device__ __forceinline__ void put_h4(__nv_bfloat16* h, int64_t row, int f, int col, const float (&v)[4]) {
+__device__ __forceinline__ float lo_part(float v, float hi) {
+  const float r = v - hi;
+  return isfinite(r) ? r : 0.f;  // the hi of an infinite v carries it alone
+}
+__device__ __forceinline__ void put_h(char* p, int n16, float v) {
+  const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+  *reinterpret_cast<__nv_bfloat16*>(p) = hi;
+  *reinterpret_cast<__nv_bfloat16*>(p + n16 * 128) = __float2bfloat16_rn(lo_part(v, __bfloat162float(hi)));
+}
+__device__ __forceinline__ void put_h4(char* p, int n16, const float (&v)[4]) {
   __nv_bfloat162 hi[2], lo[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     hi[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
     const float2 w = __bfloat1622float2(hi[i]);
-    const float r0 = v[2 * i] - w.x, r1 = v[2 * i + 1] - w.y;
-    lo[i] = __floats2bfloat162_rn(isfinite(r0) ? r0 : 0.f, isfinite(r1) ? r1 : 0.f);
+    lo[i] = __floats2bfloat162_rn(lo_part(v[2 * i], w.x), lo_part(v[2 * i + 1], w.y));
   }
-  *reinterpret_cast<uint2*>(h + row * 2 * f + col) = *reinterpret_cast<const uint2*>(hi);
-  *reinterpret_cast<uint2*>(h + row * 2 * f + f + col) = *reinterpret_cast<const uint2*>(lo);
+  *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(hi);
+  *reinterpret_cast<uint2*>(p + n16 * 128) = *reinterpret_cast<const uint2*>(lo);
+}
+
+// After a wait that gave up: the copies in flight land within this time.
+__device__ __noinline__ void settle() {
+  const uint64_t t0 = dec_now();
+  while (dec_now() - t0 < 5000000ull) {
+  }
 }
 
 __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_constant__ TcMapsD maps,
-                                                             const __grid_constant__ DecodeArgs a, int nst, int slot) {
+                                                             const __grid_constant__ DecodeArgs a, int nst, int blocks) {
+  constexpr int slot = TC_SLOT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Routing& R = *reinterpret_cast<Routing*>(smem + nst * slot);
@@ -176,7 +208,8 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < nst; ++i) {
-      mbar_init(smem_addr(&C.full[i]), 1);
+      mbar_init(smem_addr(&C.wfull[i]), 1);
+      mbar_init(smem_addr(&C.bfull[i]), 1);
       mbar_init(smem_addr(&C.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -190,7 +223,6 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
     prefetch_map(&maps.W1);
     prefetch_map(&maps.W3);
     prefetch_map(&maps.W2);
-    prefetch_map(&maps.h);
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(&C.tmem), TC_COLS);
@@ -213,110 +245,129 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
   const int64_t dslot = (int64_t)a.T * DEC_N;
 
   if (warp == 0) {
+    // ---- weights ----
     if (lane == 0) {
       const uint64_t once = l2_evict_first_policy();
-      int st = 0, issued = 0;
-      uint32_t phase = 0;
+      int st = 0, oldest = 0, stages = 0, queued = 0;
+      uint32_t phase = 0, oldest_phase = 0, sizes = 0;  // sizes: units of the stages on their way, 4 bits each
       bool alive = true;
-      auto acquire = [&]() {
-        if (!mbar_wait(smem_addr(&C.empty[st]), phase ^ 1u, abort_flag, a.err, 710)) alive = false;
-        return alive;
+      // At most TC_QUEUE units of weights are on their way: more only lengthen
+      // HBM's queue, and with it the latency of every fence and atomic.
+      auto arrived = [&]() {
+        queued -= sizes & 15;
+        sizes >>= 4;
+        --stages;
+        if (++oldest == nst) {
+          oldest = 0;
+          oldest_phase ^= 1u;
+        }
+      };
+      auto open = [&](int units) {
+        while (stages > 0 && queued + units > TC_QUEUE) {
+          if (!ring_wait(&C.wfull[oldest], oldest_phase, abort_flag, a.err, 712)) return alive = false;
+          arrived();
+        }
+        if (!ring_wait(&C.empty[st], phase ^ 1u, abort_flag, a.err, 710)) return alive = false;
+        if (stages == nst) arrived();  // this slot's last, which has been read
+        mbar_expect_tx(smem_addr(&C.wfull[st]), units * TC_TILE);
+        sizes |= (uint32_t)units << (4 * stages++);
+        queued += units;
+        return true;
       };
       auto next = [&]() {
-        ++issued;
         if (++st == nst) {
           st = 0;
           phase ^= 1u;
         }
       };
+#pragma unroll 1
       for (int half = 0; half < 2; ++half)
         for (int u = u0; u < u1 && alive;) {
           const Seg s = up_seg(R, u, u1, half, FT, KU);
-          for (int kb = s.kb0; kb < s.kb1 && acquire(); ++kb) {
-            const uint32_t fb = smem_addr(&C.full[st]), sA = ring + st * slot;
-            mbar_expect_tx(fb, 2 * TC_TILE + NT * 128);
-            const int row = s.e * a.d + kb * TC_KB;
-            tma_load_once(sA, &maps.W1, fb, s.c0, row, once);
-            tma_load_once(sA + TC_TILE / 2, &maps.W1, fb, s.c0 + 64, row, once);
-            tma_load_once(sA + TC_TILE, &maps.W3, fb, s.c0, row, once);
-            tma_load_once(sA + TC_TILE + TC_TILE / 2, &maps.W3, fb, s.c0 + 64, row, once);
-            tma_load_2d(sA + 2 * TC_TILE, &maps.x, fb, kb * TC_KB, 0);
+          int row = s.e * a.d + s.kb0 * TC_KB;
+#pragma unroll 1
+          for (int kb = s.kb0; kb < s.kb1 && open(2); ++kb, row += TC_KB) {
+            const uint32_t fb = smem_addr(&C.wfull[st]), sA = ring + st * slot;
+            load_weights(sA, &maps.W1, fb, row, s.c0 / 64, once);
+            load_weights(sA + TC_TILE, &maps.W3, fb, row, s.c0 / 64, once);
             next();
           }
           u += s.kb1 - s.kb0;
         }
-      auto load_w2 = [&](const Seg& s, int kb, int nk) {
-        const uint32_t fb = smem_addr(&C.full[st]), sA = ring + st * slot;
-        mbar_expect_tx(fb, nk * (TC_TILE + 2 * pad16(s.n) * 128));
-        for (int i = 0; i < nk; ++i) {
-          const int row = s.e * a.f + (kb + i) * TC_KB;
-          tma_load_once(sA + i * TC_TILE, &maps.W2, fb, s.c0, row, once);
-          tma_load_once(sA + i * TC_TILE + TC_TILE / 2, &maps.W2, fb, s.c0 + 64, row, once);
-        }
-      };
-      auto load_h = [&](const Seg& s, int kb, int nk, int stage) {
-        const uint32_t fb = smem_addr(&C.full[stage]);
-        const int n16 = pad16(s.n);
-        uint32_t sB = ring + stage * slot + nk * TC_TILE;
-        for (int i = 0; i < nk; ++i)
-          for (int part = 0; part < 2; ++part)
-            for (int r = 0; r < n16; r += 16, sB += 2048)
-              tma_load_2d(sB, &maps.h, fb, part * a.f + (kb + i) * TC_KB, s.base + r);
-      };
-      for (int half = 0; half < 2; ++half) {
-        // the ring full of W2 tiles, then the wait for every CTA's h, then their h tiles
-        const int first = st;
-        int ahead = 0;
-        int v = v0;
-        while (v < v1 && ahead < nst && alive && acquire()) {
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half)
+        for (int v = v0; v < v1 && alive;) {
           const Seg s = down_seg(R, v, v1, half, per, KD);
-          const int nk = down_units(s, s.kb0);
-          load_w2(s, s.kb0, nk);
-          next();
-          v += nk;
-          ++ahead;
-        }
-        if (ahead > 0) {
-          if (!wait_count(bar + half, G, a.err, 711)) {
-            *abort_flag = 1;
-            alive = false;
-          }
-          fence_async_all();
-          int stage = first;
-          for (int w = v0; w < v;) {  // after a timeout too: every stage begun is completed
-            const Seg s = down_seg(R, w, v1, half, per, KD);
-            const int nk = down_units(s, s.kb0);
-            load_h(s, s.kb0, nk, stage);
-            if (++stage == nst) stage = 0;
-            w += nk;
-          }
-        }
-        while (v < v1 && alive) {
-          const Seg s = down_seg(R, v, v1, half, per, KD);
-          int kb = s.kb0;
-          while (kb < s.kb1 && acquire()) {
+          int row = s.e * a.f + s.kb0 * TC_KB;
+#pragma unroll 1
+          for (int kb = s.kb0; kb < s.kb1;) {
             const int nk = down_units(s, kb);
-            load_w2(s, kb, nk);
-            load_h(s, kb, nk, st);
+            if (!open(nk)) break;
+            const uint32_t fb = smem_addr(&C.wfull[st]), sA = ring + st * slot;
+            load_weights(sA, &maps.W2, fb, row, s.c0 / 64, once);
+            if (nk == 2) load_weights(sA + TC_TILE, &maps.W2, fb, row + TC_KB, s.c0 / 64, once);
             next();
             kb += nk;
+            row += nk * TC_KB;
+          }
+          v += s.kb1 - s.kb0;
+        }
+      if (!alive) settle();
+    }
+  } else if (warp == 2) {
+    // ---- tokens: x, then h ----
+    if (lane == 0) {
+      int st = 0;
+      uint32_t phase = 0;
+      bool alive = true;
+      auto open = [&](int bytes) {
+        if (!ring_wait(&C.empty[st], phase ^ 1u, abort_flag, a.err, 713)) return alive = false;
+        mbar_expect_tx(smem_addr(&C.bfull[st]), bytes);
+        return true;
+      };
+      auto next = [&]() {
+        if (++st == nst) {
+          st = 0;
+          phase ^= 1u;
+        }
+      };
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half)
+        for (int u = u0; u < u1 && alive;) {
+          const Seg s = up_seg(R, u, u1, half, FT, KU);
+#pragma unroll 1
+          for (int kb = s.kb0; kb < s.kb1 && open(NT * 128); ++kb) {
+            tma_load_2d(ring + st * slot + 2 * TC_TILE, &maps.x, smem_addr(&C.bfull[st]), kb * TC_KB, 0);
+            next();
+          }
+          u += s.kb1 - s.kb0;
+        }
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (v0 < v1 && alive && !wait_count(bar + half, G, a.err, 711)) {
+          *abort_flag = 1;
+          alive = false;
+        }
+        fence_async_all();  // the other CTAs' h is read by copies
+        for (int v = v0; v < v1 && alive;) {
+          const Seg s = down_seg(R, v, v1, half, per, KD);
+          const uint32_t bytes = pad16(s.n) * 256;
+          const char* src = static_cast<const char*>(a.h) + ((int64_t)s.kb0 * blocks + s.block) * 4096;
+#pragma unroll 1
+          for (int kb = s.kb0; kb < s.kb1;) {
+            const int nk = down_units(s, kb);
+            if (!open(nk * bytes)) break;
+            const uint32_t fb = smem_addr(&C.bfull[st]), sB = ring + st * slot + nk * TC_TILE;
+            load_bytes(sB, src, bytes, fb);
+            if (nk == 2) load_bytes(sB + bytes, src + (int64_t)blocks * 4096, bytes, fb);
+            next();
+            kb += nk;
+            src += (int64_t)nk * blocks * 4096;
           }
           v += s.kb1 - s.kb0;
         }
       }
-      if (!alive) {  // wait for the copies in flight
-        const int n = issued < nst ? issued : nst;
-        int s = st;
-        uint32_t ph = phase;
-        for (int i = 0; i < n; ++i) {
-          if (--s < 0) {
-            s = nst - 1;
-            ph ^= 1u;
-          }
-          for (uint32_t it = 0; it < (1u << 20) && !mbar_try_wait(smem_addr(&C.full[s]), ph); ++it) {
-          }
-        }
-      }
+      if (!alive) settle();
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -332,12 +383,14 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
       };
       auto open = [&]() {  // the segment's accumulator is free
         const uint32_t par = ((seg >> 1) & 1) ^ 1;
-        if (!mbar_wait(smem_addr(&C.tempty[seg & 1]), par, abort_flag, a.err, 720)) alive = false;
+        if (!ring_wait(&C.tempty[seg & 1], par, abort_flag, a.err, 720)) alive = false;
         tc_fence_after();
         return alive;
       };
       auto filled = [&]() {
-        if (!mbar_wait(smem_addr(&C.full[st]), phase, abort_flag, a.err, 721)) alive = false;
+        if (!ring_wait(&C.wfull[st], phase, abort_flag, a.err, 721) ||
+            !ring_wait(&C.bfull[st], phase, abort_flag, a.err, 722))
+          alive = false;
         tc_fence_after();
         return alive;
       };
@@ -345,14 +398,15 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
         for (int u = u0; u < u1 && alive && open();) {
           const Seg s = up_seg(R, u, u1, half, FT, KU);
           const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(NT);
+#pragma unroll 1
           for (int kb = s.kb0; kb < s.kb1 && filled(); ++kb) {
-            const uint32_t sA = ring + st * slot, sB = sA + 2 * TC_TILE;
-#pragma unroll
-            for (int q = 0; q < TC_KB / 16; ++q) {
-              const uint64_t bd = sdesc(sB + q * 32, 16, 1024);
-              const uint32_t on = kb != s.kb0 || q != 0;
-              umma_bf16(acc, sdesc(sA + q * 2048, 8192, 1024), bd, id, on);
-              umma_bf16(acc + TC_B, sdesc(sA + TC_TILE + q * 2048, 8192, 1024), bd, id, on);
+            // descriptors of the following K steps differ in the address alone (in 16-byte units)
+            uint64_t ad = sdesc(ring + st * slot, 8192, 1024), bd = sdesc(ring + st * slot + 2 * TC_TILE, 16, 1024);
+            uint32_t on = kb != s.kb0;
+#pragma unroll 1
+            for (int q = 0; q < TC_KB / 16; ++q, ad += 2048 / 16, bd += 32 / 16, on = 1) {
+              umma_bf16(acc, ad, bd, id, on);
+              umma_bf16(acc + TC_B, ad + TC_TILE / 16, bd, id, on);
             }
             advance();
           }
@@ -366,16 +420,17 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
           const Seg s = down_seg(R, v, v1, half, per, KD);
           const int n16 = pad16(s.n);
           const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(n16);
+#pragma unroll 1
           for (int kb = s.kb0; kb < s.kb1 && filled();) {
             const int nk = down_units(s, kb);
-            for (int i = 0; i < nk; ++i) {
-              const uint32_t sA = ring + st * slot + i * TC_TILE;
-              const uint32_t sB = ring + st * slot + nk * TC_TILE + i * 2 * n16 * 128;
-#pragma unroll
-              for (int q = 0; q < TC_KB / 16; ++q) {
-                const uint64_t ad = sdesc(sA + q * 2048, 8192, 1024);
-                umma_bf16(acc, ad, sdesc(sB + q * 32, 16, 1024), id, kb + i != s.kb0 || q != 0);
-                umma_bf16(acc, ad, sdesc(sB + n16 * 128 + q * 32, 16, 1024), id, 1);
+            uint64_t ad = sdesc(ring + st * slot, 8192, 1024), bd = sdesc(ring + st * slot + nk * TC_TILE, 16, 1024);
+            uint32_t on = kb != s.kb0;
+#pragma unroll 1
+            for (int i = 0; i < nk; ++i, ad += (TC_TILE - 8192) / 16, bd += (2 * n16 * 128 - 128) / 16) {
+#pragma unroll 1
+              for (int q = 0; q < TC_KB / 16; ++q, ad += 2048 / 16, bd += 32 / 16, on = 1) {
+                umma_bf16(acc, ad, bd, id, on);
+                umma_bf16(acc, ad, bd + n16 * 128 / 16, id, 1);
               }
             }
             advance();
@@ -407,7 +462,6 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
       ++seg;
     };
     auto signal = [&](uint32_t* ctr) {  // this CTA's part is written
-      __threadfence();
       epi_sync();
       if (tid == 0) red_release(ctr);
     };
@@ -419,7 +473,6 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
     };
 
     // ---- up product ----
-    __nv_bfloat16* h = static_cast<__nv_bfloat16*>(a.h);
     const int64_t pslot = (int64_t)a.T * 2 * DEC_N;
     for (int half = 0; half < 2 && alive; ++half) {
       float* parts = a.up_part + (int64_t)half * G * 2 * pslot;
@@ -434,7 +487,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
           const uint32_t at = tmem + lanes + (seg & 1) * TC_BUF + R.tok[row];
           const float2 v = tmem_ld_ab(at);
           if (whole) {
-            put_h(h, row, a.f, s.c0 + col, R.gate[row] * silu_bf16(v.x) * v.y);
+            put_h(h_at(a, blocks, s, m, s.c0 + col), pad16(s.n), R.gate[row] * silu_bf16(v.x) * v.y);
           } else {
             part[m * 2 * DEC_N] = v.x;
             part[m * 2 * DEC_N + DEC_N] = v.y;
@@ -475,7 +528,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
               const float gate = R.gate[s.base + m];
               const float v[4] = {gate * silu_bf16(va.x) * vb.x, gate * silu_bf16(va.y) * vb.y,
                                   gate * silu_bf16(va.z) * vb.z, gate * silu_bf16(va.w) * vb.w};
-              put_h4(h, s.base + m, a.f, s.c0 + cc, v);
+              put_h4(h_at(a, blocks, s, m, s.c0 + cc), pad16(s.n), v);
             }
           }
         }
@@ -573,31 +626,39 @@ bool dec_encode_ready() {
   return dec_encode != nullptr;
 }
 
-// 2-D bf16 tensor map of dense rows, boxes of 64 columns, 128-byte swizzle.
-bool dec_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return dec_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+// bf16 rows in boxes of 64 columns, 128-byte swizzle: x as [rows][cols], weights
+// as [cols / 64][rows][64] with two neighbouring chunks of columns to a box.
+bool dec_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows, bool weights) {
+  cuuint64_t dims[3] = {weights ? 64 : cols, rows, cols / 64};
+  cuuint64_t strides[2] = {cols * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return dec_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, weights ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Most blocks of 16 rows of h: every expert with rows begins one.
+int h_blocks(const Shape& s) {
+  const int Tk = s.T * s.k, experts = s.E < Tk ? s.E : Tk;
+  return (Tk + 15 * experts) / 16;
+}
+
 }  // namespace
+
+size_t decode_tc_h_bytes(const Shape& s) { return (size_t)(s.f / 64) * h_blocks(s) * 4096; }
 
 cudaError_t launch_decode_tc(const Shape& s, const DecodeArgs& args, int G, cudaStream_t st) {
   if (!dec_encode_ready()) return cudaErrorNotSupported;
   DecodeArgs a = args;
   const uint32_t NT = (uint32_t)(s.T + 15) / 16 * 16;
-  int slot = 2 * TC_TILE + 8192;  // two weight tiles, and 64 tokens of x or two units' hi and lo of 16 rows of h
   const int fixed = 1024 + (int)sizeof(Routing) + (int)sizeof(TcCtrl) + s.T * DEC_N * 4;
-  int nst = (TC_SMEM_MAX - fixed) / slot;
+  int nst = (TC_SMEM_MAX - fixed) / TC_SLOT, blocks = h_blocks(s);
   if (nst > TC_MAX_ST) nst = TC_MAX_ST;
   TcMapsD m;
-  if (!dec_map(&m.x, a.io.x, s.T, s.d, NT) || !dec_map(&m.W1, a.io.W1, (uint64_t)s.E * s.d, s.f, 64) ||
-      !dec_map(&m.W3, a.io.W3, (uint64_t)s.E * s.d, s.f, 64) || !dec_map(&m.W2, a.io.W2, (uint64_t)s.E * s.f, s.d, 64) ||
-      !dec_map(&m.h, a.h, (uint64_t)s.T * s.k, 2 * (uint64_t)s.f, 16))
+  if (!dec_map(&m.x, a.io.x, s.T, s.d, NT, false) || !dec_map(&m.W1, a.io.W1, (uint64_t)s.E * s.d, s.f, 64, true) ||
+      !dec_map(&m.W3, a.io.W3, (uint64_t)s.E * s.d, s.f, 64, true) ||
+      !dec_map(&m.W2, a.io.W2, (uint64_t)s.E * s.f, s.d, 64, true))
     return cudaErrorInvalidValue;
   static bool attr_done[64] = {false};
   int dev = 0;
@@ -609,10 +670,10 @@ cudaError_t launch_decode_tc(const Shape& s, const DecodeArgs& args, int G, cuda
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
-  void* params[] = {&m, &a, &nst, &slot};
+  void* params[] = {&m, &a, &nst, &blocks};
   LaunchScope ls(KK_DECODE, st);
   return cudaLaunchCooperativeKernel((const void*)decode_tc_kernel, dim3(G), dim3(TC_NT), params,
-                                     (size_t)(fixed + nst * slot), st);
+                                     (size_t)(fixed + nst * TC_SLOT), st);
 }
 
 }  // namespace moe
