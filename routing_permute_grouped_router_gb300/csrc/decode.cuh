@@ -102,7 +102,7 @@ struct Split {
 // the loops from here on are kept rolled and the bodies short (the unrolled
 // forms of the score, pick and epilogue loops cost a one-token step 20 us).
 struct ScoreScratch {
-  float w[4096];            // rows of W_r
+  float w[8192];            // rows of W_r
   float x[256 * DEC_TG];    // the same columns of the tokens
   float red[256 * DEC_TG];
 };
@@ -119,7 +119,7 @@ __device__ __forceinline__ void score_slice(const DecodeArgs& a, ScoreScratch& s
   const int ep = pow2_at_least(a.E), subs = 256 / ep;
   const int e = threadIdx.x & (ep - 1), sub = threadIdx.x / ep, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const bool on = threadIdx.x < 256 && e < a.E;
-  const int most = 4096 / a.E < 256 ? 4096 / a.E : 256;
+  const int most = 8192 / a.E < 256 ? 8192 / a.E : 256;
   float acc[DEC_TG];
 #pragma unroll
   for (int t = 0; t < DEC_TG; ++t) acc[t] = 0.f;
@@ -130,11 +130,21 @@ __device__ __forceinline__ void score_slice(const DecodeArgs& a, ScoreScratch& s
     const float* W = a.io.W_r + (int64_t)c0 * a.E;
     const T* x = static_cast<const T*>(a.io.x) + (int64_t)(t0 + warp) * a.d + c0;
     const bool live = warp < DEC_TG && t0 + warp < a.T;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < n * a.E; i += NT) s.w[i] = __ldg(W + i);
+    // loads in guarded batches: the rest of an unrolled loop would take them one latency at a time
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = live && lane + 32 * j < n ? to_f32(x[lane + 32 * j]) : 0.f;
     if (warp < DEC_TG) {
-#pragma unroll 4
-      for (int r = lane; r < n; r += 32) s.x[r * DEC_TG + warp] = live ? to_f32(x[r]) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s.x[(lane + 32 * j) * DEC_TG + warp] = v[j];
+    }
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < n * a.E; i0 += 8 * NT) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = i0 + j * NT < n * a.E ? __ldg(W + i0 + j * NT) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i0 + j * NT < n * a.E) s.w[i0 + j * NT] = v[j];
     }
     __syncthreads();
     if (on) {
@@ -185,58 +195,56 @@ __device__ __forceinline__ void pick_experts(const DecodeArgs& a, ScoreScratch& 
     const int e = i & (ep - 1), t = (i / ep) & (np - 1), sub = i / pairs;
     float v = 0.f;
     if (e < a.E && t < n) {
-#pragma unroll 8
-      for (int q = sub; q < a.slices; q += subs) v += __ldcg(part + q * step + t * a.E + e);
+#pragma unroll 1
+      for (int q0 = sub; q0 < a.slices; q0 += 8 * subs) {
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = q0 + j * subs < a.slices ? __ldcg(part + (q0 + j * subs) * step + t * a.E + e) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v += w[j];
+      }
     }
     s.red[(t * subs + sub) * ep + e] = v;
   }
   __syncthreads();
   if (warp >= n) return;
   float* lg = s.x + warp * DEC_E;  // the token's logits
-  float v[DEC_E / 32];
-  float mx = -INFINITY;
+  uint32_t key[DEC_E / 32];        // ordered as the logits are; 0 for what cannot be picked
 #pragma unroll
   for (int c = 0; c < DEC_E / 32; ++c) {
     const int e = lane + 32 * c;
-    float sc = -INFINITY;
+    key[c] = 0;
     if (e < a.E) {
-      sc = a.io.bias ? __ldg(a.io.bias + e) : 0.f;
+      float sc = a.io.bias ? __ldg(a.io.bias + e) : 0.f;
 #pragma unroll 1
       for (int q = 0; q < subs; ++q) sc += s.red[(warp * subs + q) * ep + e];
-      if (isnan(sc)) sc = -INFINITY;
+      sc = isnan(sc) ? -INFINITY : sc + 0.f;  // -0 as 0
+      lg[e] = sc;
+      const uint32_t u = __float_as_uint(sc);
+      key[c] = u & 0x80000000u ? ~u : u | 0x80000000u;
     }
-    lg[e] = v[c] = sc;
-    mx = fmaxf(mx, sc);
   }
-#pragma unroll 1
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  uint32_t taken = 0;
-  float mine = -INFINITY;  // lane j keeps the j-th pick and its logit
+  float mx = 0.f, mine = 0.f;  // lane j keeps the j-th pick and its logit
   int pick = 0;
 #pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
-    float bv = -INFINITY;
+    uint32_t bk = 0;
     int be = 0x7fffffff;
 #pragma unroll
-    for (int c = 0; c < DEC_E / 32; ++c) {
-      const int e = lane + 32 * c;
-      if (e < a.E && !((taken >> c) & 1u) && (v[c] > bv || (v[c] == bv && e < be))) {
-        bv = v[c];
-        be = e;
+    for (int c = 0; c < DEC_E / 32; ++c)
+      if (key[c] > bk) {
+        bk = key[c];
+        be = lane + 32 * c;
       }
-    }
-#pragma unroll 1
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (ov > bv || (ov == bv && oe < be)) {
-        bv = ov;
-        be = oe;
-      }
-    }
-    if ((be & 31) == lane) taken |= 1u << (be >> 5);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, bk);
+    be = __reduce_min_sync(0xffffffffu, bk == top ? be : 0x7fffffff);
+#pragma unroll
+    for (int c = 0; c < DEC_E / 32; ++c)
+      if (be == lane + 32 * c) key[c] = 0;
+    const float v = __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
+    if (j == 0) mx = v;
     if (lane == j) {
-      mine = bv;
+      mine = v;
       pick = be;
     }
   }

@@ -17,9 +17,10 @@
 // Both products are done in two halves of f, in the order up 0, up 1, down 0,
 // down 1: the exchange of the partial sums of one half and the grid barrier
 // behind its h (some 5 us) run under the stream of the next part's weights.
-// h is split into two bf16 parts, hi + lo, whose products go to the same
-// accumulator: 16 significant bits where one bf16 would round h to 8 and
-// double the error of y.  The second product is free here.
+// h is split into two bf16 parts, hi + lo, side by side in the N dimension: 16
+// significant bits where one bf16 would round h to 8 and double the square of
+// y's error.  The second product is free here: an MMA of this shape is bound by
+// reading its 4 KB of A.
 #include <cudaTypedefs.h>
 
 #include "decode.cuh"
@@ -141,15 +142,17 @@ __device__ __forceinline__ float2 tmem_ld_ab(uint32_t at) {
       : "memory");
   return v;
 }
-__device__ __forceinline__ float4 tmem_ld4(uint32_t at) {
-  float4 v;
+// four columns and the four `lo` columns behind them, added
+__device__ __forceinline__ float4 tmem_ld4_sum(uint32_t at, int lo) {
+  float4 v, w;
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%4, %5, %6, %7}, [%9];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w)
-      : "r"(at)
+      : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w), "=&f"(w.x), "=&f"(w.y), "=&f"(w.z), "=&f"(w.w)
+      : "r"(at), "r"(at + lo)
       : "memory");
-  return v;
+  return make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
 }
 __device__ __forceinline__ void add4(float4& v, const float4& w) {
   v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
         for (int v = v0; v < v1 && alive && open();) {
           const Seg s = down_seg(R, v, v1, half, per, KD);
           const int n16 = pad16(s.n);
-          const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(n16);
+          const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(2 * n16);
 #pragma unroll 1
           for (int kb = s.kb0; kb < s.kb1 && filled();) {
             const int nk = down_units(s, kb);
@@ -428,10 +431,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
 #pragma unroll 1
             for (int i = 0; i < nk; ++i, ad += (TC_TILE - 8192) / 16, bd += (2 * n16 * 128 - 128) / 16) {
 #pragma unroll 1
-              for (int q = 0; q < TC_KB / 16; ++q, ad += 2048 / 16, bd += 32 / 16, on = 1) {
-                umma_bf16(acc, ad, bd, id, on);
-                umma_bf16(acc, ad, bd + n16 * 128 / 16, id, 1);
-              }
+              for (int q = 0; q < TC_KB / 16; ++q, ad += 2048 / 16, bd += 32 / 16, on = 1) umma_bf16(acc, ad, bd, id, on);
             }
             advance();
             kb += nk;
@@ -512,11 +512,24 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
             const int j = jb + tid / L, m = j / (DEC_N / 4), cc = j % (DEC_N / 4) * 4;
             float4 va = make_float4(0.f, 0.f, 0.f, 0.f), vb = va;
             if (j < j1) {
-#pragma unroll 4
-              for (int g = sub; g < segs; g += L) {
-                const float4* p = reinterpret_cast<const float4*>(p0 + (g == 0 ? 0 : g * 2 - 1) * pslot + m * 2 * DEC_N + cc);
-                add4(va, __ldcg(p));
-                add4(vb, __ldcg(p + DEC_N / 4));
+#pragma unroll 1
+              for (int g0 = sub; g0 < segs; g0 += 4 * L) {
+                float4 x[4], z[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int g = g0 + i * L;
+                  const float4* p = reinterpret_cast<const float4*>(p0 + (g == 0 ? 0 : g * 2 - 1) * pslot + m * 2 * DEC_N + cc);
+                  x[i] = z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (g < segs) {
+                    x[i] = __ldcg(p);
+                    z[i] = __ldcg(p + DEC_N / 4);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  add4(va, x[i]);
+                  add4(vb, z[i]);
+                }
               }
             }
 #pragma unroll 1
@@ -545,7 +558,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
         const Seg s = down_seg(R, v, v1, half, per, KD);
 #pragma unroll 1
         for (int m0 = 0; m0 < s.n; m0 += 4) {
-          const float4 r = tmem_ld4(tmem + lanes + (seg & 1) * TC_BUF + m0);
+          const float4 r = tmem_ld4_sum(tmem + lanes + (seg & 1) * TC_BUF + m0, pad16(s.n));
           const uint8_t* tok = R.tok + s.base + m0;
           yacc[tok[0] * DEC_N + col] += r.x;
           if (m0 + 1 < s.n) yacc[tok[1] * DEC_N + col] += r.y;
@@ -590,9 +603,17 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
     if (on && R.nact > 0) {
       const int dt = col / DEC_N, first = down.owner(dt * per), n = down.owner((dt + 1) * per - 1) - first + 1;
       const float* p = a.down_part + (int64_t)(first + dt) * dslot + t * DEC_N + col % DEC_N;
-#pragma unroll 4
-      for (int g = sub; g < 2 * n; g += L) {
-        add4(v, __ldcg(reinterpret_cast<const float4*>(p + (int64_t)(g < n ? g : G + DT + g - n) * dslot)));
+#pragma unroll 1
+      for (int g0 = sub; g0 < 2 * n; g0 += 8 * L) {
+        float4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int g = g0 + j * L;
+          w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (g < 2 * n) w[j] = __ldcg(reinterpret_cast<const float4*>(p + (int64_t)(g < n ? g : G + DT + g - n) * dslot));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) add4(v, w[j]);
       }
     }
 #pragma unroll 1
