@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(SM_NT, 1) decode_kernel(const __grid_constant_
 inline size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct DecodeWs {
-  size_t score, ids, gates, ctr, h, up, down, total;
+  size_t score, ids, gates, ctr, h, up, whole, down, total;
 };
 DecodeWs decode_ws(const Shape& s) {
   const size_t G = sm_count(), T = s.T, DT = (s.d + DEC_N - 1) / DEC_N;
@@ -243,7 +243,8 @@ DecodeWs decode_ws(const Shape& s) {
   w.ctr = w.gates + up256(T * s.k * 4);
   w.h = w.ctr + up256((2 * G + 3) * 4);
   w.up = w.h + up256(s.bf16 ? decode_tc_h_bytes(s) : T * s.k * s.f * 4);
-  w.down = w.up + up256(2 * G * 2 * T * 2 * DEC_N * 4);
+  w.whole = w.up + up256(2 * G * 2 * T * 2 * DEC_N * 4);
+  w.down = w.whole + up256(s.bf16 ? decode_tc_whole_bytes(s) : 0);
   w.total = w.down + up256(2 * (G + DT) * T * DEC_N * 4);
   return w;
 }
@@ -280,6 +281,7 @@ cudaError_t launch_decode(const Shape& s, const DecodeIo& io, void* ws, uint32_t
   a.ctr = reinterpret_cast<uint32_t*>(base + w.ctr);
   a.h = base + w.h;
   a.up_part = reinterpret_cast<float*>(base + w.up);
+  a.up_whole = reinterpret_cast<float*>(base + w.whole);
   a.down_part = reinterpret_cast<float*>(base + w.down);
   a.err = err;
   a.T = s.T;

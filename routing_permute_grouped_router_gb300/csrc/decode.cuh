@@ -21,6 +21,7 @@ struct DecodeArgs {
   uint32_t* ctr;      // [2 G + 3]: arrivals at split tiles and grid barriers
   void* h;            // rows of the experts, gate * silu(a) * b: [T k][f] fp32, or tiles of bf16 (decode_tc.cu)
   float* up_part;     // [2][G][2][T][2 * DEC_N] a and b of split tiles
+  float* up_whole;    // [T k][f / DEC_N][2 * DEC_N] a and b of tiles that are not split (decode_tc.cu, few rows)
   float* down_part;   // [2][G + column tiles][T][DEC_N] sums of the CTAs over their part of a column tile
   uint32_t* err;
   int T, d, f, E, k, cap;
@@ -28,6 +29,7 @@ struct DecodeArgs {
 };
 // decode_tc.cu: bf16 layers, G CTAs
 size_t decode_tc_h_bytes(const Shape& s);
+size_t decode_tc_whole_bytes(const Shape& s);
 cudaError_t launch_decode_tc(const Shape& s, const DecodeArgs& args, int G, cudaStream_t st);
 
 namespace {
@@ -106,6 +108,10 @@ struct ScoreScratch {
   float x[256 * DEC_TG];    // the same columns of the tokens
   float red[256 * DEC_TG];
 };
+__device__ __forceinline__ void copy4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
 __device__ __forceinline__ int pow2_at_least(int e) { return e <= 1 ? 1 : 1 << (32 - __clz(e - 1)); }
 
 // Partial logits of DEC_TG tokens over one slice of d, so W_r is read once a
@@ -130,7 +136,10 @@ __device__ __forceinline__ void score_slice(const DecodeArgs& a, ScoreScratch& s
     const float* W = a.io.W_r + (int64_t)c0 * a.E;
     const T* x = static_cast<const T*>(a.io.x) + (int64_t)(t0 + warp) * a.d + c0;
     const bool live = warp < DEC_TG && t0 + warp < a.T;
-    // loads in guarded batches: the rest of an unrolled loop would take them one latency at a time
+    // all loads at once: W_r by asynchronous copies, x in a guarded batch (the
+    // rest of an unrolled loop would take them one latency at a time)
+#pragma unroll 2
+    for (int i = threadIdx.x; i < n * a.E; i += NT) copy4(s.w + i, W + i);
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = live && lane + 32 * j < n ? to_f32(x[lane + 32 * j]) : 0.f;
@@ -138,14 +147,7 @@ __device__ __forceinline__ void score_slice(const DecodeArgs& a, ScoreScratch& s
 #pragma unroll
       for (int j = 0; j < 8; ++j) s.x[(lane + 32 * j) * DEC_TG + warp] = v[j];
     }
-#pragma unroll 1
-    for (int i0 = threadIdx.x; i0 < n * a.E; i0 += 8 * NT) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = i0 + j * NT < n * a.E ? __ldg(W + i0 + j * NT) : 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i0 + j * NT < n * a.E) s.w[i0 + j * NT] = v[j];
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (on) {
 #pragma unroll 2
@@ -295,8 +297,13 @@ __device__ __forceinline__ void list_rows(const DecodeArgs& a, Routing& R) {
       const int u = __shfl_up_sync(0xffffffffu, pre, o);
       if (lane >= o) pre += u;
     }
-    if (lane == 31) R.nact = pre >> 16;
+    const int nact = __shfl_sync(0xffffffffu, pre, 31) >> 16;
+    if (lane == 0) R.nact = nact;
     pre -= own;
+    // The r-th expert with rows is the (r * stride mod nact)-th of the list:
+    // experts of neighbouring indices, which can all be popular, go to
+    // different CTAs.  64 tokens of the Zipf-routed dropless layer: 3 us.
+    const int stride = nact % 37 != 0 ? 37 : 41;
     int blocks = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) blocks += (c[q] + 15) / 16;
@@ -313,7 +320,7 @@ __device__ __forceinline__ void list_rows(const DecodeArgs& a, Routing& R) {
       at += (c[q] + 15) / 16;
       R.base[lane * 4 + q] = (int16_t)(pre & 0xffff);
       if (c[q] > 0) {
-        R.act[pre >> 16] = (uint8_t)(lane * 4 + q);
+        R.act[(pre >> 16) * stride % nact] = (uint8_t)(lane * 4 + q);
         pre += c[q] + (1 << 16);
       }
     }

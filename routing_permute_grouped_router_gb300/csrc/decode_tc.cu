@@ -35,6 +35,7 @@ constexpr int TC_TILE = DEC_N * TC_KB * 2;  // 16 KB: two boxes of 64 columns x 
 constexpr int TC_MAX_ST = 8;
 constexpr int TC_SLOT = 2 * TC_TILE + 8192;  // and 64 tokens of x, or two units' hi and lo of 16 rows of h
 constexpr int TC_QUEUE = 6;
+constexpr int TC_DIRECT_ROWS = 64;  // most picks of a call whose CTAs build h themselves
 constexpr int TC_SMEM_MAX = 232448;       // 227 KB a CTA
 constexpr uint32_t TC_COLS = 256;         // TMEM: two accumulators of a and b, 64 tokens each
 constexpr uint32_t TC_BUF = 128, TC_B = 64;
@@ -71,7 +72,7 @@ __host__ __device__ constexpr uint32_t dec_idesc(int n) {  // fp32 D, bf16 A (MN
 
 // A CTA's consecutive units of one weight tile.
 struct Seg {
-  int e, n, base, block;  // expert, its rows, the first of them, its first block of rows of h
+  int ai, e, n, base, block;  // place in the list, expert, its rows, the first of them, its first block of rows of h
   int c0;          // first weight column
   int kb0, kb1;    // units
   int tile;        // up: the weight tile; down: the column tile of y
@@ -83,6 +84,7 @@ __device__ __forceinline__ Seg up_seg(const Routing& R, int u, int u1, int half,
   s.kb0 = u - s.tile * KU;
   s.kb1 = u1 - s.tile * KU < KU ? u1 - s.tile * KU : KU;
   const int ai = s.tile / FT;
+  s.ai = ai;
   s.e = R.act[ai];
   s.c0 = (half * FT + s.tile - ai * FT) * DEC_N;
   s.n = R.cnt[s.e];
@@ -98,6 +100,7 @@ __device__ __forceinline__ Seg down_seg(const Routing& R, int u, int u1, int hal
   s.kb1 = u1 - u < KD - s.kb0 ? s.kb0 + u1 - u : KD;
   s.kb0 += half * KD;
   s.kb1 += half * KD;
+  s.ai = ai;
   s.e = R.act[ai];
   s.c0 = s.tile * DEC_N;
   s.n = R.cnt[s.e];
@@ -179,16 +182,36 @@ __device__ __forceinline__ void put_h(char* p, int n16, float v) {
   *reinterpret_cast<__nv_bfloat16*>(p) = hi;
   *reinterpret_cast<__nv_bfloat16*>(p + n16 * 128) = __float2bfloat16_rn(lo_part(v, __bfloat162float(hi)));
 }
-__device__ __forceinline__ void put_h4(char* p, int n16, const float (&v)[4]) {
+__device__ __forceinline__ void split4(const float4& v, __nv_bfloat162 (&hi)[2], __nv_bfloat162 (&lo)[2]) {
+  hi[0] = __floats2bfloat162_rn(v.x, v.y);
+  hi[1] = __floats2bfloat162_rn(v.z, v.w);
+  const float2 p = __bfloat1622float2(hi[0]), q = __bfloat1622float2(hi[1]);
+  lo[0] = __floats2bfloat162_rn(lo_part(v.x, p.x), lo_part(v.y, p.y));
+  lo[1] = __floats2bfloat162_rn(lo_part(v.z, q.x), lo_part(v.w, q.y));
+}
+__device__ __forceinline__ void put_h4(char* p, int n16, const float4& v) {
   __nv_bfloat162 hi[2], lo[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    hi[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    const float2 w = __bfloat1622float2(hi[i]);
-    lo[i] = __floats2bfloat162_rn(lo_part(v[2 * i], w.x), lo_part(v[2 * i + 1], w.y));
-  }
+  split4(v, hi, lo);
   *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(hi);
   *reinterpret_cast<uint2*>(p + n16 * 128) = *reinterpret_cast<const uint2*>(lo);
+}
+
+__device__ __forceinline__ float4 swiglu4(float gate, const float4& a, const float4& b) {
+  return make_float4(gate * silu_bf16(a.x) * b.x, gate * silu_bf16(a.y) * b.y, gate * silu_bf16(a.z) * b.z,
+                     gate * silu_bf16(a.w) * b.w);
+}
+// The parts of a split tile: the first CTA's is its second, the others' are
+// their first, counted from the first CTA's second.
+__device__ __forceinline__ int part_at(int g) { return g == 0 ? 0 : g * 2 - 1; }
+// item j of a tile: four columns of a row
+__device__ __forceinline__ int item_at(int j) { return j / (DEC_N / 4) * 2 * DEC_N + j % (DEC_N / 4) * 4; }
+__device__ __forceinline__ void load_ab(const float* p, float4& a, float4& b) {
+  a = __ldcg(reinterpret_cast<const float4*>(p));
+  b = __ldcg(reinterpret_cast<const float4*>(p + DEC_N));
+}
+// a and b of row `row` and columns c0.. (a whole tile's)
+__device__ __forceinline__ float* up_whole(const DecodeArgs& a, int row, int c0) {
+  return a.up_whole + (int64_t)row * a.f * 2 + c0 * 2;
 }
 
 // After a wait that gave up: the copies in flight land within this time.
@@ -245,7 +268,12 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
   const Split up(R.nact * FT * KU, G), down(per * DT, G);
   const int u0 = up.begin(c), u1 = up.begin(c + 1), v0 = down.begin(c), v1 = down.begin(c + 1);
   uint32_t* bar = a.ctr + 2 * G;  // h of half 0, of half 1, the partial sums of y
-  const int64_t dslot = (int64_t)a.T * DEC_N;
+  const int64_t dslot = (int64_t)a.T * DEC_N, pslot = (int64_t)a.T * 2 * DEC_N;
+  // Few rows: the partial sums of the up product go straight to the CTAs of the
+  // down product, which add them and make h for themselves.  That repeats the
+  // sums in every column tile of y but saves an exchange (a fence, a wait and a
+  // barrier of some 2 us each under load).
+  const bool direct = a.T * a.k <= TC_DIRECT_ROWS && a.T * a.k <= 2 * R.nact;
 
   if (warp == 0) {
     // ---- weights ----
@@ -317,7 +345,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
         }
       if (!alive) settle();
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 && !direct) {
     // ---- tokens: x, then h ----
     if (lane == 0) {
       int st = 0;
@@ -372,6 +400,93 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
       }
       if (!alive) settle();
     }
+  } else if (direct && (warp == 2 || warp == 3)) {
+    // ---- tokens of few rows: x as above, then h from the partial sums; the two warps take stages in turn ----
+    int st = 0, turn = 0;
+    uint32_t phase = 0;
+    bool alive = true;
+    auto next = [&]() {
+      turn ^= 1;
+      if (++st == nst) {
+        st = 0;
+        phase ^= 1u;
+      }
+    };
+    auto open = [&]() {
+      const bool ok = ring_wait(&C.empty[st], phase ^ 1u, abort_flag, a.err, 714);
+      return alive = __all_sync(0xffffffffu, ok);
+    };
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half)
+      for (int u = u0; u < u1 && alive;) {
+        const Seg s = up_seg(R, u, u1, half, FT, KU);
+#pragma unroll 1
+        for (int kb = s.kb0; kb < s.kb1; ++kb) {
+          if (turn == warp - 2) {
+            if (!open()) break;
+            if (lane == 0) {
+              mbar_expect_tx(smem_addr(&C.bfull[st]), NT * 128);
+              tma_load_2d(ring + st * slot + 2 * TC_TILE, &maps.x, smem_addr(&C.bfull[st]), kb * TC_KB, 0);
+            }
+          }
+          next();
+        }
+        u += s.kb1 - s.kb0;
+      }
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const float* parts = a.up_part + (int64_t)half * G * 2 * pslot;
+      if (v0 < v1 && alive) {
+        const bool ok = lane != 0 || wait_count(bar + half, G, a.err, 715);
+        alive = __all_sync(0xffffffffu, ok);
+        if (!alive) *abort_flag = 1;
+      }
+      for (int v = v0; v < v1 && alive;) {
+        const Seg s = down_seg(R, v, v1, half, per, KD);
+        const int n16 = pad16(s.n);
+#pragma unroll 1
+        for (int kb = s.kb0; kb < s.kb1;) {
+          const int nk = down_units(s, kb);
+          if (turn == warp - 2) {
+            if (!open()) break;
+            char* sB = reinterpret_cast<char*>(smem + st * slot + nk * TC_TILE);
+#pragma unroll 1
+            for (int i = lane; i < nk * s.n * (TC_KB / 4); i += 32) {
+              const int r = i / (TC_KB / 4), m = r % s.n, q = r / s.n;  // row m of unit q, four columns
+              const int at = i % (TC_KB / 4) * 4, col = (kb + q) * TC_KB + at;
+              const int tile = s.ai * FT + col / DEC_N - half * FT;
+              const int first = up.owner(tile * KU), segs = up.owner(tile * KU + KU - 1) - first + 1;
+              const float* p = segs == 1 ? up_whole(a, s.base + m, col / DEC_N * DEC_N) + col % DEC_N
+                                         : parts + ((int64_t)first * 2 + 1) * pslot + m * 2 * DEC_N + col % DEC_N;
+              float4 va = make_float4(0.f, 0.f, 0.f, 0.f), vb = va;
+#pragma unroll 1
+              for (int g0 = 0; g0 < segs; g0 += 8) {
+                float4 x[8], z[8];
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                  x[g] = z[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (g0 + g < segs) load_ab(p + part_at(g0 + g) * pslot, x[g], z[g]);
+                }
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                  add4(va, x[g]);
+                  add4(vb, z[g]);
+                }
+              }
+              put_h4(sB + q * n16 * 256 + m * 128 + (((at / 8) ^ (m & 7)) << 4) + at % 8 * 2, n16,
+                     swiglu4(R.gate[s.base + m], va, vb));
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&C.bfull[st]));
+          }
+          next();
+          kb += nk;
+        }
+        v += s.kb1 - s.kb0;
+      }
+    }
+    if (!alive) settle();
   } else if (warp == 1) {
     if (lane == 0) {
       int st = 0, seg = 0;
@@ -473,75 +588,70 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
     };
 
     // ---- up product ----
-    const int64_t pslot = (int64_t)a.T * 2 * DEC_N;
     for (int half = 0; half < 2 && alive; ++half) {
       float* parts = a.up_part + (int64_t)half * G * 2 * pslot;
       uint32_t* ctr = a.ctr + half * G;
       for (int u = u0; u < u1 && ready();) {
         const Seg s = up_seg(R, u, u1, half, FT, KU);
         const bool whole = s.kb0 == 0 && s.kb1 == KU;
-        float* part = parts + ((int64_t)c * 2 + (s.kb0 > 0 ? 0 : 1)) * pslot + col;
+        float* part = whole ? up_whole(a, s.base, s.c0) : parts + ((int64_t)c * 2 + (s.kb0 > 0 ? 0 : 1)) * pslot;
+        const int64_t step = whole ? (int64_t)a.f * 2 : 2 * DEC_N;
 #pragma unroll 1
         for (int m = 0; m < s.n; ++m) {  // the row's token is its column
           const int row = s.base + m;
-          const uint32_t at = tmem + lanes + (seg & 1) * TC_BUF + R.tok[row];
-          const float2 v = tmem_ld_ab(at);
-          if (whole) {
+          const float2 v = tmem_ld_ab(tmem + lanes + (seg & 1) * TC_BUF + R.tok[row]);
+          if (whole && !direct) {
             put_h(h_at(a, blocks, s, m, s.c0 + col), pad16(s.n), R.gate[row] * silu_bf16(v.x) * v.y);
           } else {
-            part[m * 2 * DEC_N] = v.x;
-            part[m * 2 * DEC_N + DEC_N] = v.y;
+            part[m * step + col] = v.x;
+            part[m * step + col + DEC_N] = v.y;
           }
         }
         release();
-        if (!whole) signal(ctr + up.owner(s.tile * KU));
+        if (!whole && !direct) signal(ctr + up.owner(s.tile * KU));
         u += s.kb1 - s.kb0;
       }
       // a share of each tile that other CTAs have a part of
-      for (int u = u0; u < u1 && alive;) {
-        const int64_t tile = u / KU, end = (tile + 1) * KU;
+      for (int u = u0; u < u1 && alive && !direct;) {
+        const int tile = u / KU, end = (tile + 1) * KU;
         const int first = up.owner(tile * KU), segs = up.owner(end - 1) - first + 1;
         if (segs > 1 && wait_all(ctr + first, segs, 731)) {
           const Seg s = up_seg(R, tile * KU, end, half, FT, KU);
-          const float* p0 = parts + ((int64_t)first * 2 + 1) * pslot;  // the first CTA's, then the others'
+          const float* p0 = parts + ((int64_t)first * 2 + 1) * pslot;
           const int N4 = s.n * (DEC_N / 4), j0 = (c - first) * N4 / segs, j1 = (c - first + 1) * N4 / segs;
-          // four columns to `L` threads, each some of the parts
-          const int L = j1 - j0 <= 16 ? 8 : 1, sub = tid % L;
+          // four columns to `L` threads, each some of the parts; two such items at once
+          int L = 8;
+          while (L > 1 && (j1 - j0) * L > 128) L /= 2;
+          const int sub = tid % L;
 #pragma unroll 1
-          for (int jb = j0; jb < j1; jb += 128 / L) {
-            const int j = jb + tid / L, m = j / (DEC_N / 4), cc = j % (DEC_N / 4) * 4;
-            float4 va = make_float4(0.f, 0.f, 0.f, 0.f), vb = va;
-            if (j < j1) {
+          for (int jb = j0 + tid / L; jb - tid / L < j1; jb += 256 / L) {
+            float4 va[2], vb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) va[i] = vb[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-              for (int g0 = sub; g0 < segs; g0 += 4 * L) {
-                float4 x[4], z[4];
+            for (int g0 = sub; g0 < segs; g0 += 2 * L) {
+              float4 x[4], z[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int g = g0 + i * L;
-                  const float4* p = reinterpret_cast<const float4*>(p0 + (g == 0 ? 0 : g * 2 - 1) * pslot + m * 2 * DEC_N + cc);
-                  x[i] = z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                  if (g < segs) {
-                    x[i] = __ldcg(p);
-                    z[i] = __ldcg(p + DEC_N / 4);
-                  }
-                }
+              for (int i = 0; i < 4; ++i) {
+                const int g = g0 + (i & 1) * L, j = jb + (i >> 1) * (128 / L);
+                x[i] = z[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (g < segs && j < j1) load_ab(p0 + part_at(g) * pslot + item_at(j), x[i], z[i]);
+              }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  add4(va, x[i]);
-                  add4(vb, z[i]);
-                }
+              for (int i = 0; i < 4; ++i) {
+                add4(va[i >> 1], x[i]);
+                add4(vb[i >> 1], z[i]);
               }
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll 1
-            for (int o = 1; o < L; o *= 2) {
-              xor4(va, o);
-              xor4(vb, o);
-            }
-            if (sub == 0 && j < j1) {
-              const float gate = R.gate[s.base + m];
-              const float v[4] = {gate * silu_bf16(va.x) * vb.x, gate * silu_bf16(va.y) * vb.y,
-                                  gate * silu_bf16(va.z) * vb.z, gate * silu_bf16(va.w) * vb.w};
-              put_h4(h_at(a, blocks, s, m, s.c0 + cc), pad16(s.n), v);
+              for (int o = 1; o < L; o *= 2) {
+                xor4(va[i], o);
+                xor4(vb[i], o);
+              }
+              const int j = jb + i * (128 / L), m = j / (DEC_N / 4), cc = j % (DEC_N / 4) * 4;
+              if (sub == 0 && j < j1) put_h4(h_at(a, blocks, s, m, s.c0 + cc), pad16(s.n), swiglu4(R.gate[s.base + m], va[i], vb[i]));
             }
           }
         }
@@ -667,6 +777,9 @@ int h_blocks(const Shape& s) {
 
 }  // namespace
 
+size_t decode_tc_whole_bytes(const Shape& s) {
+  return s.T * s.k <= TC_DIRECT_ROWS ? (size_t)s.T * s.k * s.f * 8 : 0;
+}
 size_t decode_tc_h_bytes(const Shape& s) { return (size_t)(s.f / 64) * h_blocks(s) * 4096; }
 
 cudaError_t launch_decode_tc(const Shape& s, const DecodeArgs& args, int G, cudaStream_t st) {
