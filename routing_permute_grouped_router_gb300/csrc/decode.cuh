@@ -53,7 +53,7 @@ struct alignas(16) Routing {
   int16_t base[DEC_E];     // first row of each expert
   int16_t block[DEC_E];    // first block of 16 rows of each expert, where each begins a block (bf16: rows of h)
   uint8_t act[DEC_E];      // experts with rows
-  int nact;
+  int nact, rows;          // experts with rows, and all their rows
 };
 
 __device__ __forceinline__ uint64_t dec_now() {
@@ -298,7 +298,10 @@ __device__ __forceinline__ void list_rows(const DecodeArgs& a, Routing& R) {
       if (lane >= o) pre += u;
     }
     const int nact = __shfl_sync(0xffffffffu, pre, 31) >> 16;
-    if (lane == 0) R.nact = nact;
+    if (lane == 31) {
+      R.nact = nact;
+      R.rows = pre & 0xffff;
+    }
     pre -= own;
     // The r-th expert with rows is the (r * stride mod nact)-th of the list:
     // experts of neighbouring indices, which can all be popular, go to

@@ -11,7 +11,7 @@
 //     of a W1 and a W3 tile and the same columns of all tokens; one of the down
 //     product 64 or 128 rows of f of a W2 tile and those columns of the
 //     expert's rows of h.
-//   warp 1, one lane: MMAs.  Two accumulators in turn, so the next segment's
+//   warp 1: MMAs.  Two accumulators in turn, so the next segment's
 //     products run under a segment's epilogue.
 //   warps 4-7: epilogue, one weight column a thread.
 // Both products are done in two halves of f, in the order up 0, up 1, down 0,
@@ -29,7 +29,7 @@
 namespace moe {
 namespace {
 
-constexpr int TC_NT = 256;
+constexpr int TC_NT = 320;
 constexpr int TC_KB = 64;                 // rows of a unit: 128 bytes of a token's row
 constexpr int TC_TILE = DEC_N * TC_KB * 2;  // 16 KB: two boxes of 64 columns x 64 rows
 constexpr int TC_MAX_ST = 8;
@@ -123,6 +123,23 @@ __device__ __forceinline__ void load_bytes(uint32_t dst, const void* src, uint32
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
+}
+// tcgen05.mma and its commit by one lane of a converged warp
+__device__ __forceinline__ void umma_elected(uint32_t d, uint64_t ad, uint64_t bd, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(id), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 // wait, the call only where the phase is not complete yet
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
@@ -273,7 +290,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
   // down product, which add them and make h for themselves.  That repeats the
   // sums in every column tile of y but saves an exchange (a fence, a wait and a
   // barrier of some 2 us each under load).
-  const bool direct = a.T * a.k <= TC_DIRECT_ROWS && a.T * a.k <= 2 * R.nact;
+  const bool direct = a.T * a.k <= TC_DIRECT_ROWS && R.rows <= 2 * R.nact;
 
   if (warp == 0) {
     // ---- weights ----
@@ -400,13 +417,13 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
       }
       if (!alive) settle();
     }
-  } else if (direct && (warp == 2 || warp == 3)) {
-    // ---- tokens of few rows: x as above, then h from the partial sums; the two warps take stages in turn ----
-    int st = 0, turn = 0;
+  } else if (direct && (warp == 2 || warp == 3 || warp >= 8)) {
+    // ---- tokens of few rows: x as above, then h from the partial sums; the four warps take stages in turn ----
+    int st = 0, turn = (warp & 1) + (warp >= 8 ? 2 : 0);  // 0: this warp's
     uint32_t phase = 0;
     bool alive = true;
     auto next = [&]() {
-      turn ^= 1;
+      turn = (turn + 1) & 3;
       if (++st == nst) {
         st = 0;
         phase ^= 1u;
@@ -422,7 +439,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
         const Seg s = up_seg(R, u, u1, half, FT, KU);
 #pragma unroll 1
         for (int kb = s.kb0; kb < s.kb1; ++kb) {
-          if (turn == warp - 2) {
+          if (turn == 0) {
             if (!open()) break;
             if (lane == 0) {
               mbar_expect_tx(smem_addr(&C.bfull[st]), NT * 128);
@@ -447,7 +464,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
 #pragma unroll 1
         for (int kb = s.kb0; kb < s.kb1;) {
           const int nk = down_units(s, kb);
-          if (turn == warp - 2) {
+          if (turn == 0) {
             if (!open()) break;
             char* sB = reinterpret_cast<char*>(smem + st * slot + nk * TC_TILE);
 #pragma unroll 1
@@ -488,79 +505,80 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
     }
     if (!alive) settle();
   } else if (warp == 1) {
-    if (lane == 0) {
-      int st = 0, seg = 0;
-      uint32_t phase = 0;
-      bool alive = true;
-      auto advance = [&]() {
-        umma_commit(smem_addr(&C.empty[st]));
-        if (++st == nst) {
-          st = 0;
-          phase ^= 1u;
-        }
-      };
-      auto open = [&]() {  // the segment's accumulator is free
-        const uint32_t par = ((seg >> 1) & 1) ^ 1;
-        if (!ring_wait(&C.tempty[seg & 1], par, abort_flag, a.err, 720)) alive = false;
-        tc_fence_after();
-        return alive;
-      };
-      auto filled = [&]() {
-        if (!ring_wait(&C.wfull[st], phase, abort_flag, a.err, 721) ||
-            !ring_wait(&C.bfull[st], phase, abort_flag, a.err, 722))
-          alive = false;
-        tc_fence_after();
-        return alive;
-      };
-      for (int half = 0; half < 2; ++half)
-        for (int u = u0; u < u1 && alive && open();) {
-          const Seg s = up_seg(R, u, u1, half, FT, KU);
-          const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(NT);
-#pragma unroll 1
-          for (int kb = s.kb0; kb < s.kb1 && filled(); ++kb) {
-            // descriptors of the following K steps differ in the address alone (in 16-byte units)
-            uint64_t ad = sdesc(ring + st * slot, 8192, 1024), bd = sdesc(ring + st * slot + 2 * TC_TILE, 16, 1024);
-            uint32_t on = kb != s.kb0;
-#pragma unroll 1
-            for (int q = 0; q < TC_KB / 16; ++q, ad += 2048 / 16, bd += 32 / 16, on = 1) {
-              umma_bf16(acc, ad, bd, id, on);
-              umma_bf16(acc + TC_B, ad + TC_TILE / 16, bd, id, on);
-            }
-            advance();
-          }
-          if (!alive) break;
-          umma_commit(smem_addr(&C.tfull[seg & 1]));
-          ++seg;
-          u += s.kb1 - s.kb0;
-        }
-      for (int half = 0; half < 2; ++half)
-        for (int v = v0; v < v1 && alive && open();) {
-          const Seg s = down_seg(R, v, v1, half, per, KD);
-          const int n16 = pad16(s.n);
-          const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(2 * n16);
-#pragma unroll 1
-          for (int kb = s.kb0; kb < s.kb1 && filled();) {
-            const int nk = down_units(s, kb);
-            uint64_t ad = sdesc(ring + st * slot, 8192, 1024), bd = sdesc(ring + st * slot + nk * TC_TILE, 16, 1024);
-            uint32_t on = kb != s.kb0;
-#pragma unroll 1
-            for (int i = 0; i < nk; ++i, ad += (TC_TILE - 8192) / 16, bd += (2 * n16 * 128 - 128) / 16) {
-#pragma unroll 1
-              for (int q = 0; q < TC_KB / 16; ++q, ad += 2048 / 16, bd += 32 / 16, on = 1) umma_bf16(acc, ad, bd, id, on);
-            }
-            advance();
-            kb += nk;
-          }
-          if (!alive) break;
-          umma_commit(smem_addr(&C.tfull[seg & 1]));
-          ++seg;
-          v += s.kb1 - s.kb0;
-        }
-      umma_commit(smem_addr(&C.drain));
-      for (uint32_t it = 0; it < (1u << 26) && !mbar_try_wait(smem_addr(&C.drain), 0); ++it) {
+    // ---- MMAs: the whole warp walks the stages, so descriptors stay in uniform registers; one lane issues ----
+    int st = 0, seg = 0;
+    uint32_t phase = 0;
+    bool alive = true;
+    auto wait = [&](uint64_t* b, uint32_t parity, uint32_t where) {
+      return __all_sync(0xffffffffu, ring_wait(b, parity, abort_flag, a.err, where));
+    };
+    auto advance = [&]() {
+      commit_elected(smem_addr(&C.empty[st]));
+      if (++st == nst) {
+        st = 0;
+        phase ^= 1u;
       }
+    };
+    auto open = [&]() {  // the segment's accumulator is free
+      alive = wait(&C.tempty[seg & 1], ((seg >> 1) & 1) ^ 1, 720);
+      tc_fence_after();
+      return alive;
+    };
+    auto filled = [&]() {
+      alive = wait(&C.wfull[st], phase, 721) && wait(&C.bfull[st], phase, 722);
+      tc_fence_after();
+      return alive;
+    };
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half)
+      for (int u = u0; u < u1 && alive && open();) {
+        const Seg s = up_seg(R, u, u1, half, FT, KU);
+        const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(NT);
+#pragma unroll 1
+        for (int kb = s.kb0; kb < s.kb1 && filled(); ++kb) {
+          // descriptors of the following K steps differ in the address alone (in 16-byte units)
+          const uint64_t ad = sdesc(ring + st * slot, 8192, 1024), bd = sdesc(ring + st * slot + 2 * TC_TILE, 16, 1024);
+#pragma unroll
+          for (int q = 0; q < TC_KB / 16; ++q) {
+            const uint32_t on = q != 0 || kb != s.kb0;
+            umma_elected(acc, ad + q * (2048 / 16), bd + q * (32 / 16), id, on);
+            umma_elected(acc + TC_B, ad + TC_TILE / 16 + q * (2048 / 16), bd + q * (32 / 16), id, on);
+          }
+          advance();
+        }
+        if (!alive) break;
+        commit_elected(smem_addr(&C.tfull[seg & 1]));
+        ++seg;
+        u += s.kb1 - s.kb0;
+      }
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half)
+      for (int v = v0; v < v1 && alive && open();) {
+        const Seg s = down_seg(R, v, v1, half, per, KD);
+        const int n16 = pad16(s.n);
+        const uint32_t acc = tmem + (seg & 1) * TC_BUF, id = dec_idesc(2 * n16);
+#pragma unroll 1
+        for (int kb = s.kb0; kb < s.kb1 && filled();) {
+          const int nk = down_units(s, kb);
+          uint64_t ad = sdesc(ring + st * slot, 8192, 1024), bd = sdesc(ring + st * slot + nk * TC_TILE, 16, 1024);
+#pragma unroll 1
+          for (int i = 0; i < nk; ++i, ad += TC_TILE / 16, bd += 2 * n16 * 128 / 16) {
+#pragma unroll
+            for (int q = 0; q < TC_KB / 16; ++q)
+              umma_elected(acc, ad + q * (2048 / 16), bd + q * (32 / 16), id, q != 0 || i != 0 || kb != s.kb0);
+          }
+          advance();
+          kb += nk;
+        }
+        if (!alive) break;
+        commit_elected(smem_addr(&C.tfull[seg & 1]));
+        ++seg;
+        v += s.kb1 - s.kb0;
+      }
+    commit_elected(smem_addr(&C.drain));
+    for (uint32_t it = 0; it < (1u << 26) && !mbar_try_wait(smem_addr(&C.drain), 0); ++it) {
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     const int q = warp - 4, tid = threadIdx.x - 128, col = tid;  // TMEM lanes q * 32 ..: the thread's weight column
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     int seg = 0;
