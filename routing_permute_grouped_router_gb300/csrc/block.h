@@ -38,11 +38,11 @@ cudaError_t launch_decode(const Shape& s, const DecodeIo& io, void* ws, uint32_t
 
 // ---- norm.cu ----
 cudaError_t launch_norm_fwd(int64_t rows, int d, bool bf16, const void* x, const float* gamma, const float* beta,
-                            float eps, void* y, float* mean, float* rstd, cudaStream_t st);
+                            float eps, void* y, float* mean, float* rstd, uint32_t* err, cudaStream_t st);
 size_t norm_ws_bytes(int64_t rows, int d);
 cudaError_t launch_norm_bwd(int64_t rows, int d, bool bf16, const void* x, const void* dy, const float* gamma,
                             const float* mean, const float* rstd, const void* dres, void* dx, float* dgamma,
-                            float* dbeta, int accumulate, void* ws, cudaStream_t st);
+                            float* dbeta, int accumulate, void* ws, uint32_t* err, cudaStream_t st);
 
 // ---- dropout.cu ----
 cudaError_t launch_dropout(int kind, int64_t n, bool bf16, const void* y, const void* residual, void* out,

@@ -116,7 +116,7 @@ moe_status moe_norm_fwd(int64_t rows, int32_t d, int32_t dtype, const void* x, c
   uint32_t* err = nullptr;
   MOE_TRY(current_error_word(&err));
   if (rows == 0) return MOE_OK;
-  CUDA_TRY(launch_norm_fwd(rows, d, dtype == MOE_BF16, x, gamma, beta, eps, y, mean, rstd, stream));
+  CUDA_TRY(launch_norm_fwd(rows, d, dtype == MOE_BF16, x, gamma, beta, eps, y, mean, rstd, err, stream));
   return MOE_OK;
 }
 
@@ -154,7 +154,7 @@ moe_status moe_norm_bwd(int64_t rows, int32_t d, int32_t dtype, const void* x, c
   }
   void* base = reinterpret_cast<void*>((reinterpret_cast<uintptr_t>(ws) + 255) / 256 * 256);
   CUDA_TRY(launch_norm_bwd(rows, d, dtype == MOE_BF16, x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, accumulate,
-                           base, stream));
+                           base, err, stream));
   return MOE_OK;
 }
 

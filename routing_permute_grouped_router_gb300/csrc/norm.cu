@@ -7,18 +7,23 @@
 //             dgamma = sum over rows of dy * n,  dbeta = sum over rows of dy
 //
 // Both passes are bound by HBM: the forward reads and writes a row once, the
-// backward reads x, dy (and dres) and writes dx.  A row is held in registers
-// between the load and the store: `tpr` threads share it, each with NV vectors
-// of VN elements, so the variance is the sum of squared distances from the
-// mean (no cancellation of large means) without a second read.  A CTA walks
-// rows in a grid stride and keeps its columns' gamma, beta and, in the
-// backward, its dgamma and dbeta sums in registers; the sums of the CTAs are
-// added in CTA order by a second kernel, so results do not depend on timing.
-// All statistics and sums are fp32.
+// backward reads x, dy (and dres) and writes dx.  `tpr` threads share a row (a
+// CTA, or a warp of one where 32 are enough), 16 elements each: 64 to 512 rows
+// are in work on an SM's registers while plain copies bring the next ones into
+// a ring in shared memory, up to four rows deep, so the loads' latency is out of
+// the way of the two reductions of a row.  (With the loads in registers and
+// no ring the 32768 x 4096 bf16 passes reached 3.4 and 2.8 TB/s.)  The variance
+// is the sum of squared distances from the mean: no cancellation of a large
+// mean, no second read.  Threads keep their columns' gamma, beta and, in the
+// backward, dgamma and dbeta sums in registers over all rows of the CTA; the
+// sums of the CTAs are added in CTA order by a second kernel, so results do
+// not depend on timing.  All statistics and sums are fp32.
 //
-// Rows that are not a multiple of 16 bytes (odd d) are loaded element by
-// element, coalesced; rows of more than 8192 elements are walked in a loop
-// (the wide kernels) and read again from cache.
+// A copy has to begin and end on 16 bytes.  Rows of another length are copied
+// with up to 15 bytes more on either side and read from shared memory element
+// by element; what that would read past the tensor's end is loaded directly.
+// Rows of more than 8192 elements are walked in a loop (the wide kernels) and
+// read again from cache.
 #include "block.h"
 #include "common.cuh"
 
@@ -26,58 +31,159 @@ namespace moe {
 namespace {
 
 constexpr int MAX_TPR = 512;   // most threads that share a row held in registers
-constexpr int EPT = 16;        // most elements of a row a thread holds
-constexpr int NT = 256;        // threads a CTA when tpr <= 256
+constexpr int EPT = 16;        // elements of a row a thread holds
+constexpr int FWD_REGS = 80, BWD_REGS = 128;  // a thread's, so that three and two CTAs of 256 fit an SM
+constexpr int SMEM_SM = 220 * 1024;             // shared memory of an SM that the rings may take
+constexpr int RING = 4;        // most rows on their way to a group of threads
 constexpr int WIDE_NT = 512;   // threads a CTA of the wide kernels
 constexpr int RED_COLS = 32, RED_STRIPS = 16;
 
-template <typename T, int VN>
-__device__ __forceinline__ void ld_vec(const T* p, float* v) {
-  if constexpr (VN == 1) {
-    v[0] = to_f32(*p);
-  } else {
-    float w[Vec<T>::N];
-    unpack(*reinterpret_cast<const uint4*>(p), w);
-#pragma unroll
-    for (int i = 0; i < VN; ++i) v[i] = w[i];
-  }
-}
-template <typename T, int VN>
-__device__ __forceinline__ void st_vec(T* p, const float* v) {
-  if constexpr (VN == 1) {
-    *p = from_f32<T>(v[0]);
-  } else {
-    float w[Vec<T>::N];
-#pragma unroll
-    for (int i = 0; i < VN; ++i) w[i] = v[i];
-    stg16(p, pack(w));
-  }
-}
+// Element c (of EPT) of thread r of tpr, in whole vectors of VN or one by one.
 template <int VN>
-__device__ __forceinline__ void ld_f32(const float* p, float* v) {
-#pragma unroll
-  for (int i = 0; i < VN; ++i) v[i] = __ldg(p + i);
+__device__ __forceinline__ int column(int r, int tpr, int c) {
+  return (r + c / VN * tpr) * VN + c % VN;
+}
+// whether it is one of the row's d (d is a multiple of VN)
+template <int VN>
+__device__ __forceinline__ bool in_row(int r, int tpr, int c, int d) {
+  return (r + c / VN * tpr) * VN < d;
 }
 
-// Sum over the tpr threads of a row; scratch holds one float2 a warp, twice
-// (used in turn, so one barrier a reduction).
-__device__ __forceinline__ float2 row_sum(float2 s, int tpr, float2* scratch, int& turn) {
-  s.x = warp_sum(s.x);
-  s.y = warp_sum(s.y);
-  if (tpr > 32) {
-    const int warp = threadIdx.x / 32, nw = blockDim.x / 32;
-    float2* buf = scratch + turn * nw;
-    turn ^= 1;
-    if (threadIdx.x % 32 == 0) buf[warp] = s;
-    __syncthreads();
-    const int w0 = warp & ~(tpr / 32 - 1);
-    s = make_float2(0.f, 0.f);
-    for (int i = 0; i < tpr / 32; ++i) {
-      s.x += buf[w0 + i].x;
-      s.y += buf[w0 + i].y;
+// Two fp32 operations in one instruction; each half rounds as the scalar one does.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Every warp of a row gives one float4; each thread gets that of warp
+// lane % warps, so xor shuffles over the warps (`nw`, a power of two) finish a
+// sum.  One barrier; scratch holds a float4 a warp twice, used in turn.
+__device__ __forceinline__ float4 share(float4 v, int nw, float4* scratch, int& turn) {
+  float4* buf = scratch + turn * nw;
+  turn ^= 1;
+  if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
+  __syncthreads();
+  return buf[threadIdx.x & (nw - 1)];
+}
+__device__ __forceinline__ float sum_over(float v, int n) {
+  for (int o = 1; o < n; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// ---- the ring ----
+__device__ __forceinline__ uint32_t sm_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void copy_row(uint32_t dst, const char* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// Waits for the barrier's phase, two seconds at most.
+__device__ __noinline__ void ring_wait(uint32_t bar, uint32_t parity, uint32_t* err) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 0; i < (1u << 30); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return;
+    if ((i & 255u) == 255u) {
+      uint64_t t;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (t0 == 0) t0 = t;
+      if (t - t0 > 2000000000ull) break;
     }
   }
-  return s;
+  report_error(err, DEV_TIMEOUT, 760);
+}
+
+// Where a row's copy begins and how long it is: the row itself, or the 16-byte
+// units that hold it, cut off at the end of the tensor.
+struct Span {
+  int64_t at;       // byte offset of the copy in the tensor
+  int skip, bytes;  // bytes before the row's first element; bytes of the copy
+};
+template <typename T, bool WHOLE>
+__device__ __forceinline__ Span row_span(int64_t row, int64_t rows, int d) {
+  const int64_t b0 = row * d * (int64_t)sizeof(T), b1 = b0 + d * (int64_t)sizeof(T);
+  if (WHOLE) return {b0, 0, (int)(b1 - b0)};
+  const int64_t total = rows * d * (int64_t)sizeof(T), a0 = b0 & ~(int64_t)15;
+  int64_t a1 = (b1 + 15) & ~(int64_t)15;
+  if (a1 > total) a1 = total & ~(int64_t)15;
+  return {a0, (int)(b0 - a0), a1 > a0 ? (int)(a1 - a0) : 0};
+}
+
+// The thread's elements of a row, from the ring (zeros past the row's end).
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void take_row(const char* stage, const Span& sp, const T* tensor, int r, int tpr, int d,
+                                         float2 (&v)[EPT / 2]) {
+  if constexpr (WHOLE) {
+    constexpr int VN = Vec<T>::N;
+#pragma unroll
+    for (int i = 0; i < EPT / VN; ++i) {
+      const int q = r + i * tpr;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (q * VN < d) u = *reinterpret_cast<const uint4*>(stage + q * 16);
+      float w[VN];
+      unpack(u, w);
+#pragma unroll
+      for (int j = 0; j < VN; j += 2) v[(i * VN + j) / 2] = make_float2(w[j], w[j + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < EPT; ++c) {
+      const int e = r + c * tpr, at = sp.skip + e * (int)sizeof(T);
+      float w = 0.f;
+      if (e < d)
+        w = to_f32(at < sp.bytes ? *reinterpret_cast<const T*>(stage + at) : tensor[(sp.at + at) / (int64_t)sizeof(T)]);
+      (c & 1 ? v[c / 2].y : v[c / 2].x) = w;
+    }
+  }
+}
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void put_row(T* row, int r, int tpr, int d, const float2 (&v)[EPT / 2]) {
+  if constexpr (WHOLE) {
+    constexpr int VN = Vec<T>::N;
+#pragma unroll
+    for (int i = 0; i < EPT / VN; ++i) {
+      const int q = r + i * tpr;
+      float w[VN];
+#pragma unroll
+      for (int j = 0; j < VN; j += 2) {
+        w[j] = v[(i * VN + j) / 2].x;
+        w[j + 1] = v[(i * VN + j) / 2].y;
+      }
+      if (q * VN < d) stg16(row + (size_t)q * VN, pack(w));
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < EPT; ++c)
+      if (r + c * tpr < d) row[r + c * tpr] = from_f32<T>(c & 1 ? v[c / 2].y : v[c / 2].x);
+  }
 }
 
 struct NormArgs {
@@ -96,69 +202,135 @@ struct NormArgs {
   float* dbeta;
   int64_t rows;
   int d, tpr, parts, accumulate;
+  int slot, ring;  // bytes of a row's place in the ring, places
   float eps;
+  uint32_t* err;
 };
 
-template <typename T, int VN, int NV>
-__global__ void __launch_bounds__(MAX_TPR) norm_fwd_kernel(const NormArgs a) {
-  pdl_enter();  // see pdl_wait: no global access before this
-  __shared__ float2 scratch[2 * MAX_TPR / 32];
-  int turn = 0;
-  const T* x = static_cast<const T*>(a.x);
-  T* y = static_cast<T*>(a.out);
-  const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr, r = threadIdx.x % a.tpr;
-  const int nvec = a.d / VN;
-  const float inv = 1.f / (float)a.d;
-  float ga[NV * VN], be[NV * VN];
+// A group of tpr threads, its rows (first, first + step, ...) and its ring.
+// The group's first thread starts the copies; a place is filled again once the
+// group has taken its row into registers (after the first reduction).
+template <typename T, bool WHOLE, int NBUF>
+struct Rows {
+  const char* src[NBUF];
+  char* base;
+  uint64_t* bars;
+  int64_t first, step, rows;
+  int d, slot, ring;
+  int at = 0;           // the place of the row in work
+  uint32_t phase = 0;   // and its barrier's phase
+  __device__ __forceinline__ void start(int64_t row, int p) const {
+    if (row >= rows) return;
+    const Span sp = row_span<T, WHOLE>(row, rows, d);
+    const uint32_t bar = sm_addr(bars + p);
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(sp.bytes * NBUF) : "memory");
+    if (sp.bytes > 0) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int q = r + i * a.tpr;
-#pragma unroll
-    for (int j = 0; j < VN; ++j) ga[i * VN + j] = be[i * VN + j] = 0.f;
-    if (q < nvec) {
-      ld_f32<VN>(a.gamma + (size_t)q * VN, ga + i * VN);
-      ld_f32<VN>(a.beta + (size_t)q * VN, be + i * VN);
+      for (int b = 0; b < NBUF; ++b) copy_row(sm_addr(base + (p * NBUF + b) * slot), src[b] + sp.at, sp.bytes, bar);
     }
   }
-  // every group of the CTA makes the same number of turns (row_sum has a barrier)
-  for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += (int64_t)gridDim.x * groups) {
-    const int64_t row = row0 + g;
-    const bool live = row < a.rows;
-    const T* xr = x + row * a.d;
-    float v[NV * VN];
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int q = r + i * a.tpr;
-#pragma unroll
-      for (int j = 0; j < VN; ++j) v[i * VN + j] = 0.f;
-      if (live && q < nvec) ld_vec<T, VN>(xr + (size_t)q * VN, v + i * VN);
+  __device__ __forceinline__ void wait(uint32_t* err) const { ring_wait(sm_addr(bars + at), phase, err); }
+  __device__ __forceinline__ const char* place(int b) const { return base + (at * NBUF + b) * slot; }
+  // The row in work has been taken: its place gets the row `ring` turns on.
+  __device__ __forceinline__ void taken(int64_t row, bool leader) {
+    if (leader) start(row + ring * step, at);
+    if (++at == ring) {
+      at = 0;
+      phase ^= 1u;
     }
+  }
+};
+
+extern __shared__ __align__(128) char norm_smem[];
+
+template <typename T, bool WHOLE, int NBUF>
+__device__ __forceinline__ Rows<T, WHOLE, NBUF> begin_rows(const NormArgs& a, uint64_t* bars, int r) {
+  const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr;
+  Rows<T, WHOLE, NBUF> R;
+  R.src[0] = static_cast<const char*>(a.x);
+  if (NBUF > 1) R.src[1] = static_cast<const char*>(a.dy);
+  if (NBUF > 2) R.src[2] = static_cast<const char*>(a.dres);
+  R.base = norm_smem + (size_t)g * a.ring * NBUF * a.slot;
+  R.bars = bars + g * RING;
+  R.first = (int64_t)blockIdx.x * groups + g;
+  R.step = (int64_t)gridDim.x * groups;
+  R.rows = a.rows;
+  R.d = a.d;
+  R.slot = a.slot;
+  R.ring = a.ring;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < groups * RING; ++i)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(sm_addr(bars + i)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_enter();  // see pdl_wait: no global access before this
+  if (r == 0)
+    for (int i = 0; i < a.ring; ++i) R.start(R.first + i * R.step, i);
+  return R;
+}
+
+// The columns' weights, in pairs (0 past the row's end).
+template <int VN>
+__device__ __forceinline__ void take_weights(const float* w, int r, int tpr, int d, float2 (&v)[EPT / 2]) {
 #pragma unroll
-    for (int i = 0; i < NV * VN; ++i) s += v[i];
-    const float mean = row_sum(make_float2(s, 0.f), a.tpr, scratch, turn).x * inv;
-    s = 0.f;
+  for (int c = 0; c < EPT; ++c) {
+    const float u = in_row<VN>(r, tpr, c, d) ? __ldg(w + column<VN>(r, tpr, c)) : 0.f;
+    (c & 1 ? v[c / 2].y : v[c / 2].x) = u;
+  }
+}
+
+template <typename T, bool WHOLE>
+__global__ void __maxnreg__(FWD_REGS) norm_fwd_kernel(const NormArgs a) {
+  constexpr int VN = WHOLE ? Vec<T>::N : 1;
+  __shared__ float4 scratch[2 * MAX_TPR / 32];
+  __shared__ uint64_t bars[4 * RING];
+  int turn = 0;
+  const int r = threadIdx.x % a.tpr, nw = a.tpr / 32;
+  Rows<T, WHOLE, 1> R = begin_rows<T, WHOLE, 1>(a, bars, r);
+  T* y = static_cast<T*>(a.out);
+  const float inv = 1.f / (float)a.d;
+  float2 ga[EPT / 2], be[EPT / 2];
+  take_weights<VN>(a.gamma, r, a.tpr, a.d, ga);
+  take_weights<VN>(a.beta, r, a.tpr, a.d, be);
+  // the warp's elements of a row
+  float mine = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (r + i * a.tpr < nvec) {
+  for (int c = 0; c < EPT; ++c) mine += in_row<VN>(r, a.tpr, c, a.d) ? 1.f : 0.f;
+  const float wn = warp_sum(mine), winv = wn > 0.f ? 1.f / wn : 0.f;
+#pragma unroll 1
+  for (int64_t row = R.first; row < a.rows; row += R.step) {
+    const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
+    R.wait(a.err);
+    float2 v[EPT / 2];
+    take_row<T, WHOLE>(R.place(0), sp, static_cast<const T*>(a.x), r, a.tpr, a.d, v);
+    // mean and squared distances of the warp's elements first; the warps then
+    // combine theirs with the distances of their means
+    float2 s2 = both(0.f);
 #pragma unroll
-        for (int j = 0; j < VN; ++j) {
-          v[i * VN + j] -= mean;
-          s = fmaf(v[i * VN + j], v[i * VN + j], s);
-        }
-      }
-    const float var = row_sum(make_float2(s, 0.f), a.tpr, scratch, turn).x * inv;
-    const float rstd = 1.f / sqrtf(var + a.eps);
-    if (!live) continue;
+    for (int c = 0; c < EPT / 2; ++c) s2 = add2(s2, v[c]);
+    const float ws = warp_sum(s2.x + s2.y), wmean = ws * winv;
+    s2 = both(0.f);
+    const float2 off = both(-wmean);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int q = r + i * a.tpr;
-      if (q < nvec) {
-#pragma unroll
-        for (int j = 0; j < VN; ++j) v[i * VN + j] = fmaf(v[i * VN + j] * rstd, ga[i * VN + j], be[i * VN + j]);
-        st_vec<T, VN>(y + row * a.d + (size_t)q * VN, v + i * VN);
-      }
+    for (int c = 0; c < EPT / 2; ++c) {
+      const float2 t = add2(v[c], off);
+      if (in_row<VN>(r, a.tpr, 2 * c, a.d)) s2.x = fmaf(t.x, t.x, s2.x);
+      if (in_row<VN>(r, a.tpr, 2 * c + 1, a.d)) s2.y = fmaf(t.y, t.y, s2.y);
     }
+    float m2 = warp_sum(s2.x + s2.y), mean = wmean;
+    if (nw > 1) {
+      const float4 w = share(make_float4(ws, m2, wmean, wn), nw, scratch, turn);
+      mean = sum_over(w.x, nw) * inv;
+      m2 = sum_over(fmaf(w.w * (w.z - mean), w.z - mean, w.y), nw);
+    }
+    __syncwarp();
+    R.taken(row, r == 0);
+    const float rstd = 1.f / sqrtf(m2 * inv + a.eps);
+    const float2 by = both(rstd), from = both(-mean);
+#pragma unroll
+    for (int c = 0; c < EPT / 2; ++c) v[c] = fma2(mul2(add2(v[c], from), by), ga[c], be[c]);
+    put_row<T, WHOLE>(y + row * a.d, r, a.tpr, a.d, v);
     if (r == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -166,100 +338,77 @@ __global__ void __launch_bounds__(MAX_TPR) norm_fwd_kernel(const NormArgs a) {
   }
 }
 
-template <typename T, int VN, int NV, bool RES>
-__global__ void __launch_bounds__(MAX_TPR) norm_bwd_kernel(const NormArgs a) {
-  pdl_enter();
-  __shared__ float2 scratch[2 * MAX_TPR / 32];
-  extern __shared__ float dsum[];  // [2][d]: the CTA's dgamma and dbeta (groups > 1)
+template <typename T, bool WHOLE, bool RES>
+__global__ void __maxnreg__(BWD_REGS) norm_bwd_kernel(const NormArgs a) {
+  constexpr int VN = WHOLE ? Vec<T>::N : 1;
+  __shared__ float4 scratch[2 * MAX_TPR / 32];
+  __shared__ uint64_t bars[4 * RING];
   int turn = 0;
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* res = static_cast<const T*>(a.dres);
+  const int r = threadIdx.x % a.tpr, nw = a.tpr / 32;
+  Rows<T, WHOLE, RES ? 3 : 2> R = begin_rows<T, WHOLE, RES ? 3 : 2>(a, bars, r);
   T* dx = static_cast<T*>(a.out);
-  const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr, r = threadIdx.x % a.tpr;
-  const int nvec = a.d / VN;
   const float inv = 1.f / (float)a.d;
-  float ga[NV * VN], dg[NV * VN], db[NV * VN];
+  float2 ga[EPT / 2], dg[EPT / 2], db[EPT / 2];
+  take_weights<VN>(a.gamma, r, a.tpr, a.d, ga);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int q = r + i * a.tpr;
+  for (int c = 0; c < EPT / 2; ++c) dg[c] = db[c] = both(0.f);
+#pragma unroll 1
+  for (int64_t row = R.first; row < a.rows; row += R.step) {
+    const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
+    const float rstd = __ldg(a.rstd_in + row), mean = __ldg(a.mean_in + row);
+    R.wait(a.err);
+    float2 n[EPT / 2], v[EPT / 2], o[EPT / 2];
+    take_row<T, WHOLE>(R.place(0), sp, static_cast<const T*>(a.x), r, a.tpr, a.d, n);
+    take_row<T, WHOLE>(R.place(1), sp, static_cast<const T*>(a.dy), r, a.tpr, a.d, v);
+    if (RES) take_row<T, WHOLE>(R.place(2), sp, static_cast<const T*>(a.dres), r, a.tpr, a.d, o);
+    float2 sv = both(0.f), sn = both(0.f);
 #pragma unroll
-    for (int j = 0; j < VN; ++j) ga[i * VN + j] = dg[i * VN + j] = db[i * VN + j] = 0.f;
-    if (q < nvec) ld_f32<VN>(a.gamma + (size_t)q * VN, ga + i * VN);
-  }
-  for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < a.rows; row0 += (int64_t)gridDim.x * groups) {
-    const int64_t row = row0 + g;
-    const bool live = row < a.rows;
-    const float mean = live ? a.mean_in[row] : 0.f, rstd = live ? a.rstd_in[row] : 0.f;
-    float n[NV * VN], v[NV * VN];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int q = r + i * a.tpr;
-#pragma unroll
-      for (int j = 0; j < VN; ++j) n[i * VN + j] = v[i * VN + j] = 0.f;
-      if (live && q < nvec) {
-        ld_vec<T, VN>(x + row * a.d + (size_t)q * VN, n + i * VN);
-        ld_vec<T, VN>(dy + row * a.d + (size_t)q * VN, v + i * VN);
-      }
+    for (int c = 0; c < EPT / 2; ++c) {  // past the row's end dy and gamma are 0
+      n[c] = mul2(add2(n[c], both(-mean)), both(rstd));
+      dg[c] = fma2(v[c], n[c], dg[c]);
+      db[c] = add2(db[c], v[c]);
+      v[c] = mul2(v[c], ga[c]);
+      sv = add2(sv, v[c]);
+      sn = fma2(v[c], n[c], sn);
     }
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (live && r + i * a.tpr < nvec) {
-#pragma unroll
-        for (int j = 0; j < VN; ++j) {
-          const int c = i * VN + j;
-          n[c] = (n[c] - mean) * rstd;
-          dg[c] = fmaf(v[c], n[c], dg[c]);
-          db[c] += v[c];
-          v[c] *= ga[c];
-          s.x += v[c];
-          s.y = fmaf(v[c], n[c], s.y);
-        }
-      }
-    s = row_sum(s, a.tpr, scratch, turn);
-    const float m1 = s.x * inv, m2 = s.y * inv;
-    if (!live) continue;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int q = r + i * a.tpr;
-      if (q < nvec) {
-        float o[VN], rr[VN];
-        if (RES) ld_vec<T, VN>(res + row * a.d + (size_t)q * VN, rr);
-#pragma unroll
-        for (int j = 0; j < VN; ++j) {
-          const int c = i * VN + j;
-          o[j] = (v[c] - m1 - n[c] * m2) * rstd;
-          if (RES) o[j] += rr[j];
-        }
-        st_vec<T, VN>(dx + row * a.d + (size_t)q * VN, o);
-      }
+    float m1 = warp_sum(sv.x + sv.y), m2 = warp_sum(sn.x + sn.y);
+    if (nw > 1) {
+      const float4 w = share(make_float4(m1, m2, 0.f, 0.f), nw, scratch, turn);
+      m1 = sum_over(w.x, nw);
+      m2 = sum_over(w.y, nw);
     }
+    __syncwarp();
+    R.taken(row, r == 0);
+    const float2 k1 = both(-m1 * inv), k2 = both(-m2 * inv), by = both(rstd);
+#pragma unroll
+    for (int c = 0; c < EPT / 2; ++c) {
+      const float2 t = fma2(n[c], k2, add2(v[c], k1));
+      o[c] = RES ? fma2(t, by, o[c]) : mul2(t, by);
+    }
+    put_row<T, WHOLE>(dx + row * a.d, r, a.tpr, a.d, o);
   }
-  // the CTA's sums: the groups in turn, then one row pair of the partials
+  // the CTA's sums: its groups in turn (only warps form several), then one row pair of the partials
+  const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr;
   float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
+  float* dsum = reinterpret_cast<float*>(norm_smem);  // [2][d], the ring's place: all rows have been taken
   for (int t = 0; t < groups; ++t) {
     if (groups > 1) __syncthreads();
     if (g != t) continue;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int q = r + i * a.tpr;
-      if (q < nvec) {
-#pragma unroll
-        for (int j = 0; j < VN; ++j) {
-          const int c = i * VN + j, col = q * VN + j;
-          float u = dg[c], w = db[c];
-          if (t > 0) {
-            u += dsum[col];
-            w += dsum[a.d + col];
-          }
-          if (t == groups - 1) {
-            out[col] = u;
-            out[a.d + col] = w;
-          } else {
-            dsum[col] = u;
-            dsum[a.d + col] = w;
-          }
+    for (int c = 0; c < EPT; ++c) {
+      const int col = column<VN>(r, a.tpr, c);
+      if (in_row<VN>(r, a.tpr, c, a.d)) {
+        float u = c & 1 ? dg[c / 2].y : dg[c / 2].x, w = c & 1 ? db[c / 2].y : db[c / 2].x;
+        if (t > 0) {
+          u += dsum[col];
+          w += dsum[a.d + col];
+        }
+        if (t == groups - 1) {
+          out[col] = u;
+          out[a.d + col] = w;
+        } else {
+          dsum[col] = u;
+          dsum[a.d + col] = w;
         }
       }
     }
@@ -274,8 +423,17 @@ __global__ void __launch_bounds__(RED_COLS * RED_STRIPS) norm_bwd_reduce_kernel(
   const int c = threadIdx.x % RED_COLS, strip = threadIdx.x / RED_COLS;
   const int col = blockIdx.x * RED_COLS + c;  // of the 2 d columns
   float s = 0.f;
-  if (col < 2 * a.d)
-    for (int p = strip; p < a.parts; p += RED_STRIPS) s += a.partial[(size_t)p * 2 * a.d + col];
+  if (col < 2 * a.d) {
+#pragma unroll 1
+    for (int p = strip; p < a.parts; p += 8 * RED_STRIPS) {  // eight loads at once
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = p + j * RED_STRIPS < a.parts ? a.partial[(size_t)(p + j * RED_STRIPS) * 2 * a.d + col] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += v[j];
+    }
+  }
   tile[strip][c] = s;
   __syncthreads();
   if (strip == 0 && col < 2 * a.d) {
@@ -288,14 +446,15 @@ __global__ void __launch_bounds__(RED_COLS * RED_STRIPS) norm_bwd_reduce_kernel(
 }
 
 // ---- rows of more than MAX_TPR * EPT elements: one CTA a row, walked in a loop ----
-__device__ __forceinline__ float2 cta_sum(float2 s, float2* scratch, int& turn) {
-  return row_sum(s, WIDE_NT, scratch, turn);
+__device__ __forceinline__ float2 cta_sum(float2 s, float4* scratch, int& turn) {
+  const float4 w = share(make_float4(warp_sum(s.x), warp_sum(s.y), 0.f, 0.f), WIDE_NT / 32, scratch, turn);
+  return make_float2(sum_over(w.x, WIDE_NT / 32), sum_over(w.y, WIDE_NT / 32));
 }
 
 template <typename T>
 __global__ void __launch_bounds__(WIDE_NT) norm_fwd_wide_kernel(const NormArgs a) {
   pdl_enter();
-  __shared__ float2 scratch[2 * WIDE_NT / 32];
+  __shared__ float4 scratch[2 * WIDE_NT / 32];
   int turn = 0;
   const float inv = 1.f / (float)a.d;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -323,7 +482,7 @@ __global__ void __launch_bounds__(WIDE_NT) norm_fwd_wide_kernel(const NormArgs a
 template <typename T>
 __global__ void __launch_bounds__(WIDE_NT) norm_bwd_wide_kernel(const NormArgs a) {
   pdl_enter();
-  __shared__ float2 scratch[2 * WIDE_NT / 32];
+  __shared__ float4 scratch[2 * WIDE_NT / 32];
   int turn = 0;
   const float inv = 1.f / (float)a.d;
   const T* x = static_cast<const T*>(a.x);
@@ -357,63 +516,97 @@ __global__ void __launch_bounds__(WIDE_NT) norm_bwd_wide_kernel(const NormArgs a
 
 bool wide(int d) { return d > MAX_TPR * EPT; }
 
-// Threads that share a row: as few as hold it in EPT elements each.
-int threads_per_row(int d, int vn, int nv) {
+// Threads that share a row: as few as hold it, a warp at least.
+int threads_per_row(int d) {
   int tpr = 32;
-  while ((int64_t)tpr * vn * nv < d) tpr *= 2;
+  while (tpr * EPT < d) tpr *= 2;
   return tpr;
 }
-bool whole_vectors(int d, bool bf16) { return d % (bf16 ? 8 : 4) == 0; }
+// A CTA is one group of threads, or four warps each with rows of its own.
+int groups_of(int tpr) { return tpr == 32 ? 4 : 1; }
 
-// CTAs of the backward, each with its own partial sums: at most two an SM
-int bwd_ctas(int64_t rows, int d, int groups) {
-  const int64_t need = (rows + groups - 1) / groups, most = (int64_t)sm_count() * 2;
-  return (int)(need < most ? need : most);
+// Sizes of a launch whose kernel reads `bufs` tensors; the CTAs are as many as
+// are resident (ring and registers), so each walks its rows with a full ring.
+struct Grid {
+  int threads, ctas;
+  size_t smem;
+};
+Grid norm_grid(int64_t rows, int d, int es, int bufs, int regs, NormArgs* a) {
+  const int tpr = threads_per_row(d), groups = groups_of(tpr);
+  const int slot = (d * es + 15) / 16 * 16 + (d * es % 16 ? 16 : 0);
+  Grid g;
+  g.threads = tpr * groups;
+  // as many CTAs as the registers allow, and a ring as deep as their shared memory then does
+  int per = 65536 / (g.threads * regs);
+  const size_t place = (size_t)groups * bufs * slot;
+  while (per > 1 && per * 2 * (place + 1024) > SMEM_SM) --per;
+  int ring = (int)((SMEM_SM / per - 1024) / place);
+  ring = ring > RING ? RING : (ring < 1 ? 1 : ring);
+  g.smem = ring * place;
+  const size_t sums = groups > 1 ? (size_t)2 * d * 4 : 0;  // the backward's sums over groups reuse the ring
+  if (bufs > 1 && g.smem < sums) g.smem = sums;
+  const int64_t need = (rows + groups - 1) / groups, most = (int64_t)sm_count() * per;
+  g.ctas = (int)(need < most ? need : most);
+  if (a != nullptr) {
+    a->tpr = tpr;
+    a->slot = slot;
+    a->ring = ring;
+  }
+  return g;
 }
-// groups of a CTA for the vector and the element path (the partials are sized for either)
-int groups_of(int tpr) { return tpr < NT ? NT / tpr : 1; }
 
-template <typename T, int VN, int NV>
-cudaError_t fwd_n(NormArgs& a, cudaStream_t st) {
-  a.tpr = threads_per_row(a.d, VN, NV);
-  const int groups = groups_of(a.tpr), threads = a.tpr < NT ? NT : a.tpr;
-  const int64_t need = (a.rows + groups - 1) / groups, most = (int64_t)sm_count() * (2048 / threads);
-  return launch_pdl(norm_fwd_kernel<T, VN, NV>, dim3((unsigned)(need < most ? need : most)), dim3(threads), 0, st, a);
+template <typename K>
+cudaError_t launch_rows(K kernel, const Grid& g, const NormArgs& a, bool* attr_done, cudaStream_t st) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!attr_done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_SM);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  return launch_pdl(kernel, dim3(g.ctas), dim3(g.threads), g.smem, st, a);
 }
-template <typename T, int VN, int NV>
-cudaError_t bwd_n(NormArgs& a, cudaStream_t st) {
-  a.tpr = threads_per_row(a.d, VN, NV);
-  const int groups = groups_of(a.tpr), threads = a.tpr < NT ? NT : a.tpr;
-  a.parts = bwd_ctas(a.rows, a.d, groups);
-  const size_t smem = groups > 1 ? (size_t)2 * a.d * 4 : 0;
-  return a.dres ? launch_pdl(norm_bwd_kernel<T, VN, NV, true>, dim3(a.parts), dim3(threads), smem, st, a)
-                : launch_pdl(norm_bwd_kernel<T, VN, NV, false>, dim3(a.parts), dim3(threads), smem, st, a);
+
+template <typename T, bool WHOLE>
+cudaError_t fwd_w(NormArgs& a, cudaStream_t st) {
+  static bool done[64] = {false};
+  const Grid g = norm_grid(a.rows, a.d, sizeof(T), 1, FWD_REGS, &a);
+  return launch_rows(norm_fwd_kernel<T, WHOLE>, g, a, done, st);
+}
+template <typename T, bool WHOLE>
+cudaError_t bwd_w(NormArgs& a, cudaStream_t st) {
+  static bool done[2][64] = {{false}};
+  const Grid g = norm_grid(a.rows, a.d, sizeof(T), a.dres ? 3 : 2, BWD_REGS, &a);
+  a.parts = g.ctas;
+  return a.dres ? launch_rows(norm_bwd_kernel<T, WHOLE, true>, g, a, done[1], st)
+                : launch_rows(norm_bwd_kernel<T, WHOLE, false>, g, a, done[0], st);
 }
 template <typename T>
 cudaError_t fwd_t(NormArgs& a, cudaStream_t st) {
-  constexpr int VN = Vec<T>::N;
   if (wide(a.d)) {
     const int64_t most = (int64_t)sm_count() * 4;
     return launch_pdl(norm_fwd_wide_kernel<T>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(WIDE_NT), 0, st, a);
   }
-  if (a.d % VN == 0) return fwd_n<T, VN, EPT / VN>(a, st);
-  return fwd_n<T, 1, EPT>(a, st);
+  return a.d % Vec<T>::N == 0 ? fwd_w<T, true>(a, st) : fwd_w<T, false>(a, st);
+}
+int wide_ctas(int64_t rows) {
+  const int64_t most = (int64_t)sm_count() * 2;
+  return (int)(rows < most ? rows : most);
 }
 template <typename T>
 cudaError_t bwd_t(NormArgs& a, cudaStream_t st) {
-  constexpr int VN = Vec<T>::N;
   if (wide(a.d)) {
-    a.parts = bwd_ctas(a.rows, a.d, 1);
+    a.parts = wide_ctas(a.rows);
     return launch_pdl(norm_bwd_wide_kernel<T>, dim3(a.parts), dim3(WIDE_NT), 0, st, a);
   }
-  if (a.d % VN == 0) return bwd_n<T, VN, EPT / VN>(a, st);
-  return bwd_n<T, 1, EPT>(a, st);
+  return a.d % Vec<T>::N == 0 ? bwd_w<T, true>(a, st) : bwd_w<T, false>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_fwd(int64_t rows, int d, bool bf16, const void* x, const float* gamma, const float* beta,
-                            float eps, void* y, float* mean, float* rstd, cudaStream_t st) {
+                            float eps, void* y, float* mean, float* rstd, uint32_t* err, cudaStream_t st) {
   NormArgs a{};
   a.x = x;
   a.gamma = gamma;
@@ -424,17 +617,20 @@ cudaError_t launch_norm_fwd(int64_t rows, int d, bool bf16, const void* x, const
   a.rstd = rstd;
   a.rows = rows;
   a.d = d;
+  a.err = err;
   LaunchScope ls(KK_NORM_FWD, st);
   return bf16 ? fwd_t<__nv_bfloat16>(a, st) : fwd_t<float>(a, st);
 }
 
 size_t norm_ws_bytes(int64_t rows, int d) {
-  return (size_t)bwd_ctas(rows, d, 1) * 2 * d * 4;  // one group a CTA makes the most CTAs
+  // the smallest rows (bf16, without a residual) have the most CTAs
+  const int ctas = wide(d) ? wide_ctas(rows) : norm_grid(rows, d, 2, 2, BWD_REGS, nullptr).ctas;
+  return (size_t)ctas * 2 * d * 4;
 }
 
 cudaError_t launch_norm_bwd(int64_t rows, int d, bool bf16, const void* x, const void* dy, const float* gamma,
                             const float* mean, const float* rstd, const void* dres, void* dx, float* dgamma,
-                            float* dbeta, int accumulate, void* ws, cudaStream_t st) {
+                            float* dbeta, int accumulate, void* ws, uint32_t* err, cudaStream_t st) {
   NormArgs a{};
   a.x = x;
   a.dy = dy;
@@ -449,6 +645,7 @@ cudaError_t launch_norm_bwd(int64_t rows, int d, bool bf16, const void* x, const
   a.rows = rows;
   a.d = d;
   a.accumulate = accumulate;
+  a.err = err;
   {
     LaunchScope ls(KK_NORM_BWD, st);
     const cudaError_t e = bf16 ? bwd_t<__nv_bfloat16>(a, st) : bwd_t<float>(a, st);
