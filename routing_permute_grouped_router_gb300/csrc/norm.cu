@@ -32,7 +32,9 @@ namespace {
 
 constexpr int MAX_TPR = 512;   // most threads that share a row held in registers
 constexpr int EPT = 16;        // elements of a row a thread holds
-constexpr int FWD_REGS = 80, BWD_REGS = 128;  // a thread's, so that three and two CTAs of 256 fit an SM
+constexpr int FWD_REGS = 80;   // a thread's in the forward: three CTAs of 256 fit an SM
+constexpr int BWD_NT = 512;    // threads of the backward's CTAs, one an SM (few partial sums)
+constexpr int MAX_GROUPS = BWD_NT / 32;
 constexpr int SMEM_SM = 220 * 1024;             // shared memory of an SM that the rings may take
 constexpr int RING = 4;        // most rows on their way to a group of threads
 constexpr int WIDE_NT = 512;   // threads a CTA of the wide kernels
@@ -76,18 +78,31 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// Every warp of a row gives one float4; each thread gets that of warp
-// lane % warps, so xor shuffles over the warps (`nw`, a power of two) finish a
-// sum.  One barrier; scratch holds a float4 a warp twice, used in turn.
-__device__ __forceinline__ float4 share(float4 v, int nw, float4* scratch, int& turn) {
-  float4* buf = scratch + turn * nw;
-  turn ^= 1;
-  if (threadIdx.x % 32 == 0) buf[threadIdx.x / 32] = v;
-  __syncthreads();
-  return buf[threadIdx.x & (nw - 1)];
-}
-__device__ __forceinline__ float sum_over(float v, int n) {
-  for (int o = 1; o < n; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+// A group of threads: `warps` warps that share a row, the g-th of its CTA.
+// (SEVERAL: the CTA may have several groups of more than a warp.)
+template <bool SEVERAL>
+struct Group {
+  int g, r, tpr, warps;
+  __device__ __forceinline__ explicit Group(int tpr_) : g(threadIdx.x / tpr_), r(threadIdx.x % tpr_), tpr(tpr_), warps(tpr_ / 32) {}
+  __device__ __forceinline__ void sync() const {
+    if (warps == 1) __syncwarp();
+    else if (SEVERAL) asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(tpr) : "memory");
+    else __syncthreads();
+  }
+  // Every warp gives one float4; after sync() each thread gets that of warp
+  // lane % warps, so xor shuffles over the warps (a power of two) finish a
+  // sum.  scratch has two rows of 16, used in turn.
+  __device__ __forceinline__ void give(float4 v, float4* scratch, int turn) const {
+    if (threadIdx.x % 32 == 0) scratch[turn * 16 + threadIdx.x / 32] = v;
+  }
+  __device__ __forceinline__ float4 get(const float4* scratch, int turn) const {
+    return scratch[turn * 16 + g * warps + (threadIdx.x & (warps - 1))];
+  }
+};
+__device__ __forceinline__ float sum_over(float v, int n) {  // n a power of two up to 16
+#pragma unroll
+  for (int o = 1; o <= 8; o *= 2)
+    if (o < n) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -137,52 +152,53 @@ __device__ __forceinline__ Span row_span(int64_t row, int64_t rows, int d) {
   return {a0, (int)(b0 - a0), a1 > a0 ? (int)(a1 - a0) : 0};
 }
 
-// The thread's elements of a row, from the ring (zeros past the row's end).
+// A thread's elements come in chunks, pairs of fp32: a vector of the row, or
+// eight single elements where rows are not whole vectors.
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void take_row(const char* stage, const Span& sp, const T* tensor, int r, int tpr, int d,
-                                         float2 (&v)[EPT / 2]) {
+struct Chunk {
+  static constexpr int N = WHOLE ? Vec<T>::N : 8;
+};
+
+// Chunk i of a row, from the ring (zeros past the row's end).
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void take(const char* stage, const Span& sp, const T* tensor, int r, int tpr, int d, int i,
+                                     float2 (&v)[Chunk<T, WHOLE>::N / 2]) {
   if constexpr (WHOLE) {
-    constexpr int VN = Vec<T>::N;
+    const int q = r + i * tpr;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (q * Vec<T>::N < d) u = *reinterpret_cast<const uint4*>(stage + q * 16);
+    float w[Vec<T>::N];
+    unpack(u, w);
 #pragma unroll
-    for (int i = 0; i < EPT / VN; ++i) {
-      const int q = r + i * tpr;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (q * VN < d) u = *reinterpret_cast<const uint4*>(stage + q * 16);
-      float w[VN];
-      unpack(u, w);
-#pragma unroll
-      for (int j = 0; j < VN; j += 2) v[(i * VN + j) / 2] = make_float2(w[j], w[j + 1]);
-    }
+    for (int j = 0; j < Vec<T>::N; j += 2) v[j / 2] = make_float2(w[j], w[j + 1]);
   } else {
 #pragma unroll
-    for (int c = 0; c < EPT; ++c) {
-      const int e = r + c * tpr, at = sp.skip + e * (int)sizeof(T);
+    for (int j = 0; j < 8; ++j) {
+      const int e = r + (i * 8 + j) * tpr, at = sp.skip + e * (int)sizeof(T);
       float w = 0.f;
       if (e < d)
         w = to_f32(at < sp.bytes ? *reinterpret_cast<const T*>(stage + at) : tensor[(sp.at + at) / (int64_t)sizeof(T)]);
-      (c & 1 ? v[c / 2].y : v[c / 2].x) = w;
+      (j & 1 ? v[j / 2].y : v[j / 2].x) = w;
     }
   }
 }
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void put_row(T* row, int r, int tpr, int d, const float2 (&v)[EPT / 2]) {
+__device__ __forceinline__ void put(T* row, int r, int tpr, int d, int i, const float2 (&v)[Chunk<T, WHOLE>::N / 2]) {
   if constexpr (WHOLE) {
-    constexpr int VN = Vec<T>::N;
+    const int q = r + i * tpr;
+    float w[Vec<T>::N];
 #pragma unroll
-    for (int i = 0; i < EPT / VN; ++i) {
-      const int q = r + i * tpr;
-      float w[VN];
-#pragma unroll
-      for (int j = 0; j < VN; j += 2) {
-        w[j] = v[(i * VN + j) / 2].x;
-        w[j + 1] = v[(i * VN + j) / 2].y;
-      }
-      if (q * VN < d) stg16(row + (size_t)q * VN, pack(w));
+    for (int j = 0; j < Vec<T>::N; j += 2) {
+      w[j] = v[j / 2].x;
+      w[j + 1] = v[j / 2].y;
     }
+    if (q * Vec<T>::N < d) stg16(row + (size_t)q * Vec<T>::N, pack(w));
   } else {
 #pragma unroll
-    for (int c = 0; c < EPT; ++c)
-      if (r + c * tpr < d) row[r + c * tpr] = from_f32<T>(c & 1 ? v[c / 2].y : v[c / 2].x);
+    for (int j = 0; j < 8; ++j) {
+      const int e = r + (i * 8 + j) * tpr;
+      if (e < d) row[e] = from_f32<T>(j & 1 ? v[j / 2].y : v[j / 2].x);
+    }
   }
 }
 
@@ -209,7 +225,7 @@ struct NormArgs {
 
 // A group of tpr threads, its rows (first, first + step, ...) and its ring.
 // The group's first thread starts the copies; a place is filled again once the
-// group has taken its row into registers (after the first reduction).
+// group has read its row for the last time.
 template <typename T, bool WHOLE, int NBUF>
 struct Rows {
   const char* src[NBUF];
@@ -230,14 +246,18 @@ struct Rows {
     }
   }
   __device__ __forceinline__ void wait(uint32_t* err) const { ring_wait(sm_addr(bars + at), phase, err); }
-  __device__ __forceinline__ const char* place(int b) const { return base + (at * NBUF + b) * slot; }
-  // The row in work has been taken: its place gets the row `ring` turns on.
-  __device__ __forceinline__ void taken(int64_t row, bool leader) {
-    if (leader) start(row + ring * step, at);
+  __device__ __forceinline__ const char* place_at(int p, int b) const { return base + (p * NBUF + b) * slot; }
+  __device__ __forceinline__ const char* place(int b) const { return place_at(at, b); }
+  __device__ __forceinline__ void next() {
     if (++at == ring) {
       at = 0;
       phase ^= 1u;
     }
+  }
+  // The row in work has been taken: its place gets the row `ring` turns on.
+  __device__ __forceinline__ void taken(int64_t row, bool leader) {
+    if (leader) start(row + ring * step, at);
+    next();
   }
 };
 
@@ -245,14 +265,14 @@ extern __shared__ __align__(128) char norm_smem[];
 
 template <typename T, bool WHOLE, int NBUF>
 __device__ __forceinline__ Rows<T, WHOLE, NBUF> begin_rows(const NormArgs& a, uint64_t* bars, int r) {
-  const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr;
+  const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr;  // rows go to all CTAs before a second group of any
   Rows<T, WHOLE, NBUF> R;
   R.src[0] = static_cast<const char*>(a.x);
   if (NBUF > 1) R.src[1] = static_cast<const char*>(a.dy);
   if (NBUF > 2) R.src[2] = static_cast<const char*>(a.dres);
   R.base = norm_smem + (size_t)g * a.ring * NBUF * a.slot;
   R.bars = bars + g * RING;
-  R.first = (int64_t)blockIdx.x * groups + g;
+  R.first = (int64_t)g * gridDim.x + blockIdx.x;
   R.step = (int64_t)gridDim.x * groups;
   R.rows = a.rows;
   R.d = a.d;
@@ -282,11 +302,12 @@ __device__ __forceinline__ void take_weights(const float* w, int r, int tpr, int
 
 template <typename T, bool WHOLE>
 __global__ void __maxnreg__(FWD_REGS) norm_fwd_kernel(const NormArgs a) {
-  constexpr int VN = WHOLE ? Vec<T>::N : 1;
-  __shared__ float4 scratch[2 * MAX_TPR / 32];
-  __shared__ uint64_t bars[4 * RING];
+  constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2;
+  __shared__ float4 scratch[2 * 16];
+  __shared__ uint64_t bars[MAX_GROUPS * RING];
   int turn = 0;
-  const int r = threadIdx.x % a.tpr, nw = a.tpr / 32;
+  const Group<false> grp(a.tpr);
+  const int r = grp.r, nw = grp.warps;
   Rows<T, WHOLE, 1> R = begin_rows<T, WHOLE, 1>(a, bars, r);
   T* y = static_cast<T*>(a.out);
   const float inv = 1.f / (float)a.d;
@@ -302,35 +323,50 @@ __global__ void __maxnreg__(FWD_REGS) norm_fwd_kernel(const NormArgs a) {
   for (int64_t row = R.first; row < a.rows; row += R.step) {
     const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
     R.wait(a.err);
-    float2 v[EPT / 2];
-    take_row<T, WHOLE>(R.place(0), sp, static_cast<const T*>(a.x), r, a.tpr, a.d, v);
-    // mean and squared distances of the warp's elements first; the warps then
-    // combine theirs with the distances of their means
-    float2 s2 = both(0.f);
+    float2 v[EPT / 2 / CN][CN], s2 = both(0.f);
 #pragma unroll
-    for (int c = 0; c < EPT / 2; ++c) s2 = add2(s2, v[c]);
-    const float ws = warp_sum(s2.x + s2.y), wmean = ws * winv;
-    s2 = both(0.f);
-    const float2 off = both(-wmean);
+    for (int i = 0; i < EPT / 2 / CN; ++i) {
+      take<T, WHOLE>(R.place(0), sp, static_cast<const T*>(a.x), r, a.tpr, a.d, i, v[i]);
 #pragma unroll
-    for (int c = 0; c < EPT / 2; ++c) {
-      const float2 t = add2(v[c], off);
-      if (in_row<VN>(r, a.tpr, 2 * c, a.d)) s2.x = fmaf(t.x, t.x, s2.x);
-      if (in_row<VN>(r, a.tpr, 2 * c + 1, a.d)) s2.y = fmaf(t.y, t.y, s2.y);
+      for (int c = 0; c < CN; ++c) s2 = add2(s2, v[i][c]);
     }
+    // The warp's mean, the distances from it and their squares first; the
+    // warps then combine theirs with the distances of their means.
+    const float ws = warp_sum(s2.x + s2.y), wmean = ws * winv;
+    const float2 from = both(-wmean);
+    s2 = both(0.f);
+#pragma unroll
+    for (int i = 0; i < EPT / 2 / CN; ++i)
+#pragma unroll
+      for (int c = 0; c < CN; ++c) {
+        const int at = 2 * (i * CN + c);
+        v[i][c] = add2(v[i][c], from);
+        if constexpr (WHOLE) {
+          if (in_row<VN>(r, a.tpr, at, a.d)) s2 = fma2(v[i][c], v[i][c], s2);
+        } else {
+          if (in_row<VN>(r, a.tpr, at, a.d)) s2.x = fmaf(v[i][c].x, v[i][c].x, s2.x);
+          if (in_row<VN>(r, a.tpr, at + 1, a.d)) s2.y = fmaf(v[i][c].y, v[i][c].y, s2.y);
+        }
+      }
     float m2 = warp_sum(s2.x + s2.y), mean = wmean;
     if (nw > 1) {
-      const float4 w = share(make_float4(ws, m2, wmean, wn), nw, scratch, turn);
+      grp.give(make_float4(ws, m2, wmean, wn), scratch, turn);
+      grp.sync();
+      const float4 w = grp.get(scratch, turn);
+      turn ^= 1;
       mean = sum_over(w.x, nw) * inv;
       m2 = sum_over(fmaf(w.w * (w.z - mean), w.z - mean, w.y), nw);
     }
     __syncwarp();
     R.taken(row, r == 0);
-    const float rstd = 1.f / sqrtf(m2 * inv + a.eps);
-    const float2 by = both(rstd), from = both(-mean);
+    const float rstd = rsqrtf(fmaf(m2, inv, a.eps));
+    const float2 by = both(rstd), shift = both((wmean - mean) * rstd);
 #pragma unroll
-    for (int c = 0; c < EPT / 2; ++c) v[c] = fma2(mul2(add2(v[c], from), by), ga[c], be[c]);
-    put_row<T, WHOLE>(y + row * a.d, r, a.tpr, a.d, v);
+    for (int i = 0; i < EPT / 2 / CN; ++i) {
+#pragma unroll
+      for (int c = 0; c < CN; ++c) v[i][c] = fma2(fma2(v[i][c], by, shift), ga[i * CN + c], be[i * CN + c]);
+      put<T, WHOLE>(y + row * a.d, r, a.tpr, a.d, i, v[i]);
+    }
     if (r == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -338,56 +374,98 @@ __global__ void __maxnreg__(FWD_REGS) norm_fwd_kernel(const NormArgs a) {
   }
 }
 
+// A row is read from the ring twice, for the sums and for dx, and the sums of
+// the next row are formed before dx of this one: the reduction's shuffles and
+// barrier run under arithmetic that does not wait for them.  (One row after the
+// other, 32768 x 4096 bf16 took 197 us.)
 template <typename T, bool WHOLE, bool RES>
-__global__ void __maxnreg__(BWD_REGS) norm_bwd_kernel(const NormArgs a) {
-  constexpr int VN = WHOLE ? Vec<T>::N : 1;
-  __shared__ float4 scratch[2 * MAX_TPR / 32];
-  __shared__ uint64_t bars[4 * RING];
-  int turn = 0;
-  const int r = threadIdx.x % a.tpr, nw = a.tpr / 32;
-  Rows<T, WHOLE, RES ? 3 : 2> R = begin_rows<T, WHOLE, RES ? 3 : 2>(a, bars, r);
+__global__ void __launch_bounds__(BWD_NT, 1) norm_bwd_kernel(const NormArgs a) {
+  constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2, NBUF = RES ? 3 : 2;
+  __shared__ float4 scratch[2 * 16];
+  __shared__ uint64_t bars[MAX_GROUPS * RING];
+  const Group<true> grp(a.tpr);
+  const int r = grp.r;
+  Rows<T, WHOLE, NBUF> R = begin_rows<T, WHOLE, NBUF>(a, bars, r);
   T* dx = static_cast<T*>(a.out);
   const float inv = 1.f / (float)a.d;
   float2 ga[EPT / 2], dg[EPT / 2], db[EPT / 2];
   take_weights<VN>(a.gamma, r, a.tpr, a.d, ga);
 #pragma unroll
   for (int c = 0; c < EPT / 2; ++c) dg[c] = db[c] = both(0.f);
-#pragma unroll 1
-  for (int64_t row = R.first; row < a.rows; row += R.step) {
+  const T *x = static_cast<const T*>(a.x), *dy = static_cast<const T*>(a.dy), *res = static_cast<const T*>(a.dres);
+
+  // the warp's sums of row `row`, and its part of dgamma and dbeta
+  auto sums = [&](int64_t row, float2 stat) {
     const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
-    const float rstd = __ldg(a.rstd_in + row), mean = __ldg(a.mean_in + row);
+    const float2 by = both(stat.y), from = both(-stat.x);
     R.wait(a.err);
-    float2 n[EPT / 2], v[EPT / 2], o[EPT / 2];
-    take_row<T, WHOLE>(R.place(0), sp, static_cast<const T*>(a.x), r, a.tpr, a.d, n);
-    take_row<T, WHOLE>(R.place(1), sp, static_cast<const T*>(a.dy), r, a.tpr, a.d, v);
-    if (RES) take_row<T, WHOLE>(R.place(2), sp, static_cast<const T*>(a.dres), r, a.tpr, a.d, o);
     float2 sv = both(0.f), sn = both(0.f);
 #pragma unroll
-    for (int c = 0; c < EPT / 2; ++c) {  // past the row's end dy and gamma are 0
-      n[c] = mul2(add2(n[c], both(-mean)), both(rstd));
-      dg[c] = fma2(v[c], n[c], dg[c]);
-      db[c] = add2(db[c], v[c]);
-      v[c] = mul2(v[c], ga[c]);
-      sv = add2(sv, v[c]);
-      sn = fma2(v[c], n[c], sn);
-    }
-    float m1 = warp_sum(sv.x + sv.y), m2 = warp_sum(sn.x + sn.y);
-    if (nw > 1) {
-      const float4 w = share(make_float4(m1, m2, 0.f, 0.f), nw, scratch, turn);
-      m1 = sum_over(w.x, nw);
-      m2 = sum_over(w.y, nw);
-    }
-    __syncwarp();
-    R.taken(row, r == 0);
-    const float2 k1 = both(-m1 * inv), k2 = both(-m2 * inv), by = both(rstd);
+    for (int i = 0; i < EPT / 2 / CN; ++i) {
+      float2 n[CN], v[CN];
+      take<T, WHOLE>(R.place(0), sp, x, r, a.tpr, a.d, i, n);
+      take<T, WHOLE>(R.place(1), sp, dy, r, a.tpr, a.d, i, v);
 #pragma unroll
-    for (int c = 0; c < EPT / 2; ++c) {
-      const float2 t = fma2(n[c], k2, add2(v[c], k1));
-      o[c] = RES ? fma2(t, by, o[c]) : mul2(t, by);
+      for (int c = 0; c < CN; ++c) {  // past the row's end dy and gamma are 0
+        const int at = i * CN + c;
+        n[c] = mul2(add2(n[c], from), by);
+        dg[at] = fma2(v[c], n[c], dg[at]);
+        db[at] = add2(db[at], v[c]);
+        v[c] = mul2(v[c], ga[at]);
+        sv = add2(sv, v[c]);
+        sn = fma2(v[c], n[c], sn);
+      }
     }
-    put_row<T, WHOLE>(dx + row * a.d, r, a.tpr, a.d, o);
+    return make_float2(warp_sum(sv.x + sv.y), warp_sum(sn.x + sn.y));
+  };
+
+  // mean and rstd of a row, loaded two rows ahead of their use
+  auto stats = [&](int64_t row) {
+    return row < a.rows ? make_float2(__ldg(a.mean_in + row), __ldg(a.rstd_in + row)) : make_float2(0.f, 0.f);
+  };
+  float2 stat = stats(R.first), stat1 = stats(R.first + R.step);
+  int turn = 0, before = 0;  // before: the place of the row whose dx comes next
+  float2 own = make_float2(0.f, 0.f);
+  if (R.first < a.rows) {
+    own = sums(R.first, stat);
+    grp.give(make_float4(own.x, own.y, 0.f, 0.f), scratch, 0);
   }
-  // the CTA's sums: its groups in turn (only warps form several), then one row pair of the partials
+#pragma unroll 1
+  for (int64_t row = R.first; row < a.rows; row += R.step, turn ^= 1) {
+    const float2 stat2 = stats(row + 2 * R.step);
+    grp.sync();  // the row's sums are there, and everyone is done with the row before it
+    if (r == 0 && row != R.first) R.start(row + (R.ring - 1) * R.step, before == 0 ? R.ring - 1 : before - 1);
+    float4 w = grp.get(scratch, turn);
+    const bool alone = grp.warps == 1;
+    const float m1 = alone ? own.x : sum_over(w.x, grp.warps), m2 = alone ? own.y : sum_over(w.y, grp.warps);
+    R.next();
+    if (row + R.step < a.rows) {
+      own = sums(row + R.step, stat1);
+      grp.give(make_float4(own.x, own.y, 0.f, 0.f), scratch, turn ^ 1);
+    }
+    const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
+    const float2 by = both(stat.y), from = both(-stat.x);
+    const float2 k1 = both(-m1 * inv), k2 = both(-m2 * inv);
+#pragma unroll
+    for (int i = 0; i < EPT / 2 / CN; ++i) {
+      float2 n[CN], v[CN], o[CN];
+      take<T, WHOLE>(R.place_at(before, 0), sp, x, r, a.tpr, a.d, i, n);
+      take<T, WHOLE>(R.place_at(before, 1), sp, dy, r, a.tpr, a.d, i, v);
+      if (RES) take<T, WHOLE>(R.place_at(before, 2), sp, res, r, a.tpr, a.d, i, o);
+#pragma unroll
+      for (int c = 0; c < CN; ++c) {
+        n[c] = mul2(add2(n[c], from), by);
+        const float2 t = fma2(n[c], k2, fma2(v[c], ga[i * CN + c], k1));
+        o[c] = RES ? fma2(t, by, o[c]) : mul2(t, by);
+      }
+      put<T, WHOLE>(dx + row * a.d, r, a.tpr, a.d, i, o);
+    }
+    before = R.at;
+    stat = stat1;
+    stat1 = stat2;
+  }
+  __syncthreads();
+  // the CTA's sums: its groups in turn, then one row pair of the partials
   const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr;
   float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
   float* dsum = reinterpret_cast<float*>(norm_smem);  // [2][d], the ring's place: all rows have been taken
@@ -447,7 +525,11 @@ __global__ void __launch_bounds__(RED_COLS * RED_STRIPS) norm_bwd_reduce_kernel(
 
 // ---- rows of more than MAX_TPR * EPT elements: one CTA a row, walked in a loop ----
 __device__ __forceinline__ float2 cta_sum(float2 s, float4* scratch, int& turn) {
-  const float4 w = share(make_float4(warp_sum(s.x), warp_sum(s.y), 0.f, 0.f), WIDE_NT / 32, scratch, turn);
+  const Group<false> all(WIDE_NT);
+  all.give(make_float4(warp_sum(s.x), warp_sum(s.y), 0.f, 0.f), scratch, turn);
+  all.sync();
+  const float4 w = all.get(scratch, turn);
+  turn ^= 1;
   return make_float2(sum_over(w.x, WIDE_NT / 32), sum_over(w.y, WIDE_NT / 32));
 }
 
@@ -522,30 +604,29 @@ int threads_per_row(int d) {
   while (tpr * EPT < d) tpr *= 2;
   return tpr;
 }
-// A CTA is one group of threads, or four warps each with rows of its own.
-int groups_of(int tpr) { return tpr == 32 ? 4 : 1; }
-
-// Sizes of a launch whose kernel reads `bufs` tensors; the CTAs are as many as
-// are resident (ring and registers), so each walks its rows with a full ring.
+// Sizes of a launch whose kernel reads `bufs` tensors.  Forward: CTAs of one
+// group of threads, or of four warps with rows of their own, as many as the
+// registers allow.  Backward: one CTA an SM.  The rings take what shared memory
+// that leaves, up to RING rows.
 struct Grid {
   int threads, ctas;
   size_t smem;
 };
-Grid norm_grid(int64_t rows, int d, int es, int bufs, int regs, NormArgs* a) {
-  const int tpr = threads_per_row(d), groups = groups_of(tpr);
-  const int slot = (d * es + 15) / 16 * 16 + (d * es % 16 ? 16 : 0);
+Grid norm_grid(int64_t rows, int d, int es, int bufs, NormArgs* a) {
+  const bool bwd = bufs > 1;
+  const int tpr = threads_per_row(d), slot = (d * es + 15) / 16 * 16 + (d * es % 16 ? 16 : 0);
+  int groups = bwd ? BWD_NT / tpr : (tpr == 32 ? 4 : 1), per = bwd ? 1 : 65536 / (tpr * groups * FWD_REGS);
+  const size_t place = (size_t)bufs * slot;
+  while (groups > 1 && bwd && groups * 2 * (place + 128) > SMEM_SM) groups /= 2;
+  while (per > 1 && per * 2 * (groups * place + 1024) > SMEM_SM) --per;
+  int ring = (int)((SMEM_SM / per - 1024) / (groups * place));
+  ring = ring > RING ? RING : (ring < 2 ? 2 : ring);
   Grid g;
   g.threads = tpr * groups;
-  // as many CTAs as the registers allow, and a ring as deep as their shared memory then does
-  int per = 65536 / (g.threads * regs);
-  const size_t place = (size_t)groups * bufs * slot;
-  while (per > 1 && per * 2 * (place + 1024) > SMEM_SM) --per;
-  int ring = (int)((SMEM_SM / per - 1024) / place);
-  ring = ring > RING ? RING : (ring < 1 ? 1 : ring);
-  g.smem = ring * place;
+  g.smem = ring * groups * place;
   const size_t sums = groups > 1 ? (size_t)2 * d * 4 : 0;  // the backward's sums over groups reuse the ring
-  if (bufs > 1 && g.smem < sums) g.smem = sums;
-  const int64_t need = (rows + groups - 1) / groups, most = (int64_t)sm_count() * per;
+  if (bwd && g.smem < sums) g.smem = sums;
+  const int64_t need = bwd ? rows : (rows + groups - 1) / groups, most = (int64_t)sm_count() * per;
   g.ctas = (int)(need < most ? need : most);
   if (a != nullptr) {
     a->tpr = tpr;
@@ -571,13 +652,13 @@ cudaError_t launch_rows(K kernel, const Grid& g, const NormArgs& a, bool* attr_d
 template <typename T, bool WHOLE>
 cudaError_t fwd_w(NormArgs& a, cudaStream_t st) {
   static bool done[64] = {false};
-  const Grid g = norm_grid(a.rows, a.d, sizeof(T), 1, FWD_REGS, &a);
+  const Grid g = norm_grid(a.rows, a.d, sizeof(T), 1, &a);
   return launch_rows(norm_fwd_kernel<T, WHOLE>, g, a, done, st);
 }
 template <typename T, bool WHOLE>
 cudaError_t bwd_w(NormArgs& a, cudaStream_t st) {
   static bool done[2][64] = {{false}};
-  const Grid g = norm_grid(a.rows, a.d, sizeof(T), a.dres ? 3 : 2, BWD_REGS, &a);
+  const Grid g = norm_grid(a.rows, a.d, sizeof(T), a.dres ? 3 : 2, &a);
   a.parts = g.ctas;
   return a.dres ? launch_rows(norm_bwd_kernel<T, WHOLE, true>, g, a, done[1], st)
                 : launch_rows(norm_bwd_kernel<T, WHOLE, false>, g, a, done[0], st);
@@ -623,8 +704,7 @@ cudaError_t launch_norm_fwd(int64_t rows, int d, bool bf16, const void* x, const
 }
 
 size_t norm_ws_bytes(int64_t rows, int d) {
-  // the smallest rows (bf16, without a residual) have the most CTAs
-  const int ctas = wide(d) ? wide_ctas(rows) : norm_grid(rows, d, 2, 2, BWD_REGS, nullptr).ctas;
+  const int ctas = wide(d) ? wide_ctas(rows) : norm_grid(rows, d, 2, 2, nullptr).ctas;
   return (size_t)ctas * 2 * d * 4;
 }
 
