@@ -281,45 +281,57 @@ def moe_layer_bwd(cfg, weights: dict, x, dy, saved: dict, dx, grads: dict, accum
 
 
 # ----------------------------- around the layer -------------------------- #
-def _same(name: str, t, like, dtype=None) -> Optional[int]:
-    """Pointer of ``t`` (or None), which has to be as large as ``like`` and of its (or the given) type."""
+# These calls can be a few microseconds long on the GPU, so they keep the
+# marshalling short: one helper a tensor, types resolved once.
+_types = None
+
+
+def _torch_types():
+    """(float32, int32, {dtype: moe_dtype}, raw stream of a device), resolved at the first call."""
+    global _types
+    if _types is None:
+        import torch
+
+        _types = (torch.float32, torch.int32, {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32},
+                  torch._C._cuda_getCurrentRawStream)
+    return _types
+
+
+def _arg(name: str, t, n: int, dtype) -> Optional[int]:
+    """Pointer of a dense CUDA tensor of ``n`` elements of ``dtype``; None for None."""
     if t is None:
         return None
-    if t.dtype != (like.dtype if dtype is None else dtype):
-        raise TypeError(f"{name} has type {t.dtype}")
-    if t.numel() != like.numel():
-        raise ValueError(f"{name} has {t.numel()} elements, not {like.numel()}")
-    return _ptr(t)
-
-
-def _vec(name: str, t, n: int, dtype=None) -> Optional[int]:
-    """Pointer of ``t`` (or None), which has to have ``n`` elements of float32 (or the given type)."""
-    if t is None:
-        return None
-    import torch
-
-    if t.dtype != (torch.float32 if dtype is None else dtype):
-        raise TypeError(f"{name} has type {t.dtype}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has type {t.dtype}, not {dtype}")
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} elements, not {n}")
-    return _ptr(t)
-
-
-def _dtype(t) -> int:
-    import torch
-
-    if t.dtype == torch.bfloat16:
-        return MOE_BF16
-    if t.dtype == torch.float32:
-        return MOE_F32
-    raise TypeError(f"expected a bfloat16 or float32 tensor, not {t.dtype}")
+    if n == 0:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _rows(x):
-    """(rows, d) of [..., d]."""
-    if x.dim() < 1 or x.shape[-1] < 1:
+    """(rows, d, moe_dtype) of [..., d]."""
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
         raise ValueError("expected rows of at least one element")
-    return x.numel() // x.shape[-1], x.shape[-1]
+    return x.numel() // shape[-1], shape[-1], _dtype(x)
+
+
+def _dtype(t) -> int:
+    code = _torch_types()[2].get(t.dtype)
+    if code is None:
+        raise TypeError(f"expected a bfloat16 or float32 tensor, not {t.dtype}")
+    return code
+
+
+def _stream_of(t, stream) -> int:
+    """The given stream, else the current one of the device of ``t``."""
+    return _types[3](t.get_device()) if stream is None else stream.cuda_stream
 
 
 def moe_layer_decode(cfg: MoeConfig, weights: dict, x, residual, y, ids, gates, ws, stream=None) -> None:
@@ -327,45 +339,54 @@ def moe_layer_decode(cfg: MoeConfig, weights: dict, x, residual, y, ids, gates, 
 
     ``residual``, ``ids`` [T, k] int32 and ``gates`` [T, k] float32 may be None.
     """
-    import torch
-
-    n, Tk = cfg.T * cfg.d_model, cfg.T * cfg.k
-    act = torch.bfloat16 if cfg.dtype == MOE_BF16 else torch.float32
-    w = _weights(weights)
+    f32, i32, codes, _ = _torch_types()
+    act = x.dtype
+    if codes.get(act) != cfg.dtype:
+        raise TypeError(f"x has type {act}, not the layer's")
+    T, d, E, wn = cfg.T, cfg.d_model, cfg.E, cfg.E * cfg.d_model * cfg.d_ff
+    n = T * d
+    w = MoeWeights(_arg("W_r", weights["W_r"], d * E, f32), _arg("bias", weights.get("bias"), E, f32),
+                   _arg("W1", weights["W1"], wn, act), _arg("W3", weights["W3"], wn, act),
+                   _arg("W2", weights["W2"], wn, act))
     _check("moe_layer_decode", lib().moe_layer_decode(
-        ctypes.byref(cfg), ctypes.byref(w), _vec("x", x, n, act), _vec("residual", residual, n, act),
-        _vec("y", y, n, act), _vec("ids", ids, Tk, torch.int32), _vec("gates", gates, Tk), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)))
+        cfg, w, _arg("x", x, n, act), _arg("residual", residual, n, act), _arg("y", y, n, act),
+        _arg("ids", ids, T * cfg.k, i32), _arg("gates", gates, T * cfg.k, f32), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream_of(ws, stream)))
 
 
 def moe_norm_fwd(x, gamma, beta, eps: float, y, mean=None, rstd=None, stream=None) -> None:
     """Layer norm of the rows of x [..., d]; ``mean`` and ``rstd`` [rows] float32 are kept for the backward."""
-    rows, d = _rows(x)
+    rows, d, code = _rows(x)
+    f32, t, n = _types[0], x.dtype, rows * d
     _check("moe_norm_fwd", lib().moe_norm_fwd(
-        rows, d, _dtype(x), _ptr(x), _vec("gamma", gamma, d), _vec("beta", beta, d), eps, _same("y", y, x),
-        _vec("mean", mean, rows), _vec("rstd", rstd, rows), _stream(stream)))
+        rows, d, code, _arg("x", x, n, t), _arg("gamma", gamma, d, f32), _arg("beta", beta, d, f32), eps,
+        _arg("y", y, n, t), _arg("mean", mean, rows, f32), _arg("rstd", rstd, rows, f32), _stream_of(gamma, stream)))
 
 
 def moe_norm_bwd(x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, accumulate: bool, ws, stream=None) -> None:
     """dx (+ dres), dgamma and dbeta of the layer norm; ``dres`` may be None."""
-    rows, d = _rows(x)
+    rows, d, code = _rows(x)
+    f32, t, n = _types[0], x.dtype, rows * d
     _check("moe_norm_bwd", lib().moe_norm_bwd(
-        rows, d, _dtype(x), _ptr(x), _same("dy", dy, x), _vec("gamma", gamma, d), _vec("mean", mean, rows),
-        _vec("rstd", rstd, rows), _same("dres", dres, x), _same("dx", dx, x), _vec("dgamma", dgamma, d),
-        _vec("dbeta", dbeta, d), int(accumulate), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        rows, d, code, _arg("x", x, n, t), _arg("dy", dy, n, t), _arg("gamma", gamma, d, f32),
+        _arg("mean", mean, rows, f32), _arg("rstd", rstd, rows, f32), _arg("dres", dres, n, t), _arg("dx", dx, n, t),
+        _arg("dgamma", dgamma, d, f32), _arg("dbeta", dbeta, d, f32), accumulate, _ptr(ws),
+        ws.numel() * ws.element_size(), _stream_of(gamma, stream)))
 
 
 def moe_dropout_add(y, residual, out, p: float, seed: int, offset: int, stream=None) -> None:
     """out = residual + dropout(y), the mask drawn from (seed, offset, element); ``residual`` may be None."""
+    code, n, t = _dtype(y), y.numel(), y.dtype
     _check("moe_dropout_add", lib().moe_dropout_add(
-        y.numel(), _dtype(y), _ptr(y), _same("residual", residual, y), _same("out", out, y), p, seed, offset,
-        _stream(stream)))
+        n, code, _arg("y", y, n, t), _arg("residual", residual, n, t), _arg("out", out, n, t), p, seed, offset,
+        _stream_of(y, stream)))
 
 
 def moe_dropout_bwd(dout, dy, p: float, seed: int, offset: int, stream=None) -> None:
     """dy = the gradient of dropout(y), with the mask of the same seed and offset."""
+    code, n, t = _dtype(dout), dout.numel(), dout.dtype
     _check("moe_dropout_bwd", lib().moe_dropout_bwd(
-        dout.numel(), _dtype(dout), _ptr(dout), _same("dy", dy, dout), p, seed, offset, _stream(stream)))
+        n, code, _arg("dout", dout, n, t), _arg("dy", dy, n, t), p, seed, offset, _stream_of(dout, stream)))
 
 
 def moe_get_device_error(clear: bool = True):

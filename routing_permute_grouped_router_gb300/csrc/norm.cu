@@ -141,15 +141,16 @@ __device__ __noinline__ void ring_wait(uint32_t bar, uint32_t parity, uint32_t* 
 struct Span {
   int64_t at;       // byte offset of the copy in the tensor
   int skip, bytes;  // bytes before the row's first element; bytes of the copy
+  bool whole;       // it has all of the row
 };
 template <typename T, bool WHOLE>
 __device__ __forceinline__ Span row_span(int64_t row, int64_t rows, int d) {
   const int64_t b0 = row * d * (int64_t)sizeof(T), b1 = b0 + d * (int64_t)sizeof(T);
-  if (WHOLE) return {b0, 0, (int)(b1 - b0)};
+  if (WHOLE) return {b0, 0, (int)(b1 - b0), true};
   const int64_t total = rows * d * (int64_t)sizeof(T), a0 = b0 & ~(int64_t)15;
   int64_t a1 = (b1 + 15) & ~(int64_t)15;
   if (a1 > total) a1 = total & ~(int64_t)15;
-  return {a0, (int)(b0 - a0), a1 > a0 ? (int)(a1 - a0) : 0};
+  return {a0, (int)(b0 - a0), a1 > a0 ? (int)(a1 - a0) : 0, a1 >= b1};
 }
 
 // A thread's elements come in chunks, pairs of fp32: a vector of the row, or
@@ -172,13 +173,23 @@ __device__ __forceinline__ void take(const char* stage, const Span& sp, const T*
 #pragma unroll
     for (int j = 0; j < Vec<T>::N; j += 2) v[j / 2] = make_float2(w[j], w[j + 1]);
   } else {
+    const int step = tpr * (int)sizeof(T), left = ((d - r + tpr - 1) >> (31 - __clz(tpr))) - i * 8;  // the thread's elements from here on
+    int at = sp.skip + (r + i * 8 * tpr) * (int)sizeof(T);
+    if (sp.whole) {
+      const char* p = stage + at;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = r + (i * 8 + j) * tpr, at = sp.skip + e * (int)sizeof(T);
-      float w = 0.f;
-      if (e < d)
-        w = to_f32(at < sp.bytes ? *reinterpret_cast<const T*>(stage + at) : tensor[(sp.at + at) / (int64_t)sizeof(T)]);
-      (j & 1 ? v[j / 2].y : v[j / 2].x) = w;
+      for (int j = 0; j < 8; ++j, p += step) {
+        const float w = j < left ? to_f32(*reinterpret_cast<const T*>(p)) : 0.f;
+        (j & 1 ? v[j / 2].y : v[j / 2].x) = w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j, at += step) {
+        float w = 0.f;
+        if (j < left)
+          w = to_f32(at < sp.bytes ? *reinterpret_cast<const T*>(stage + at) : tensor[(sp.at + at) / (int64_t)sizeof(T)]);
+        (j & 1 ? v[j / 2].y : v[j / 2].x) = w;
+      }
     }
   }
 }
@@ -194,11 +205,11 @@ __device__ __forceinline__ void put(T* row, int r, int tpr, int d, int i, const 
     }
     if (q * Vec<T>::N < d) stg16(row + (size_t)q * Vec<T>::N, pack(w));
   } else {
+    const int left = ((d - r + tpr - 1) >> (31 - __clz(tpr))) - i * 8;
+    T* p = row + r + i * 8 * tpr;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = r + (i * 8 + j) * tpr;
-      if (e < d) row[e] = from_f32<T>(j & 1 ? v[j / 2].y : v[j / 2].x);
-    }
+    for (int j = 0; j < 8; ++j, p += tpr)
+      if (j < left) *p = from_f32<T>(j & 1 ? v[j / 2].y : v[j / 2].x);
   }
 }
 
@@ -465,31 +476,26 @@ __global__ void __launch_bounds__(BWD_NT, 1) norm_bwd_kernel(const NormArgs a) {
     stat1 = stat2;
   }
   __syncthreads();
-  // the CTA's sums: its groups in turn, then one row pair of the partials
-  const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr;
+  // the CTA's sums, over its groups in order, are one row pair of the partials
+  const int groups = blockDim.x / a.tpr;
   float* out = a.partial + (size_t)blockIdx.x * 2 * a.d;
-  float* dsum = reinterpret_cast<float*>(norm_smem);  // [2][d], the ring's place: all rows have been taken
-  for (int t = 0; t < groups; ++t) {
-    if (groups > 1) __syncthreads();
-    if (g != t) continue;
+  float* mine = groups == 1 ? out : reinterpret_cast<float*>(norm_smem) + (size_t)grp.g * 2 * a.d;
 #pragma unroll
-    for (int c = 0; c < EPT; ++c) {
-      const int col = column<VN>(r, a.tpr, c);
-      if (in_row<VN>(r, a.tpr, c, a.d)) {
-        float u = c & 1 ? dg[c / 2].y : dg[c / 2].x, w = c & 1 ? db[c / 2].y : db[c / 2].x;
-        if (t > 0) {
-          u += dsum[col];
-          w += dsum[a.d + col];
-        }
-        if (t == groups - 1) {
-          out[col] = u;
-          out[a.d + col] = w;
-        } else {
-          dsum[col] = u;
-          dsum[a.d + col] = w;
-        }
-      }
+  for (int c = 0; c < EPT; ++c) {
+    const int col = column<VN>(r, a.tpr, c);
+    if (in_row<VN>(r, a.tpr, c, a.d)) {
+      mine[col] = c & 1 ? dg[c / 2].y : dg[c / 2].x;
+      mine[a.d + col] = c & 1 ? db[c / 2].y : db[c / 2].x;
     }
+  }
+  if (groups == 1) return;
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(norm_smem);
+  for (int i = threadIdx.x; i < 2 * a.d; i += blockDim.x) {
+    float u = 0.f;
+#pragma unroll 4
+    for (int g = 0; g < groups; ++g) u += all[(size_t)g * 2 * a.d + i];
+    out[i] = u;
   }
 }
 
@@ -624,7 +630,7 @@ Grid norm_grid(int64_t rows, int d, int es, int bufs, NormArgs* a) {
   Grid g;
   g.threads = tpr * groups;
   g.smem = ring * groups * place;
-  const size_t sums = groups > 1 ? (size_t)2 * d * 4 : 0;  // the backward's sums over groups reuse the ring
+  const size_t sums = groups > 1 ? (size_t)groups * 2 * d * 4 : 0;  // the backward's groups' sums take the ring's place
   if (bwd && g.smem < sums) g.smem = sums;
   const int64_t need = bwd ? rows : (rows + groups - 1) / groups, most = (int64_t)sm_count() * per;
   g.ctas = (int)(need < most ? need : most);

@@ -144,11 +144,16 @@ def test_binding_refuses_mismatched_tensors(lib):
         pkg.moe_norm_fwd(x, v, v, 1e-5, x)
     with pytest.raises(TypeError):
         pkg.moe_dropout_add(x.half(), None, x.half(), 0.1, 0, 0)
+    f32 = torch.float32
     with pytest.raises(TypeError):
-        pkg._same("y", x.bfloat16(), x)
+        pkg._arg("y", x.bfloat16(), 32, f32)
     with pytest.raises(ValueError):
-        pkg._same("y", x[:2], x)
+        pkg._arg("y", x[:2], 32, f32)
     with pytest.raises(ValueError):
-        pkg._vec("gamma", v, 9)
+        pkg._arg("gamma", v, 9, f32)
+    with pytest.raises(ValueError):
+        pkg._arg("y", x.t(), 32, f32)
+    assert pkg._arg("residual", None, 32, f32) is None
+    cfg = pkg.config(4, 8, 8, 2, 1, dtype=pkg.MOE_F32)
     with pytest.raises(TypeError):
-        pkg._vec("gamma", v.double(), 8)
+        pkg.moe_layer_decode(cfg, {}, x.bfloat16(), None, x, None, None, x)
