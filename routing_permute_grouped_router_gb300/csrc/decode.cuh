@@ -98,6 +98,16 @@ struct Split {
   }
 };
 
+// Few rows: the partial sums of the up product go straight to the CTAs of the
+// down product, which add them and make h for themselves.  That repeats the
+// sums in every column tile of y but saves an exchange: the CTAs of a split
+// tile add a share of its parts each and write h, and all wait for that (a
+// fence, a wait and a barrier of some 2 us each under load).
+constexpr int DEC_DIRECT = 64;  // most picks of such a call
+__device__ __forceinline__ bool few_rows(const DecodeArgs& a, const Routing& R) {
+  return a.T * a.k <= DEC_DIRECT && R.nact > 0 && R.rows <= 2 * R.nact;
+}
+
 // ---- scores ----
 // The kernel runs once through most of its code, and every 128-byte line of
 // it that is not yet in an SM's instruction cache costs an L2 or DRAM latency:

@@ -35,7 +35,6 @@ constexpr int TC_TILE = DEC_N * TC_KB * 2;  // 16 KB: two boxes of 64 columns x 
 constexpr int TC_MAX_ST = 8;
 constexpr int TC_SLOT = 2 * TC_TILE + 8192;  // and 64 tokens of x, or two units' hi and lo of 16 rows of h
 constexpr int TC_QUEUE = 6;
-constexpr int TC_DIRECT_ROWS = 64;  // most picks of a call whose CTAs build h themselves
 constexpr int TC_SMEM_MAX = 232448;       // 227 KB a CTA
 constexpr uint32_t TC_COLS = 256;         // TMEM: two accumulators of a and b, 64 tokens each
 constexpr uint32_t TC_BUF = 128, TC_B = 64;
@@ -286,11 +285,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
   const int u0 = up.begin(c), u1 = up.begin(c + 1), v0 = down.begin(c), v1 = down.begin(c + 1);
   uint32_t* bar = a.ctr + 2 * G;  // h of half 0, of half 1, the partial sums of y
   const int64_t dslot = (int64_t)a.T * DEC_N, pslot = (int64_t)a.T * 2 * DEC_N;
-  // Few rows: the partial sums of the up product go straight to the CTAs of the
-  // down product, which add them and make h for themselves.  That repeats the
-  // sums in every column tile of y but saves an exchange (a fence, a wait and a
-  // barrier of some 2 us each under load).
-  const bool direct = a.T * a.k <= TC_DIRECT_ROWS && R.rows <= 2 * R.nact;
+  const bool direct = few_rows(a, R);
 
   if (warp == 0) {
     // ---- weights ----
@@ -796,7 +791,7 @@ int h_blocks(const Shape& s) {
 }  // namespace
 
 size_t decode_tc_whole_bytes(const Shape& s) {
-  return s.T * s.k <= TC_DIRECT_ROWS ? (size_t)s.T * s.k * s.f * 8 : 0;
+  return s.T * s.k <= DEC_DIRECT ? (size_t)s.T * s.k * s.f * 8 : 0;
 }
 size_t decode_tc_h_bytes(const Shape& s) { return (size_t)(s.f / 64) * h_blocks(s) * 4096; }
 

@@ -18,7 +18,8 @@
 namespace moe {
 namespace {
 
-constexpr int DROP_THREADS = 256;
+constexpr int DROP_THREADS = 256, BATCH = 2;
+constexpr int DROP_CTAS = 8;  // an SM
 
 struct DropArgs {
   const void* y;
@@ -56,13 +57,13 @@ __device__ __forceinline__ void drop8(float (&v)[8], const uint4& u, uint32_t cu
   }
 }
 
-// plain loads, not the read-only path: out may be y or the residual
+// the eight values of a block's vectors (loaded plainly, not on the read-only path: out may be y or the residual)
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+__device__ __forceinline__ void expand(const uint4 (&u)[8 / Vec<T>::N], float (&v)[8]) {
 #pragma unroll
   for (int q = 0; q < 8 / Vec<T>::N; ++q) {
     float w[Vec<T>::N];
-    unpack(*reinterpret_cast<const uint4*>(p + q * Vec<T>::N), w);
+    unpack(u[q], w);
 #pragma unroll
     for (int i = 0; i < Vec<T>::N; ++i) v[q * Vec<T>::N + i] = w[i];
   }
@@ -84,28 +85,46 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const DropArgs a)
   const T* y = static_cast<const T*>(a.y);
   const T* res = static_cast<const T*>(a.residual);
   T* out = static_cast<T*>(a.out);
-  const int64_t blocks = (a.n + 7) / 8, step = (int64_t)gridDim.x * DROP_THREADS;
-  for (int64_t b = (int64_t)blockIdx.x * DROP_THREADS + threadIdx.x; b < blocks; b += step) {
-    const int64_t i0 = b * 8;
-    float v[8], r[8];
-    if (i0 + 8 <= a.n) {
-      load8(y + i0, v);
-      if (RES) load8(res + i0, r);
+  const int64_t whole = a.n / 8, step = (int64_t)gridDim.x * DROP_THREADS;
+  // BATCH blocks of a thread are loaded before the first is drawn for
+  for (int64_t b0 = (int64_t)blockIdx.x * DROP_THREADS + threadIdx.x; b0 < whole; b0 += BATCH * step) {
+    uint4 u[BATCH][8 / Vec<T>::N], w[BATCH][8 / Vec<T>::N];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j)
+      if (b0 + j * step < whole) {
+#pragma unroll
+        for (int q = 0; q < 8 / Vec<T>::N; ++q) {
+          u[j][q] = *reinterpret_cast<const uint4*>(y + (b0 + j * step) * 8 + q * Vec<T>::N);
+          if (RES) w[j][q] = *reinterpret_cast<const uint4*>(res + (b0 + j * step) * 8 + q * Vec<T>::N);
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      const int64_t b = b0 + j * step;
+      if (b >= whole) break;
+      float v[8];
+      expand<T>(u[j], v);
       drop8(v, philox((uint64_t)b, a.offset, a.seed), a.cut, a.scale);
       if (RES) {
+        float r[8];
+        expand<T>(w[j], r);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += r[i];
       }
-      store8(out + i0, v);
-    } else {  // the last, short block
-      const int m = (int)(a.n - i0);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < m ? to_f32(y[i0 + i]) : 0.f;
-      drop8(v, philox((uint64_t)b, a.offset, a.seed), a.cut, a.scale);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < m) out[i0 + i] = from_f32<T>(RES ? v[i] + to_f32(res[i0 + i]) : v[i]);
+      store8(out + b * 8, v);
     }
+  }
+  // the last, short block
+  if (a.n % 8 != 0 && blockIdx.x == 0 && threadIdx.x == 0) {
+    const int64_t i0 = whole * 8;
+    const int m = (int)(a.n - i0);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < m ? to_f32(y[i0 + i]) : 0.f;
+    drop8(v, philox((uint64_t)whole, a.offset, a.seed), a.cut, a.scale);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < m) out[i0 + i] = from_f32<T>(RES ? v[i] + to_f32(res[i0 + i]) : v[i]);
   }
 }
 
@@ -114,7 +133,7 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const DropArgs a)
 cudaError_t launch_dropout(int kind, int64_t n, bool bf16, const void* y, const void* residual, void* out,
                            uint32_t cut, uint64_t seed, uint64_t offset, cudaStream_t st) {
   const DropArgs a{y, residual, out, n, seed, offset, cut, (float)(65536.0 / (65536.0 - cut))};
-  const int64_t need = ((n + 7) / 8 + DROP_THREADS - 1) / DROP_THREADS, most = (int64_t)sm_count() * 8;
+  const int64_t need = ((n + 7) / 8 + DROP_THREADS - 1) / DROP_THREADS, most = (int64_t)sm_count() * DROP_CTAS;
   const dim3 grid((unsigned)(need < most ? need : most)), block(DROP_THREADS);
   LaunchScope ls(kind, st);
   if (bf16)
