@@ -18,8 +18,7 @@
 namespace moe {
 namespace {
 
-constexpr int DROP_THREADS = 256, BATCH = 2;
-constexpr int DROP_CTAS = 8;  // an SM
+constexpr int DROP_THREADS = 256;
 
 struct DropArgs {
   const void* y;
@@ -79,39 +78,70 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   }
 }
 
+// How a type and direction walk their blocks.  bf16 with a residual, whose
+// loads and draws take about as long, loads the next block before it draws for
+// this one (2^27 values: 121 us; two blocks loaded and then drawn for: 136).
+// The others draw for two blocks loaded together: without a residual the
+// 32-bit products of the draws bound bf16 (97 us; the next blocks loaded ahead:
+// 103), and float32 is at HBM's rate either way (2^26 values: 116 and 119).
 template <typename T, bool RES>
-__global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const DropArgs a) {
+struct Walk {
+  static constexpr bool AHEAD = RES && sizeof(T) == 2;
+  static constexpr int B = AHEAD ? 1 : 2;
+  static constexpr int RESIDENT = AHEAD ? 6 : 1;  // CTAs an SM that the registers are kept down for
+  static constexpr int CTAS = AHEAD ? 12 : 8;     // launched an SM
+};
+
+template <typename T, bool RES>
+__global__ void __launch_bounds__(DROP_THREADS, Walk<T, RES>::RESIDENT) dropout_kernel(const DropArgs a) {
   pdl_enter();  // see pdl_wait: no global access before this
+  constexpr int Q = 8 / Vec<T>::N, B = Walk<T, RES>::B;
+  constexpr bool AHEAD = Walk<T, RES>::AHEAD;
   const T* y = static_cast<const T*>(a.y);
   const T* res = static_cast<const T*>(a.residual);
   T* out = static_cast<T*>(a.out);
   const int64_t whole = a.n / 8, step = (int64_t)gridDim.x * DROP_THREADS;
-  // BATCH blocks of a thread are loaded before the first is drawn for
-  for (int64_t b0 = (int64_t)blockIdx.x * DROP_THREADS + threadIdx.x; b0 < whole; b0 += BATCH * step) {
-    uint4 u[BATCH][8 / Vec<T>::N], w[BATCH][8 / Vec<T>::N];
+  auto load = [&](const T* p, int64_t b, uint4 (&u)[B][Q]) {
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j)
-      if (b0 + j * step < whole) {
+    for (int j = 0; j < B; ++j)
+      if (b + j * step < whole) {
 #pragma unroll
-        for (int q = 0; q < 8 / Vec<T>::N; ++q) {
-          u[j][q] = *reinterpret_cast<const uint4*>(y + (b0 + j * step) * 8 + q * Vec<T>::N);
-          if (RES) w[j][q] = *reinterpret_cast<const uint4*>(res + (b0 + j * step) * 8 + q * Vec<T>::N);
+        for (int q = 0; q < Q; ++q) u[j][q] = *reinterpret_cast<const uint4*>(p + (b + j * step) * 8 + q * Vec<T>::N);
+      }
+  };
+  int64_t b0 = (int64_t)blockIdx.x * DROP_THREADS + threadIdx.x;
+  uint4 u[B][Q], w[B][Q], u1[B][Q], w1[B][Q];
+  if (AHEAD) {
+    load(y, b0, u);
+    if (RES) load(res, b0, w);
+  }
+#pragma unroll 1
+  for (; b0 < whole; b0 += B * step) {
+    load(y, AHEAD ? b0 + B * step : b0, AHEAD ? u1 : u);
+    if (RES) load(res, AHEAD ? b0 + B * step : b0, AHEAD ? w1 : w);
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      const int64_t b = b0 + j * step;
+      if (b < whole) {
+        const uint4 draws = philox((uint64_t)b, a.offset, a.seed);
+        float v[8];
+        expand<T>(u[j], v);
+        drop8(v, draws, a.cut, a.scale);
+        if (RES) {
+          float r[8];
+          expand<T>(w[j], r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += r[i];
+        }
+        store8(out + b * 8, v);
+      }
+      if (AHEAD) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          u[j][q] = u1[j][q];
+          w[j][q] = w1[j][q];
         }
       }
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const int64_t b = b0 + j * step;
-      if (b >= whole) break;
-      float v[8];
-      expand<T>(u[j], v);
-      drop8(v, philox((uint64_t)b, a.offset, a.seed), a.cut, a.scale);
-      if (RES) {
-        float r[8];
-        expand<T>(w[j], r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
-      }
-      store8(out + b * 8, v);
     }
   }
   // the last, short block
@@ -128,19 +158,21 @@ __global__ void __launch_bounds__(DROP_THREADS) dropout_kernel(const DropArgs a)
   }
 }
 
+template <typename T, bool RES>
+cudaError_t launch_drop(const DropArgs& a, cudaStream_t st) {
+  using W = Walk<T, RES>;
+  const int64_t need = ((a.n + 7) / 8 + DROP_THREADS - 1) / DROP_THREADS, most = (int64_t)sm_count() * W::CTAS;
+  return launch_pdl(dropout_kernel<T, RES>, dim3((unsigned)(need < most ? need : most)), dim3(DROP_THREADS), 0, st, a);
+}
+
 }  // namespace
 
 cudaError_t launch_dropout(int kind, int64_t n, bool bf16, const void* y, const void* residual, void* out,
                            uint32_t cut, uint64_t seed, uint64_t offset, cudaStream_t st) {
   const DropArgs a{y, residual, out, n, seed, offset, cut, (float)(65536.0 / (65536.0 - cut))};
-  const int64_t need = ((n + 7) / 8 + DROP_THREADS - 1) / DROP_THREADS, most = (int64_t)sm_count() * DROP_CTAS;
-  const dim3 grid((unsigned)(need < most ? need : most)), block(DROP_THREADS);
   LaunchScope ls(kind, st);
-  if (bf16)
-    return residual ? launch_pdl(dropout_kernel<__nv_bfloat16, true>, grid, block, 0, st, a)
-                    : launch_pdl(dropout_kernel<__nv_bfloat16, false>, grid, block, 0, st, a);
-  return residual ? launch_pdl(dropout_kernel<float, true>, grid, block, 0, st, a)
-                  : launch_pdl(dropout_kernel<float, false>, grid, block, 0, st, a);
+  if (bf16) return residual ? launch_drop<__nv_bfloat16, true>(a, st) : launch_drop<__nv_bfloat16, false>(a, st);
+  return residual ? launch_drop<float, true>(a, st) : launch_drop<float, false>(a, st);
 }
 
 }  // namespace moe
