@@ -22,8 +22,9 @@
 // A copy has to begin and end on 16 bytes.  Rows of another length are copied
 // with up to 15 bytes more on either side and read from shared memory element
 // by element; what that would read past the tensor's end is loaded directly.
-// Rows of more than 8192 elements are walked in a loop (the wide kernels) and
-// read again from cache.
+// Rows of more than 8192 elements are walked in a loop (the wide kernels),
+// again from cache for each pass, and the backward reads x and dy once more for
+// dgamma and dbeta.
 #include "block.h"
 #include "common.cuh"
 
@@ -529,7 +530,8 @@ __global__ void __launch_bounds__(RED_COLS * RED_STRIPS) norm_bwd_reduce_kernel(
   }
 }
 
-// ---- rows of more than MAX_TPR * EPT elements: one CTA a row, walked in a loop ----
+// ---- rows of more than MAX_TPR * EPT elements: one CTA a row, walked in a
+// loop, again from cache for each pass; dgamma and dbeta in a pass of their own ----
 __device__ __forceinline__ float2 cta_sum(float2 s, float4* scratch, int& turn) {
   const Group<false> all(WIDE_NT);
   all.give(make_float4(warp_sum(s.x), warp_sum(s.y), 0.f, 0.f), scratch, turn);
@@ -539,7 +541,34 @@ __device__ __forceinline__ float2 cta_sum(float2 s, float4* scratch, int& turn) 
   return make_float2(sum_over(w.x, WIDE_NT / 32), sum_over(w.y, WIDE_NT / 32));
 }
 
-template <typename T>
+// VN elements: a 16-byte vector, or one
+template <typename T, int VN>
+__device__ __forceinline__ void ld_n(const T* p, float (&v)[VN]) {
+  if constexpr (VN == 1) v[0] = to_f32(*p);
+  else unpack(*reinterpret_cast<const uint4*>(p), v);
+}
+template <int VN>
+__device__ __forceinline__ void ld_w(const float* p, float (&v)[VN]) {  // of the weights
+  if constexpr (VN == 1) {
+    v[0] = __ldg(p);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VN; j += 4) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(p + j));
+      v[j] = w.x;
+      v[j + 1] = w.y;
+      v[j + 2] = w.z;
+      v[j + 3] = w.w;
+    }
+  }
+}
+template <typename T, int VN>
+__device__ __forceinline__ void st_n(T* p, const float (&v)[VN]) {
+  if constexpr (VN == 1) *p = from_f32<T>(v[0]);
+  else stg16(p, pack(v));
+}
+
+template <typename T, int VN>
 __global__ void __launch_bounds__(WIDE_NT) norm_fwd_wide_kernel(const NormArgs a) {
   pdl_enter();
   __shared__ float4 scratch[2 * WIDE_NT / 32];
@@ -549,16 +578,33 @@ __global__ void __launch_bounds__(WIDE_NT) norm_fwd_wide_kernel(const NormArgs a
     const T* xr = static_cast<const T*>(a.x) + row * a.d;
     T* yr = static_cast<T*>(a.out) + row * a.d;
     float s = 0.f;
-    for (int i = threadIdx.x; i < a.d; i += WIDE_NT) s += to_f32(xr[i]);
+#pragma unroll 4
+    for (int i = threadIdx.x * VN; i < a.d; i += WIDE_NT * VN) {
+      float v[VN];
+      ld_n<T, VN>(xr + i, v);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) s += v[j];
+    }
     const float mean = cta_sum(make_float2(s, 0.f), scratch, turn).x * inv;
     s = 0.f;
-    for (int i = threadIdx.x; i < a.d; i += WIDE_NT) {
-      const float c = to_f32(xr[i]) - mean;
-      s = fmaf(c, c, s);
+#pragma unroll 4
+    for (int i = threadIdx.x * VN; i < a.d; i += WIDE_NT * VN) {
+      float v[VN];
+      ld_n<T, VN>(xr + i, v);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) s = fmaf(v[j] - mean, v[j] - mean, s);
     }
-    const float rstd = 1.f / sqrtf(cta_sum(make_float2(s, 0.f), scratch, turn).x * inv + a.eps);
-    for (int i = threadIdx.x; i < a.d; i += WIDE_NT)
-      yr[i] = from_f32<T>(fmaf((to_f32(xr[i]) - mean) * rstd, __ldg(a.gamma + i), __ldg(a.beta + i)));
+    const float rstd = rsqrtf(fmaf(cta_sum(make_float2(s, 0.f), scratch, turn).x, inv, a.eps));
+#pragma unroll 2
+    for (int i = threadIdx.x * VN; i < a.d; i += WIDE_NT * VN) {
+      float v[VN], g[VN], b[VN];
+      ld_n<T, VN>(xr + i, v);
+      ld_w<VN>(a.gamma + i, g);
+      ld_w<VN>(a.beta + i, b);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) v[j] = fmaf((v[j] - mean) * rstd, g[j], b[j]);
+      st_n<T, VN>(yr + i, v);
+    }
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -566,39 +612,79 @@ __global__ void __launch_bounds__(WIDE_NT) norm_fwd_wide_kernel(const NormArgs a
   }
 }
 
-// dx of the rows row = blockIdx.x, + gridDim.x, ... and the sums of the same rows
-template <typename T>
+template <typename T, int VN>
 __global__ void __launch_bounds__(WIDE_NT) norm_bwd_wide_kernel(const NormArgs a) {
   pdl_enter();
   __shared__ float4 scratch[2 * WIDE_NT / 32];
   int turn = 0;
   const float inv = 1.f / (float)a.d;
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
-  const T* res = static_cast<const T*>(a.dres);
-  T* dx = static_cast<T*>(a.out);
-  float* part = a.partial + (size_t)blockIdx.x * 2 * a.d;
-  bool first = true;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float mean = a.mean_in[row], rstd = a.rstd_in[row];
-    const int64_t at = row * a.d;
+    const T* x = static_cast<const T*>(a.x) + row * a.d;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.d;
+    const T* res = static_cast<const T*>(a.dres) + (a.dres ? row * a.d : 0);
+    T* dx = static_cast<T*>(a.out) + row * a.d;
     float2 s = make_float2(0.f, 0.f);
-    for (int i = threadIdx.x; i < a.d; i += WIDE_NT) {
-      const float v = to_f32(dy[at + i]) * __ldg(a.gamma + i);
-      s.x += v;
-      s.y = fmaf(v, (to_f32(x[at + i]) - mean) * rstd, s.y);
+#pragma unroll 2
+    for (int i = threadIdx.x * VN; i < a.d; i += WIDE_NT * VN) {
+      float n[VN], v[VN], g[VN];
+      ld_n<T, VN>(x + i, n);
+      ld_n<T, VN>(dy + i, v);
+      ld_w<VN>(a.gamma + i, g);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) {
+        v[j] *= g[j];
+        s.x += v[j];
+        s.y = fmaf(v[j], (n[j] - mean) * rstd, s.y);
+      }
     }
     s = cta_sum(s, scratch, turn);
     const float m1 = s.x * inv, m2 = s.y * inv;
-    for (int i = threadIdx.x; i < a.d; i += WIDE_NT) {
-      const float g = to_f32(dy[at + i]), n = (to_f32(x[at + i]) - mean) * rstd;
-      float o = (g * __ldg(a.gamma + i) - m1 - n * m2) * rstd;
-      if (res) o += to_f32(res[at + i]);
-      dx[at + i] = from_f32<T>(o);
-      part[i] = first ? g * n : fmaf(g, n, part[i]);
-      part[a.d + i] = first ? g : part[a.d + i] + g;
+#pragma unroll 2
+    for (int i = threadIdx.x * VN; i < a.d; i += WIDE_NT * VN) {
+      float n[VN], v[VN], o[VN], g[VN];
+      ld_n<T, VN>(x + i, n);
+      ld_n<T, VN>(dy + i, v);
+      ld_w<VN>(a.gamma + i, g);
+      if (a.dres) ld_n<T, VN>(res + i, o);
+#pragma unroll
+      for (int j = 0; j < VN; ++j) {
+        const float t = (fmaf(v[j], g[j], -m1) - (n[j] - mean) * rstd * m2) * rstd;
+        o[j] = a.dres ? o[j] + t : t;
+      }
+      st_n<T, VN>(dx + i, o);
     }
-    first = false;
+  }
+}
+
+// dgamma and dbeta of VN columns a thread over the rows blockIdx.y, + gridDim.y,
+// ...; it runs before dx is written, which may be x or dy
+constexpr int COL_NT = 128;
+template <typename T, int VN>
+__global__ void __launch_bounds__(COL_NT) norm_bwd_columns_kernel(const NormArgs a) {
+  pdl_enter();
+  const int i = (blockIdx.x * COL_NT + threadIdx.x) * VN;
+  if (i >= a.d) return;
+  float g[VN], b[VN];
+#pragma unroll
+  for (int j = 0; j < VN; ++j) g[j] = b[j] = 0.f;
+#pragma unroll 4
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float mean = __ldg(a.mean_in + row), rstd = __ldg(a.rstd_in + row);
+    float n[VN], v[VN];
+    ld_n<T, VN>(static_cast<const T*>(a.x) + row * a.d + i, n);
+    ld_n<T, VN>(static_cast<const T*>(a.dy) + row * a.d + i, v);
+#pragma unroll
+    for (int j = 0; j < VN; ++j) {
+      g[j] = fmaf(v[j], (n[j] - mean) * rstd, g[j]);
+      b[j] += v[j];
+    }
+  }
+  float* out = a.partial + (size_t)blockIdx.y * 2 * a.d;
+#pragma unroll
+  for (int j = 0; j < VN; ++j) {
+    out[i + j] = g[j];
+    out[a.d + i + j] = b[j];
   }
 }
 
@@ -669,25 +755,37 @@ cudaError_t bwd_w(NormArgs& a, cudaStream_t st) {
   return a.dres ? launch_rows(norm_bwd_kernel<T, WHOLE, true>, g, a, done[1], st)
                 : launch_rows(norm_bwd_kernel<T, WHOLE, false>, g, a, done[0], st);
 }
+template <typename T, int VN>
+cudaError_t fwd_wide(const NormArgs& a, cudaStream_t st) {
+  const int64_t most = (int64_t)sm_count() * 4;
+  return launch_pdl(norm_fwd_wide_kernel<T, VN>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(WIDE_NT), 0, st, a);
+}
+// Row slices of the columns' sums: about 16 CTAs an SM
+int wide_slices(int64_t rows, int d) {
+  const int64_t tiles = (d + COL_NT * 8 - 1) / (COL_NT * 8), most = ((int64_t)sm_count() * 16 + tiles - 1) / tiles;
+  return (int)(rows < most ? rows : most);
+}
+template <typename T, int VN>
+cudaError_t bwd_wide(NormArgs& a, cudaStream_t st) {
+  a.parts = wide_slices(a.rows, a.d);
+  cudaError_t e = launch_pdl(norm_bwd_columns_kernel<T, VN>, dim3((a.d + COL_NT * VN - 1) / (COL_NT * VN), a.parts),
+                             dim3(COL_NT), 0, st, a);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (int64_t)sm_count() * 4;
+  return launch_pdl(norm_bwd_wide_kernel<T, VN>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(WIDE_NT), 0, st, a);
+}
+bool vectors(const float* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 template <typename T>
 cudaError_t fwd_t(NormArgs& a, cudaStream_t st) {
-  if (wide(a.d)) {
-    const int64_t most = (int64_t)sm_count() * 4;
-    return launch_pdl(norm_fwd_wide_kernel<T>, dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(WIDE_NT), 0, st, a);
-  }
-  return a.d % Vec<T>::N == 0 ? fwd_w<T, true>(a, st) : fwd_w<T, false>(a, st);
-}
-int wide_ctas(int64_t rows) {
-  const int64_t most = (int64_t)sm_count() * 2;
-  return (int)(rows < most ? rows : most);
+  const bool whole = a.d % Vec<T>::N == 0;
+  if (wide(a.d)) return whole && vectors(a.gamma) && vectors(a.beta) ? fwd_wide<T, Vec<T>::N>(a, st) : fwd_wide<T, 1>(a, st);
+  return whole ? fwd_w<T, true>(a, st) : fwd_w<T, false>(a, st);
 }
 template <typename T>
 cudaError_t bwd_t(NormArgs& a, cudaStream_t st) {
-  if (wide(a.d)) {
-    a.parts = wide_ctas(a.rows);
-    return launch_pdl(norm_bwd_wide_kernel<T>, dim3(a.parts), dim3(WIDE_NT), 0, st, a);
-  }
-  return a.d % Vec<T>::N == 0 ? bwd_w<T, true>(a, st) : bwd_w<T, false>(a, st);
+  const bool whole = a.d % Vec<T>::N == 0;
+  if (wide(a.d)) return whole && vectors(a.gamma) ? bwd_wide<T, Vec<T>::N>(a, st) : bwd_wide<T, 1>(a, st);
+  return whole ? bwd_w<T, true>(a, st) : bwd_w<T, false>(a, st);
 }
 
 }  // namespace
@@ -710,7 +808,7 @@ cudaError_t launch_norm_fwd(int64_t rows, int d, bool bf16, const void* x, const
 }
 
 size_t norm_ws_bytes(int64_t rows, int d) {
-  const int ctas = wide(d) ? wide_ctas(rows) : norm_grid(rows, d, 2, 2, nullptr).ctas;
+  const int ctas = wide(d) ? wide_slices(rows, d) : norm_grid(rows, d, 2, 2, nullptr).ctas;
   return (size_t)ctas * 2 * d * 4;
 }
 
