@@ -27,7 +27,7 @@ struct DropArgs {
   int64_t n;
   uint64_t seed, offset;
   uint32_t cut;
-  float scale;
+  float scale, scale_lo;  // 65536 / (65536 - cut) in two parts
 };
 
 __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_t seed) {
@@ -46,13 +46,33 @@ __device__ __forceinline__ uint4 philox(uint64_t block, uint64_t offset, uint64_
   return make_uint4(c0, c1, c2, c3);
 }
 
-// keep or drop the eight values of a block; a dropped value is 0 whatever it was (infinities and NaN too)
-__device__ __forceinline__ void drop8(float (&v)[8], const uint4& u, uint32_t cut, float scale) {
+__device__ __forceinline__ uint32_t draw_of(const uint4& u, int i) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  return (i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
+}
+// res + y * (scale + lo), rounded once: the product's and the sum's rounding
+// errors are formed exactly (two-sum) and added back, so a float32 output keeps
+// its 24 bits where the residual and the scaled value cancel.  The rounded
+// intrinsics keep the compiler from fusing the steps.
+__device__ __forceinline__ float add_scaled(float res, float y, float scale, float lo) {
+  const float p = __fmul_rn(y, scale), pe = __fmaf_rn(y, scale, -p);
+  const float s = __fadd_rn(res, p), b = __fsub_rn(s, res);
+  const float se = __fadd_rn(__fsub_rn(res, __fsub_rn(s, b)), __fsub_rn(p, b));
+  return isfinite(s) ? __fadd_rn(s, __fadd_rn(se, __fmaf_rn(y, lo, pe))) : s;
+}
+// Keep or drop the eight values of a block and add the residual's; a dropped
+// value is 0 whatever it was (infinities and NaN too).
+template <typename T, bool RES>
+__device__ __forceinline__ void drop8(float (&v)[8], const float (&r)[8], const uint4& u, const DropArgs& a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint32_t r = (i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu;
-    v[i] = r >= cut ? v[i] * scale : 0.f;
+    const bool keep = draw_of(u, i) >= a.cut;
+    if (RES && sizeof(T) == 4) {
+      v[i] = keep ? add_scaled(r[i], v[i], a.scale, a.scale_lo) : r[i];
+    } else {
+      v[i] = keep ? v[i] * a.scale : 0.f;
+      if (RES) v[i] += r[i];
+    }
   }
 }
 
@@ -124,15 +144,10 @@ __global__ void __launch_bounds__(DROP_THREADS, Walk<T, RES>::RESIDENT) dropout_
       const int64_t b = b0 + j * step;
       if (b < whole) {
         const uint4 draws = philox((uint64_t)b, a.offset, a.seed);
-        float v[8];
+        float v[8], r[8];
         expand<T>(u[j], v);
-        drop8(v, draws, a.cut, a.scale);
-        if (RES) {
-          float r[8];
-          expand<T>(w[j], r);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += r[i];
-        }
+        if (RES) expand<T>(w[j], r);
+        drop8<T, RES>(v, r, draws, a);
         store8(out + b * 8, v);
       }
       if (AHEAD) {
@@ -148,13 +163,16 @@ __global__ void __launch_bounds__(DROP_THREADS, Walk<T, RES>::RESIDENT) dropout_
   if (a.n % 8 != 0 && blockIdx.x == 0 && threadIdx.x == 0) {
     const int64_t i0 = whole * 8;
     const int m = (int)(a.n - i0);
-    float v[8];
+    float v[8], r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < m ? to_f32(y[i0 + i]) : 0.f;
-    drop8(v, philox((uint64_t)whole, a.offset, a.seed), a.cut, a.scale);
+    for (int i = 0; i < 8; ++i) {
+      v[i] = i < m ? to_f32(y[i0 + i]) : 0.f;
+      r[i] = RES && i < m ? to_f32(res[i0 + i]) : 0.f;
+    }
+    drop8<T, RES>(v, r, philox((uint64_t)whole, a.offset, a.seed), a);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < m) out[i0 + i] = from_f32<T>(RES ? v[i] + to_f32(res[i0 + i]) : v[i]);
+      if (i < m) out[i0 + i] = from_f32<T>(v[i]);
   }
 }
 
@@ -169,7 +187,8 @@ cudaError_t launch_drop(const DropArgs& a, cudaStream_t st) {
 
 cudaError_t launch_dropout(int kind, int64_t n, bool bf16, const void* y, const void* residual, void* out,
                            uint32_t cut, uint64_t seed, uint64_t offset, cudaStream_t st) {
-  const DropArgs a{y, residual, out, n, seed, offset, cut, (float)(65536.0 / (65536.0 - cut))};
+  const double scale = 65536.0 / (65536.0 - cut);
+  const DropArgs a{y, residual, out, n, seed, offset, cut, (float)scale, (float)(scale - (float)scale)};
   LaunchScope ls(kind, st);
   if (bf16) return residual ? launch_drop<__nv_bfloat16, true>(a, st) : launch_drop<__nv_bfloat16, false>(a, st);
   return residual ? launch_drop<float, true>(a, st) : launch_drop<float, false>(a, st);
