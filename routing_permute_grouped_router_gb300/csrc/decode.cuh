@@ -86,7 +86,7 @@ __device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t want, uin
 // U equal units in order: the first U % G CTAs take one more than the others,
 // so with fewer units than CTAs the last ones take none.  A tile of several
 // units can begin in one CTA and end in another, so every CTA streams the same
-// bytes to within a unit whatever the number of tiles.  U < 2^26 by the limits
+// bytes to within a unit whatever the number of tiles.  U < 2^28 by the limits
 // on d, f and E.
 struct Split {
   int base, more;

@@ -723,6 +723,9 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
     const bool on = i < i1;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     const int t = i / (a.d / 4), col = (i - t * (a.d / 4)) * 4;
+    const int64_t o = (int64_t)t * a.d + col;
+    uint2 u = make_uint2(0, 0);
+    if (on && sub == 0 && res) u = *reinterpret_cast<const uint2*>(res + o);
     if (on && R.nact > 0) {
       const int dt = col / DEC_N, first = down.owner(dt * per), n = down.owner((dt + 1) * per - 1) - first + 1;
       const float* p = a.down_part + (int64_t)(first + dt) * dslot + t * DEC_N + col % DEC_N;
@@ -742,9 +745,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
 #pragma unroll 1
     for (int o = 1; o < L; o *= 2) xor4(v, o);
     if (on && sub == 0) {
-      const int64_t o = (int64_t)t * a.d + col;
       if (res) {
-        const uint2 u = *reinterpret_cast<const uint2*>(res + o);
         const float2 r0 = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(u.x));
         const float2 r1 = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(u.y));
         v = make_float4(v.x + r0.x, v.y + r0.y, v.z + r1.x, v.w + r1.y);

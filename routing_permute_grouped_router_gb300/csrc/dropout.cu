@@ -98,18 +98,18 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   }
 }
 
-// How a type and direction walk their blocks.  bf16 with a residual, whose
-// loads and draws take about as long, loads the next block before it draws for
-// this one (2^27 values: 121 us; two blocks loaded and then drawn for: 136).
-// The others draw for two blocks loaded together: without a residual the
-// 32-bit products of the draws bound bf16 (97 us; the next blocks loaded ahead:
-// 103), and float32 is at HBM's rate either way (2^26 values: 116 and 119).
+// How a direction walks its blocks.  With a residual the next block is loaded
+// before this one is drawn for, whose loads take about as long as the draws
+// (2^27 bf16 values: 121 us; two blocks loaded and then drawn for: 136.  2^26
+// float32 values: 121 and 131).  Without one two blocks are loaded together:
+// the 32-bit products of the draws bound bf16 (2^27 values: 98 us; the next
+// blocks loaded ahead: 103), and float32 is at HBM's rate either way.
 template <typename T, bool RES>
 struct Walk {
-  static constexpr bool AHEAD = RES && sizeof(T) == 2;
+  static constexpr bool AHEAD = RES;
   static constexpr int B = AHEAD ? 1 : 2;
-  static constexpr int RESIDENT = AHEAD ? 6 : 1;  // CTAs an SM that the registers are kept down for
-  static constexpr int CTAS = AHEAD ? 12 : 8;     // launched an SM
+  static constexpr int RESIDENT = AHEAD ? (sizeof(T) == 2 ? 6 : 4) : 1;  // CTAs an SM that the registers leave room for
+  static constexpr int CTAS = AHEAD ? 12 : 8;                            // launched an SM
 };
 
 template <typename T, bool RES>

@@ -114,19 +114,22 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const char* src, uint32_t
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
+__device__ __forceinline__ bool ring_ready(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // Waits for the barrier's phase, two seconds at most.
 __device__ __noinline__ void ring_wait(uint32_t bar, uint32_t parity, uint32_t* err) {
   uint64_t t0 = 0;
   for (uint32_t i = 0; i < (1u << 30); ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return;
+    if (ring_ready(bar, parity)) return;
     if ((i & 255u) == 255u) {
       uint64_t t;
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -257,7 +260,9 @@ struct Rows {
       for (int b = 0; b < NBUF; ++b) copy_row(sm_addr(base + (p * NBUF + b) * slot), src[b] + sp.at, sp.bytes, bar);
     }
   }
-  __device__ __forceinline__ void wait(uint32_t* err) const { ring_wait(sm_addr(bars + at), phase, err); }
+  __device__ __forceinline__ void wait(uint32_t* err) const {
+    if (!ring_ready(sm_addr(bars + at), phase)) ring_wait(sm_addr(bars + at), phase, err);
+  }
   __device__ __forceinline__ const char* place_at(int p, int b) const { return base + (p * NBUF + b) * slot; }
   __device__ __forceinline__ const char* place(int b) const { return place_at(at, b); }
   __device__ __forceinline__ void next() {
