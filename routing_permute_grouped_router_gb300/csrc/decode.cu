@@ -18,6 +18,8 @@
 //      rows to the tokens in shared memory, and the CTAs that share a column
 //      tile add their sums in CTA order and write y.
 // Nothing is summed in an order that depends on timing.
+#include <stddef.h>
+
 #include "decode.cuh"
 
 namespace moe {
@@ -40,6 +42,7 @@ struct SimtSmem {
     float red[SM_WARPS * SM_TOK * 2 * DEC_N];  // [warp][token][matrix][column]
   };
 };
+static_assert(offsetof(SimtSmem, red) % 16 == 0 && offsetof(SimtSmem, score) % 16 == 0, "read as float4");
 
 // out(m, c, sums) for each of n <= TOK inputs and the 128 columns at c0 of MATS
 // matrices (`width` columns wide): the sums over rows k0..k1 of in(m, k) *

@@ -113,7 +113,7 @@ __device__ __forceinline__ bool few_rows(const DecodeArgs& a, const Routing& R) 
 // it that is not yet in an SM's instruction cache costs an L2 or DRAM latency:
 // the loops from here on are kept rolled and the bodies short (the unrolled
 // forms of the score, pick and epilogue loops cost a one-token step 20 us).
-struct ScoreScratch {
+struct alignas(16) ScoreScratch {
   float w[8192];            // rows of W_r
   float x[256 * DEC_TG];    // the same columns of the tokens
   float red[256 * DEC_TG];

@@ -39,7 +39,7 @@ constexpr int MAX_GROUPS = BWD_NT / 32;
 constexpr int SMEM_SM = 220 * 1024;             // shared memory of an SM that the rings may take
 constexpr int RING = 4;        // most rows on their way to a group of threads
 constexpr int WIDE_NT = 512;   // threads a CTA of the wide kernels
-constexpr int RED_COLS = 32, RED_STRIPS = 16;
+constexpr int RED_COLS = 32, RED_STRIPS = 32;
 
 // Element c (of EPT) of thread r of tpr, in whole vectors of VN or one by one.
 template <int VN>
