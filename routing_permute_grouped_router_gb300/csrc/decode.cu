@@ -6,7 +6,7 @@
 //
 // With few tokens the layer is bound by reading the picked experts' weights
 // once from HBM, and everything else has to stay out of the way.  One
-// cooperative launch, one CTA an SM, in three steps:
+// cooperative launch, one CTA an SM (two for fp32 weights), in three steps:
 //   1. the CTAs score slices of d for groups of tokens, meet at a grid
 //      barrier, and each derives the same picks and row lists;
 //   2. up product: the W1 and W3 tiles (128 columns, all of d) of the experts
@@ -17,7 +17,13 @@
 //      of y, all experts in turn) split the same way; a CTA adds its experts'
 //      rows to the tokens in shared memory, and the CTAs that share a column
 //      tile add their sums in CTA order and write y.
+// Where rows are few, step 3 makes h from the partial sums itself (few_rows).
 // Nothing is summed in an order that depends on timing.
+// Measured for fp32: seven tokens of a layer with d 1024, f 4096, eight experts,
+// top-2 (352 MB of weights), 84 us; the SMs get unequal shares of HBM, and the
+// CTAs wait for the slowest between the products.  Handing the parts out while
+// the kernel runs took 95 us: shorter parts cost more at their ends than the
+// waits they save.
 #include <stddef.h>
 
 #include "decode.cuh"

@@ -103,6 +103,8 @@ struct Split {
 // sums in every column tile of y but saves an exchange: the CTAs of a split
 // tile add a share of its parts each and write h, and all wait for that (a
 // fence, a wait and a barrier of some 2 us each under load).
+// One token of a dropless top-4 layer of 32 experts: 39 us, and 44 with the
+// exchange; 8 tokens of it, three rows an expert: 91 and 75.
 constexpr int DEC_DIRECT = 64;  // most picks of such a call
 __device__ __forceinline__ bool few_rows(const DecodeArgs& a, const Routing& R) {
   return a.T * a.k <= DEC_DIRECT && R.nact > 0 && R.rows <= 2 * R.nact;

@@ -11,8 +11,9 @@
 // CTA, or a warp of one where 32 are enough), 16 elements each: 64 to 512 rows
 // are in work on an SM's registers while plain copies bring the next ones into
 // a ring in shared memory, up to four rows deep, so the loads' latency is out of
-// the way of the two reductions of a row.  (With the loads in registers and
-// no ring the 32768 x 4096 bf16 passes reached 3.4 and 2.8 TB/s.)  The variance
+// the way of the two reductions of a row.  (32768 x 4096 bf16: 92.5 us forward,
+// 5.8 TB/s, and 168 us backward, 6.4 TB/s; with the loads in registers and no
+// ring 155 and 367.)  The variance
 // is the sum of squared distances from the mean: no cancellation of a large
 // mean, no second read.  Threads keep their columns' gamma, beta and, in the
 // backward, dgamma and dbeta sums in registers over all rows of the CTA; the
@@ -393,8 +394,9 @@ __global__ void __maxnreg__(FWD_REGS) norm_fwd_kernel(const NormArgs a) {
 
 // A row is read from the ring twice, for the sums and for dx, and the sums of
 // the next row are formed before dx of this one: the reduction's shuffles and
-// barrier run under arithmetic that does not wait for them.  (One row after the
-// other, 32768 x 4096 bf16 took 197 us.)
+// barrier run under arithmetic that does not wait for them.  (32768 x 4096 bf16:
+// 168 us; one row after the other 197.  The forward, bound by instruction issue,
+// loses by it: 104 us, not 92.5.)
 template <typename T, bool WHOLE, bool RES>
 __global__ void __launch_bounds__(BWD_NT, 1) norm_bwd_kernel(const NormArgs a) {
   constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2, NBUF = RES ? 3 : 2;
