@@ -714,9 +714,9 @@ struct Grid {
 Grid norm_grid(int64_t rows, int d, int es, int bufs, NormArgs* a) {
   const bool bwd = bufs > 1;
   const int tpr = threads_per_row(d), slot = (d * es + 15) / 16 * 16 + (d * es % 16 ? 16 : 0);
-  int groups = bwd ? BWD_NT / tpr : (tpr == 32 ? 4 : 1), per = bwd ? 1 : 65536 / (tpr * groups * FWD_REGS);
+  const int groups = bwd ? BWD_NT / tpr : (tpr == 32 ? 4 : 1);
+  int per = bwd ? 1 : 65536 / (tpr * groups * FWD_REGS);
   const size_t place = (size_t)bufs * slot;
-  while (groups > 1 && bwd && groups * 2 * (place + 128) > SMEM_SM) groups /= 2;
   while (per > 1 && per * 2 * (groups * place + 1024) > SMEM_SM) --per;
   int ring = (int)((SMEM_SM / per - 1024) / (groups * place));
   ring = ring > RING ? RING : (ring < 2 ? 2 : ring);
