@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
       if (v0 < v1 && alive) {
         const bool ok = lane != 0 || wait_count(bar + half, G, a.err, 715);
         alive = __all_sync(0xffffffffu, ok);
+        __syncwarp();  // a vote orders no memory: lane 0 has acquired the other CTAs' sums, all lanes read them
         if (!alive) *abort_flag = 1;
       }
       for (int v = v0; v < v1 && alive;) {
