@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(HERE, "libmoe_gb300.so")
 
 MOE_F32 = 0
 MOE_BF16 = 1
+MOE_DECODE_MAX_T = 64
 
 STATUS = ["MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_SHAPE", "MOE_ERR_DTYPE", "MOE_ERR_ALIGNMENT",
           "MOE_ERR_WORKSPACE", "MOE_ERR_CUDA", "MOE_ERR_DEVICE_CHECK", "MOE_ERR_TIMEOUT", "MOE_ERR_UNSUPPORTED"]
@@ -331,7 +332,7 @@ def _dtype(t) -> int:
 
 def _stream_of(t, stream) -> int:
     """The given stream, else the current one of the device of ``t``."""
-    return _types[3](t.get_device()) if stream is None else stream.cuda_stream
+    return _torch_types()[3](t.get_device()) if stream is None else stream.cuda_stream
 
 
 def moe_layer_decode(cfg: MoeConfig, weights: dict, x, residual, y, ids, gates, ws, stream=None) -> None:

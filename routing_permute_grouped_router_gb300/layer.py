@@ -9,13 +9,14 @@ itself.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import torch
 
-from . import (MOE_BF16, MoeConfig, allocate_grads, allocate_saved, decode_workspace, moe_dropout_add,
-               moe_dropout_bwd, moe_layer_bwd, moe_layer_decode, moe_layer_fwd, moe_max_rows, moe_norm_bwd,
-               moe_norm_fwd, norm_workspace, workspace)
+from . import (MOE_BF16, MOE_DECODE_MAX_T, MoeConfig, _stream_of, allocate_grads, allocate_saved, moe_decode_workspace_size,
+               moe_dropout_add, moe_dropout_bwd, moe_layer_bwd, moe_layer_decode, moe_layer_fwd, moe_max_rows,
+               moe_norm_bwd, moe_norm_fwd, norm_workspace, workspace)
 
 
 class MoELayer:
@@ -63,8 +64,8 @@ class MoEBlock:
         T, d = max(cfg.T, 1), cfg.d_model
         self.h = torch.empty(T, d, dtype=layer.act_dtype, device=dev)
         self.out = torch.empty_like(self.h)
-        self._decode = {}  # tokens -> config and buffers
-        self._decode_ws = None
+        self._decode = {}  # (stream, tokens) -> config, h, out and workspace
+        self._decode_ws = {}  # stream -> workspace, large enough for any number of tokens
         if layer.training:
             f32 = dict(dtype=torch.float32, device=dev)
             self.mean, self.rstd = torch.empty(T, **f32), torch.empty(T, **f32)
@@ -90,19 +91,35 @@ class MoEBlock:
         return self.dx
 
     def decode(self, x: torch.Tensor, stream=None) -> torch.Tensor:
-        """x + layer(norm(x)) for at most 64 tokens, in two kernels."""
-        T = x.shape[0]
-        if T not in self._decode:
-            c = self.layer.cfg
-            cfg = MoeConfig(T, c.d_model, c.d_ff, c.E, c.k, c.capacity_factor, c.capacity, c.dtype, 0.0)
-            ws = decode_workspace(cfg, self.layer.device)
-            if self._decode_ws is None or ws.numel() > self._decode_ws.numel():
-                self._decode_ws = ws
-            self._decode[T] = (cfg, torch.empty_like(x), torch.empty_like(x))
-        cfg, h, out = self._decode[T]
+        """x + layer(norm(x)) for at most 64 tokens, in two kernels.
+
+        The result is a buffer of the block's, written again by the next call of as many tokens on the same stream.
+        Buffers belong to one stream each and live as long as the block, so calls on several streams may overlap and
+        graphs may be captured, for any numbers of tokens in any order.  A graph uses the buffers of the stream that
+        it was captured on: its replays, and other calls on that stream, follow one another.
+        """
+        key = _stream_of(self.gamma, stream), x.shape[0]
+        if key not in self._decode:
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                self._decode[key] = self._decode_buffers(x, key[0])
+        cfg, h, out, ws = self._decode[key]
         moe_norm_fwd(x, self.gamma, self.beta, self.eps, h, None, None, stream)
-        moe_layer_decode(cfg, self.layer.weights, h, x, out, None, None, self._decode_ws, stream)
+        moe_layer_decode(cfg, self.layer.weights, h, x, out, None, None, ws, stream)
         return out
+
+    def _decode_config(self, T: int) -> MoeConfig:
+        c = self.layer.cfg
+        return MoeConfig(T, c.d_model, c.d_ff, c.E, c.k, c.capacity_factor, c.capacity, c.dtype, 0.0)
+
+    def _decode_buffers(self, x, raw_stream):
+        """Made on the stream that uses them: memory that the allocator hands out again is free in that order."""
+        cfg = self._decode_config(x.shape[0])
+        moe_decode_workspace_size(cfg)  # refuses what the layer would
+        ws = self._decode_ws.get(raw_stream)
+        if ws is None:
+            size = max(moe_decode_workspace_size(self._decode_config(t)) for t in range(1, MOE_DECODE_MAX_T + 1))
+            ws = self._decode_ws[raw_stream] = torch.empty(size, dtype=torch.uint8, device=self.layer.device)
+        return cfg, torch.empty_like(x), torch.empty_like(x), ws
 
 
 def from_workload(wl, device="cuda", training: bool = True, T: Optional[int] = None,

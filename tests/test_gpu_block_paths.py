@@ -8,6 +8,7 @@ import torch
 
 import routing_permute_grouped_router_gb300 as pkg
 from _util import check_no_device_error
+from routing_permute_grouped_router_gb300 import layer
 from routing_permute_grouped_router_gb300 import workload as W
 from test_gpu_block_ops import check_decode, decode, decode_ref
 
@@ -63,3 +64,54 @@ def test_decode_few_rows_with_whole_and_split_tiles(shape):
         pkg.moe_layer_decode(r["cfg"], r["w"], r["x"], None, r["y"], r["ids"], r["gates"], r["ws"])
         assert torch.equal(first, r["y"])
     check_no_device_error()
+
+
+# ----------------------------- the block's buffers ------------------------- #
+def serving_block():
+    wl = W.make(LS("serve", 64, 512, 256, 8, 2, 0.0, W.BF16), seed=23, micro_batches=1, with_dy=False)
+    L = layer.from_workload(wl, training=False)
+    blk = layer.MoEBlock(L, torch.ones(512, device="cuda"), torch.zeros(512, device="cuda"))
+    return blk, wl.x[0].torch("cuda"), lambda: layer.MoEBlock(L, blk.gamma, blk.beta)
+
+
+def test_block_decode_graphs_of_several_sizes():
+    """One graph a batch size, captured in ascending order, each replayed after the others were made and memory has
+    been handed out again."""
+    blk, x, fresh = serving_block()
+    st = torch.cuda.Stream()
+    sizes, graphs, xs, outs = (1, 8, 40, 64), [], [], []
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        for T in sizes:
+            xs.append(torch.zeros(T, 512, dtype=torch.bfloat16, device="cuda"))
+            blk.decode(xs[-1])
+            st.synchronize()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=st):
+                outs.append(blk.decode(xs[-1]))
+    blk.decode(x)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    others = [torch.full((n << 20,), 255, dtype=torch.uint8, device="cuda") for n in (1, 2, 4, 8, 16, 32, 64) * 2]
+    for seed in range(3):
+        want = [fresh().decode(x[seed:seed + T].contiguous()).clone() if seed + T <= 64 else None for T in sizes]
+        for T, g, xi, out, e in reversed(list(zip(sizes, graphs, xs, outs, want))):
+            if e is not None:
+                xi.copy_(x[seed:seed + T])
+                g.replay()
+                assert torch.equal(out, e)
+    check_no_device_error()
+    assert all(bool((o == 255).all()) for o in others)  # nothing was written into memory that others own
+
+
+def test_block_decode_on_two_streams():
+    blk, x, fresh = serving_block()
+    want = [fresh().decode(x[i:i + 24].contiguous()).clone() for i in (0, 40)]
+    xs = [x[i:i + 24].contiguous() for i in (0, 40)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [blk.decode(xi, stream=s) for xi, s in zip(xs, streams)]
+    torch.cuda.synchronize()
+    check_no_device_error()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
