@@ -101,25 +101,27 @@ class MoEBlock:
         key = _stream_of(self.gamma, stream), x.shape[0]
         if key not in self._decode:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
-                self._decode[key] = self._decode_buffers(x, key[0])
+                self._decode[key] = self._decode_buffers(*key)
         cfg, h, out, ws = self._decode[key]
         moe_norm_fwd(x, self.gamma, self.beta, self.eps, h, None, None, stream)
         moe_layer_decode(cfg, self.layer.weights, h, x, out, None, None, ws, stream)
-        return out
+        return out if out.shape == x.shape else out.view(x.shape)
 
     def _decode_config(self, T: int) -> MoeConfig:
         c = self.layer.cfg
         return MoeConfig(T, c.d_model, c.d_ff, c.E, c.k, c.capacity_factor, c.capacity, c.dtype, 0.0)
 
-    def _decode_buffers(self, x, raw_stream):
-        """Made on the stream that uses them: memory that the allocator hands out again is free in that order."""
-        cfg = self._decode_config(x.shape[0])
+    def _decode_buffers(self, raw_stream: int, T: int):
+        """Made on the stream that uses them: memory that the allocator hands out again is free in that order.  Their
+        sizes and type are the layer's, whatever was passed."""
+        cfg = self._decode_config(T)
         moe_decode_workspace_size(cfg)  # refuses what the layer would
         ws = self._decode_ws.get(raw_stream)
         if ws is None:
             size = max(moe_decode_workspace_size(self._decode_config(t)) for t in range(1, MOE_DECODE_MAX_T + 1))
             ws = self._decode_ws[raw_stream] = torch.empty(size, dtype=torch.uint8, device=self.layer.device)
-        return cfg, torch.empty_like(x), torch.empty_like(x), ws
+        h, out = (torch.empty(T, cfg.d_model, dtype=self.layer.act_dtype, device=self.layer.device) for _ in range(2))
+        return cfg, h, out, ws
 
 
 def from_workload(wl, device="cuda", training: bool = True, T: Optional[int] = None,

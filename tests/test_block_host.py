@@ -59,3 +59,25 @@ def test_decode_buffers_of_two_streams_are_apart(block):
         blk.decode(tokens(3), Stream(raw))
     ptrs = [{t.data_ptr() for t in c[1:]} for c in calls]
     assert not (ptrs[0] | ptrs[1]) & (ptrs[2] | ptrs[3])
+
+
+def test_decode_after_a_refused_call(block, monkeypatch):
+    """A call with a wrong type or width leaves no buffers of that type or width behind."""
+    blk, calls = block
+    s = Stream(7)
+
+    def norm(x, gamma, beta, eps, y, *a):  # the binding's checks
+        if y.dtype != x.dtype:
+            raise TypeError
+        if y.numel() != x.numel() or x.shape[-1] != gamma.numel():
+            raise ValueError
+
+    monkeypatch.setattr(layer, "moe_norm_fwd", norm)
+    for x, err in ((tokens(4).float(), TypeError), (tokens(4, 128), ValueError), (tokens(65), pkg.MoeError)):
+        with pytest.raises(err):
+            blk.decode(x, s)
+    assert not calls
+    assert blk.decode(tokens(4), s).dtype == torch.bfloat16
+    (T, ws, h, out), = calls
+    assert h.shape == out.shape == (4, 256) and h.dtype == out.dtype == torch.bfloat16
+    assert blk.decode(tokens(4).view(4, 1, 256), s).shape == (4, 1, 256)

@@ -115,3 +115,16 @@ def test_block_decode_on_two_streams():
     torch.cuda.synchronize()
     check_no_device_error()
     assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_block_decode_after_refused_calls():
+    blk, x, fresh = serving_block()
+    want = fresh().decode(x[:4].contiguous())
+    n0 = pkg.moe_launch_count()
+    for bad, err in ((x[:4].float(), TypeError), (x[:4, :256].contiguous(), ValueError), (x[:4].cpu(), ValueError),
+                     (torch.cat([x, x[:1]]), pkg.MoeError)):
+        with pytest.raises(err):
+            blk.decode(bad)
+    assert pkg.moe_launch_count() == n0
+    assert torch.equal(blk.decode(x[:4].contiguous()), want)
+    check_no_device_error()
