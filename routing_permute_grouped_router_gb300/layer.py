@@ -61,8 +61,11 @@ class MoEBlock:
         self.layer, self.p, self.eps = layer, p, eps
         self.gamma, self.beta = gamma.contiguous(), beta.contiguous()
         cfg, dev = layer.cfg, layer.device
-        T, d = max(cfg.T, 1), cfg.d_model
-        self.h = torch.empty(T, d, dtype=layer.act_dtype, device=dev)
+        T, d = cfg.T, cfg.d_model
+        # the layer's calls want valid pointers for no tokens too: what they are given has a row at least
+        rows = dict(size=(max(T, 1), d), dtype=layer.act_dtype, device=dev)
+        self._h = torch.empty(**rows)
+        self.h = self._h[:T]
         self.out = torch.empty_like(self.h)
         self._decode = {}  # (stream, tokens) -> config, h, out and workspace
         self._decode_ws = {}  # stream -> workspace, large enough for any number of tokens
@@ -70,7 +73,8 @@ class MoEBlock:
             f32 = dict(dtype=torch.float32, device=dev)
             self.mean, self.rstd = torch.empty(T, **f32), torch.empty(T, **f32)
             self.dgamma, self.dbeta = torch.zeros(d, **f32), torch.zeros(d, **f32)
-            self.dy = torch.empty_like(self.h)
+            self._dy = torch.empty(**rows)
+            self.dy = self._dy[:T]
             self.dx = torch.empty_like(self.h)
             self.ws = norm_workspace(T, d, dev)
         else:
@@ -78,14 +82,14 @@ class MoEBlock:
 
     def forward(self, x: torch.Tensor, seed: int = 0, offset: int = 0, stream=None) -> torch.Tensor:
         moe_norm_fwd(x, self.gamma, self.beta, self.eps, self.h, self.mean, self.rstd, stream)
-        y = self.layer.forward(self.h, stream)
+        y = self.layer.forward(self._h, stream)[:self.layer.cfg.T]
         moe_dropout_add(y, x, self.out, self.p if self.layer.training else 0.0, seed, offset, stream)
         return self.out
 
     def backward(self, x: torch.Tensor, dout: torch.Tensor, accumulate: bool, seed: int = 0, offset: int = 0,
                  stream=None) -> torch.Tensor:
         moe_dropout_bwd(dout, self.dy, self.p, seed, offset, stream)
-        dh = self.layer.backward(self.h, self.dy, accumulate, stream)
+        dh = self.layer.backward(self._h, self._dy, accumulate, stream)[:self.layer.cfg.T]
         moe_norm_bwd(x, dh, self.gamma, self.mean, self.rstd, dout, self.dx, self.dgamma, self.dbeta, accumulate,
                      self.ws, stream)
         return self.dx

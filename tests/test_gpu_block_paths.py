@@ -128,3 +128,19 @@ def test_block_decode_after_refused_calls():
     assert pkg.moe_launch_count() == n0
     assert torch.equal(blk.decode(x[:4].contiguous()), want)
     check_no_device_error()
+
+
+def test_block_of_no_tokens():
+    """T = 0, as the layer takes it: empty results, zero gradients when overwriting, untouched when accumulating."""
+    s = LS("empty", 0, 256, 256, 4, 2, 1.25, W.BF16, backward=True)
+    L = layer.from_workload(W.make(s.replace(T=8), micro_batches=1, with_dy=True), T=0)
+    blk = layer.MoEBlock(L, torch.ones(256, device="cuda"), torch.zeros(256, device="cuda"), p=0.1)
+    x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
+    grads = [blk.dgamma, blk.dbeta] + [L.grads[n] for n in ("dW_r", "dW1", "dW3", "dW2")]
+    for g in grads:
+        g.fill_(3.0)
+    assert blk.forward(x, 1, 2).shape == blk.decode(x).shape == (0, 256)
+    for accumulate, value in ((True, 3.0), (False, 0.0)):
+        assert blk.backward(x, x, accumulate, 1, 2).shape == (0, 256)
+        assert all(bool((g == value).all()) for g in grads)
+    check_no_device_error()
