@@ -88,6 +88,8 @@ class MoEBlock:
 
     def backward(self, x: torch.Tensor, dout: torch.Tensor, accumulate: bool, seed: int = 0, offset: int = 0,
                  stream=None) -> torch.Tensor:
+        if not self.layer.training:
+            raise RuntimeError("block's layer was built without training buffers")
         moe_dropout_bwd(dout, self.dy, self.p, seed, offset, stream)
         dh = self.layer.backward(self._h, self._dy, accumulate, stream)[:self.layer.cfg.T]
         moe_norm_bwd(x, dh, self.gamma, self.mean, self.rstd, dout, self.dx, self.dgamma, self.dbeta, accumulate,

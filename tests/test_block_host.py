@@ -81,3 +81,9 @@ def test_decode_after_a_refused_call(block, monkeypatch):
     (T, ws, h, out), = calls
     assert h.shape == out.shape == (4, 256) and h.dtype == out.dtype == torch.bfloat16
     assert blk.decode(tokens(4).view(4, 1, 256), s).shape == (4, 1, 256)
+
+
+def test_backward_without_training_buffers_says_so(block):
+    blk, _ = block
+    with pytest.raises(RuntimeError, match="without training buffers"):
+        blk.backward(tokens(4), tokens(4), False)
