@@ -47,6 +47,15 @@ moe_status device_ready(uint32_t** err) {
     ds.init = true;
   }
   if (!ds.supported) return MOE_ERR_UNSUPPORTED;
+  // A host thread gets its CUDA context with the first runtime call that needs
+  // one, and the driver's tensor-map encoder takes the thread's context: a call
+  // may begin with it, so each thread looks the symbol up once for itself.
+  thread_local int bound = -1;
+  if (bound != dev) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess) return MOE_ERR_CUDA;
+    bound = dev;
+  }
   *err = ds.err;
   return MOE_OK;
 }

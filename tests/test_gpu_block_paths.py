@@ -2,6 +2,8 @@
 
 The tolerances are those of test_gpu_block_ops, whose helpers are used here.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -144,3 +146,39 @@ def test_block_of_no_tokens():
         assert blk.backward(x, x, accumulate, 1, 2).shape == (0, 256)
         assert all(bool((g == value).all()) for g in grads)
     check_no_device_error()
+
+
+# ----------------------------- calls from other threads -------------------- #
+def test_calls_from_a_thread_that_has_used_nothing_yet():
+    """A thread's first CUDA call may be the few-token layer or the grouped FFN, both of which begin with tensor maps."""
+    wl = W.make(LS("thread", 8, 256, 256, 4, 2, 0.0, W.BF16), seed=24, micro_batches=1, with_dy=False)
+    e = decode_ref(wl, 8)
+    r = decode(wl, 8)
+    L = layer.from_workload(wl)
+    L.forward(r["x"])
+    torch.cuda.synchronize()
+    sv, w, failed = L.saved, r["w"], []
+    y_perm = sv["y_perm"].clone()
+    r["y"].fill_(float("nan"))
+    stream = torch.cuda.current_stream()
+
+    def few():
+        pkg.moe_layer_decode(r["cfg"], w, r["x"], None, r["y"], r["ids"], r["gates"], r["ws"], stream)
+
+    def ffn():
+        pkg.moe_grouped_ffn(L.cfg, sv["x_perm"], sv["counts"], sv["offsets"], w["W1"], w["W3"], w["W2"], sv["h"],
+                            sv["y_perm"], sv["a"], sv["b"], stream)
+
+    def guarded(call):
+        try:
+            call()
+        except Exception as ex:
+            failed.append(repr(ex))
+
+    for call in (few, ffn):
+        t = threading.Thread(target=guarded, args=(call,))
+        t.start()
+        t.join()
+    assert not failed, failed
+    check_decode(r, e)
+    assert torch.equal(y_perm.view(torch.int16), sv["y_perm"].view(torch.int16))
