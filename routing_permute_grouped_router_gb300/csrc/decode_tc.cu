@@ -768,19 +768,17 @@ __global__ void __launch_bounds__(TC_NT, 1) decode_tc_kernel(const __grid_consta
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 dec_encode = nullptr;
-
-bool dec_encode_ready() {
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+// Looked up once; a thread that comes meanwhile waits for it.
+PFN_cuTensorMapEncodeTiled_v12000 dec_encode() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      dec_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  return dec_encode != nullptr;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? fn : nullptr);
+  }();
+  return encode;
 }
 
 // bf16 rows in boxes of 64 columns, 128-byte swizzle: x as [rows][cols], weights
@@ -790,7 +788,7 @@ bool dec_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uin
   cuuint64_t strides[2] = {cols * 2, 128};
   cuuint32_t box[3] = {64, box_rows, 2};
   cuuint32_t estr[3] = {1, 1, 1};
-  return dec_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, weights ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+  return dec_encode()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, weights ? 3 : 2, const_cast<void*>(base), dims, strides, box,
                     estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -809,7 +807,7 @@ size_t decode_tc_whole_bytes(const Shape& s) {
 size_t decode_tc_h_bytes(const Shape& s) { return (size_t)(s.f / 64) * h_blocks(s) * 4096; }
 
 cudaError_t launch_decode_tc(const Shape& s, const DecodeArgs& args, int G, cudaStream_t st) {
-  if (!dec_encode_ready()) return cudaErrorNotSupported;
+  if (dec_encode() == nullptr) return cudaErrorNotSupported;
   DecodeArgs a = args;
   const uint32_t NT = (uint32_t)(s.T + 15) / 16 * 16;
   const int fixed = 1024 + (int)sizeof(Routing) + (int)sizeof(TcCtrl) + s.T * DEC_N * 4;

@@ -246,20 +246,17 @@ __global__ void __launch_bounds__(D_THREADS, 1) dwr_tc_kernel(const __grid_const
   if (warp == 1) tmem_dealloc(tmem_base, C::TCOLS);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 d_encode = nullptr;
-
-bool dwr_encode_ready() {
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+// Looked up once; a thread that comes meanwhile waits for it.
+PFN_cuTensorMapEncodeTiled_v12000 dwr_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      d_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  return d_encode != nullptr;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? fn : nullptr);
+  }();
+  return encode;
 }
 
 // 2-D bf16 tensor map: rows x cols with the given row pitch (elements), 128-byte swizzle.
@@ -269,7 +266,7 @@ bool map_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
   cuuint64_t strides[1] = {pitch * 2};
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return d_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  return dwr_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -326,7 +323,7 @@ size_t dwr_tc_split_bytes(const Shape& s) { return (size_t)3 * pad_experts(s.E) 
 
 cudaError_t launch_dwr_tc(const Shape& s, const void* x, const float* dl, void* dlsplit, float* partial,
                           uint32_t* err, cudaStream_t st) {
-  if (!dwr_encode_ready()) return cudaErrorNotSupported;
+  if (dwr_encoder() == nullptr) return cudaErrorNotSupported;
   const int N = pad_experts(s.E), tp = dl_pitch(s.T);
   {
     LaunchScope ls(KK_SPLIT_DL, st);

@@ -1041,20 +1041,17 @@ __global__ void __launch_bounds__(THREADS, 1) tc_gemm_kernel(const __grid_consta
 }
 
 // ------------------------------ host side --------------------------------- //
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-bool g_encode_tried = false;
-
-bool resolve_encode() {
-  if (!g_encode_tried) {
-    g_encode_tried = true;
+// Looked up once; a thread that comes meanwhile waits for it.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  return g_encode != nullptr;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? fn : nullptr);
+  }();
+  return encode;
 }
 
 // 2-D tensor map over a row-major [rows, cols] matrix, 128-byte swizzle.
@@ -1065,7 +1062,7 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
   cuuint64_t strides[1] = {cols * es};
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return g_encode(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+  return encoder()(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1138,10 +1135,10 @@ cudaError_t launch_mode(const TcMaps& maps, const TcArgs& args, int64_t pair_bou
 
 }  // namespace
 
-bool tc_driver_ready() { return resolve_encode(); }
+bool tc_driver_ready() { return encoder() != nullptr; }
 
 cudaError_t tc_ffn_fwd(const Shape& s, const FfnFwdArgs& f, uint32_t* err, cudaStream_t st) {
-  if (!resolve_encode()) return cudaErrorNotSupported;
+  if (encoder() == nullptr) return cudaErrorNotSupported;
   if (s.max_rows == 0) return cudaSuccess;
   const uint64_t R = (uint64_t)s.max_rows, E = (uint64_t)s.E, d = (uint64_t)s.d, ff = (uint64_t)s.f;
   TcArgs a{};
@@ -1183,7 +1180,7 @@ cudaError_t tc_ffn_fwd(const Shape& s, const FfnFwdArgs& f, uint32_t* err, cudaS
 }
 
 cudaError_t tc_ffn_bwd(const Shape& s, const FfnBwdArgs& b, uint32_t* err, cudaStream_t st) {
-  if (!resolve_encode()) return cudaErrorNotSupported;
+  if (encoder() == nullptr) return cudaErrorNotSupported;
   const uint64_t E = (uint64_t)s.E, d = (uint64_t)s.d, ff = (uint64_t)s.f;
   if (s.max_rows == 0) {
     if (b.accumulate || b.part == 1) return cudaSuccess;

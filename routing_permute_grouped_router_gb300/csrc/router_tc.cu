@@ -409,20 +409,17 @@ __global__ void __launch_bounds__(R_THREADS, RCfg<N>::MIN_BLOCKS) router_tc_kern
   if (warp == 1) tmem_dealloc(tmem_base, C::TCOLS);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 r_encode = nullptr;
-
-bool router_encode_ready() {
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
+// Looked up once; a thread that comes meanwhile waits for it.
+PFN_cuTensorMapEncodeTiled_v12000 router_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      r_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  return r_encode != nullptr;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? fn : nullptr);
+  }();
+  return encode;
 }
 
 bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
@@ -431,7 +428,7 @@ bool make_map_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t col
   cuuint64_t strides[1] = {cols * 2};
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return r_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+  return router_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -491,7 +488,7 @@ size_t router_wsplit_bytes(const Shape& s) { return (size_t)3 * padded_experts(s
 cudaError_t launch_router_tc(const Shape& s, const void* x, const float* W_r, const float* bias, void* wsplit,
                              int32_t* ids, float* gates, float* probs, int32_t* hist, int32_t* ticket,
                              uint32_t* err, cudaStream_t st) {
-  if (!router_encode_ready()) return cudaErrorNotSupported;
+  if (router_encoder() == nullptr) return cudaErrorNotSupported;
   const int N = padded_experts(s.E);
   {
     const int64_t n = (int64_t)N * s.d;

@@ -2,6 +2,9 @@
 
 The tolerances are those of test_gpu_block_ops, whose helpers are used here.
 """
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -182,3 +185,52 @@ def test_calls_from_a_thread_that_has_used_nothing_yet():
     assert not failed, failed
     check_decode(r, e)
     assert torch.equal(y_perm.view(torch.int16), sv["y_perm"].view(torch.int16))
+
+
+FIRST_CALLS = '''
+import sys, threading
+import torch
+import routing_permute_grouped_router_gb300 as pkg
+from routing_permute_grouped_router_gb300 import layer, workload as W
+
+torch.cuda.set_device(0)
+wl = W.make(W.LayerShape("first", 256, 256, 256, 8, 2, 0.0, W.BF16, backward=True), seed=1, micro_batches=1, with_dy=True)
+x, dy = wl.x[0].torch("cuda"), wl.dy[0].torch("cuda")
+layers = [layer.from_workload(wl) for _ in range(8)]
+cfg = pkg.config(8, 256, 256, 8, 2)
+few = [(torch.empty_like(x[:8]), pkg.decode_workspace(cfg)) for _ in layers]
+torch.cuda.synchronize()
+start, failed = threading.Barrier(len(layers)), []
+
+def calls(i):
+    try:
+        v = torch.zeros(8, device="cuda")
+        pkg.moe_norm_fwd(v, v, v, 1e-5, v)  # the thread's context and the error word
+        start.wait()
+        if sys.argv[1] == "few":
+            pkg.moe_layer_decode(cfg, layers[i].weights, x[:8], None, few[i][0], None, None, few[i][1])
+        else:
+            layers[i].forward(x)
+            layers[i].backward(x, dy, False)
+    except Exception as e:
+        failed.append(repr(e))
+
+threads = [threading.Thread(target=calls, args=(i,)) for i in range(len(layers))]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+torch.cuda.synchronize()
+assert not failed, failed
+assert pkg.moe_get_device_error() == (0, 0)
+for i in range(1, len(layers)):
+    assert torch.equal(few[0][0], few[i][0]) if sys.argv[1] == "few" else torch.equal(layers[0].y, layers[i].y)
+'''
+
+
+@pytest.mark.parametrize("kind", ["few", "layer"])
+def test_first_calls_from_several_threads(kind):
+    """Threads whose first calls of a process coincide all get the driver's tensor-map encoder."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS, kind], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
