@@ -11,11 +11,11 @@
 // CTA, or a warp of one where 32 are enough), 16 elements each: 64 to 512 rows
 // are in work on an SM's registers while plain copies bring the next ones into
 // a ring in shared memory, up to four rows deep, so the loads' latency is out of
-// the way of the two reductions of a row.  (32768 x 4096 bf16: 92.5 us forward,
-// 5.8 TB/s, and 168 us backward, 6.4 TB/s; with the loads in registers and no
-// ring 155 and 367.)  The variance
-// is the sum of squared distances from the mean: no cancellation of a large
-// mean, no second read.  Threads keep their columns' gamma, beta and, in the
+// the way of the two reductions of a row.  (32768 x 4096 bf16: 87 us forward,
+// 6.2 TB/s, and 168 us backward, 6.4 TB/s; with the loads in registers and no
+// ring 155 and 367.)  The variance is of distances from a point near the mean,
+// so a large mean neither cancels nor loses the last bits of x - mean, and needs
+// no second read.  Threads keep their columns' gamma, beta and, in the
 // backward, dgamma and dbeta sums in registers over all rows of the CTA; the
 // sums of the CTAs are added in CTA order by a second kernel, so results do
 // not depend on timing.  All statistics and sums are fp32.
@@ -101,6 +101,14 @@ struct Group {
     return scratch[turn * 16 + g * warps + (threadIdx.x & (warps - 1))];
   }
 };
+// Two sums over a warp: of a in the lower half of its lanes, of b in the upper half.
+__device__ __forceinline__ float half_sums(float a, float b, bool upper) {
+  float v = upper ? b : a;
+  v += __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 __device__ __forceinline__ float sum_over(float v, int n) {  // n a power of two up to 16
 #pragma unroll
   for (int o = 1; o <= 8; o *= 2)
@@ -165,10 +173,11 @@ struct Chunk {
   static constexpr int N = WHOLE ? Vec<T>::N : 8;
 };
 
-// Chunk i of a row, from the ring (zeros past the row's end).
+// Chunk i of a row, from the ring.  Past the row's end come zeros, or `fill`
+// where rows are not whole vectors.
 template <typename T, bool WHOLE>
 __device__ __forceinline__ void take(const char* stage, const Span& sp, const T* tensor, int r, int tpr, int d, int i,
-                                     float2 (&v)[Chunk<T, WHOLE>::N / 2]) {
+                                     float2 (&v)[Chunk<T, WHOLE>::N / 2], float fill = 0.f) {
   if constexpr (WHOLE) {
     const int q = r + i * tpr;
     uint4 u = make_uint4(0, 0, 0, 0);
@@ -184,13 +193,13 @@ __device__ __forceinline__ void take(const char* stage, const Span& sp, const T*
       const char* p = stage + at;
 #pragma unroll
       for (int j = 0; j < 8; ++j, p += step) {
-        const float w = j < left ? to_f32(*reinterpret_cast<const T*>(p)) : 0.f;
+        const float w = j < left ? to_f32(*reinterpret_cast<const T*>(p)) : fill;
         (j & 1 ? v[j / 2].y : v[j / 2].x) = w;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j, at += step) {
-        float w = 0.f;
+        float w = fill;
         if (j < left)
           w = to_f32(at < sp.bytes ? *reinterpret_cast<const T*>(stage + at) : tensor[(sp.at + at) / (int64_t)sizeof(T)]);
         (j & 1 ? v[j / 2].y : v[j / 2].x) = w;
@@ -318,10 +327,22 @@ __device__ __forceinline__ void take_weights(const float* w, int r, int tpr, int
   }
 }
 
+// Distances are taken from the mean of a sample of the row, 32 elements spread
+// over it (fewer of a short row), and their sum and the sum of their squares
+// then give the mean and the variance in one reduction:
+//   mean = near + s1 / d,  variance = s2 / d - (s1 / d)^2
+// The sample's mean is about a sixth of a deviation off, so hardly anything
+// cancels; at worst, where the sample alone holds what is large, the terms are
+// d / 32 times their difference (a channel of 1000 in the sample, d 8192: rstd to
+// 1e-6, not 2e-7).  The sample's size is a power of two, so the mean of a row of
+// one value is that value and x - mean is 0, for any d and value: the rounded
+// sum of a row times a rounded 1 / d can be ulps away, which eps 1e-5 makes 0.02
+// gamma of y at the value 1000.  (Two-pass sums over the warps, corrected by the
+// sum of the distances: 107 us at 32768 x 4096 bf16, this form 87.)
 template <typename T, bool WHOLE>
 __global__ void __maxnreg__(FWD_REGS) norm_fwd_kernel(const NormArgs a) {
   constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2;
-  __shared__ float4 scratch[2 * 16];
+  __shared__ float scratch[2][2][16];
   __shared__ uint64_t bars[MAX_GROUPS * RING];
   int turn = 0;
   const Group<false> grp(a.tpr);
@@ -332,53 +353,51 @@ __global__ void __maxnreg__(FWD_REGS) norm_fwd_kernel(const NormArgs a) {
   float2 ga[EPT / 2], be[EPT / 2];
   take_weights<VN>(a.gamma, r, a.tpr, a.d, ga);
   take_weights<VN>(a.beta, r, a.tpr, a.d, be);
-  // the warp's elements of a row
-  float mine = 0.f;
-#pragma unroll
-  for (int c = 0; c < EPT; ++c) mine += in_row<VN>(r, a.tpr, c, a.d) ? 1.f : 0.f;
-  const float wn = warp_sum(mine), winv = wn > 0.f ? 1.f / wn : 0.f;
+  // The lane's element of the sample: the first one that it holds where a warp
+  // has the row (of `size` lanes that hold any), else one of its own 4-byte bank
+  // of shared memory, 33 banks at least ahead of the row's end.
+  const int lane = threadIdx.x % 32, full = __popc(__ballot_sync(0xffffffffu, in_row<VN>(lane, a.tpr, 0, a.d)));
+  const int size = 1 << (31 - __clz(full | 1));
+  const float each = lane < size ? 1.f / (float)size : 0.f;
+  const int from_at = nw > 1 ? (lane * (a.d * (int)sizeof(T) / 4 - 64) / 32 / 32 * 32 + lane) * 4
+                             : (lane < size ? lane * VN * (int)sizeof(T) : 0);
+  const bool upper = lane >= 16;
+  const float eps = upper ? a.eps : 0.f;
 #pragma unroll 1
   for (int64_t row = R.first; row < a.rows; row += R.step) {
     const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
     R.wait(a.err);
-    float2 v[EPT / 2 / CN][CN], s2 = both(0.f);
+    const int sat = sp.skip + from_at;
+    float near = to_f32(WHOLE || sp.whole || sat < sp.bytes ? *reinterpret_cast<const T*>(R.place(0) + sat)
+                                                            : static_cast<const T*>(a.x)[(sp.at + sat) / (int64_t)sizeof(T)]);
+    near = warp_sum(each != 0.f ? near * each : 0.f);
+    float2 v[EPT / 2 / CN][CN];
 #pragma unroll
-    for (int i = 0; i < EPT / 2 / CN; ++i) {
-      take<T, WHOLE>(R.place(0), sp, static_cast<const T*>(a.x), r, a.tpr, a.d, i, v[i]);
-#pragma unroll
-      for (int c = 0; c < CN; ++c) s2 = add2(s2, v[i][c]);
-    }
-    // The warp's mean, the distances from it and their squares first; the
-    // warps then combine theirs with the distances of their means.
-    const float ws = warp_sum(s2.x + s2.y), wmean = ws * winv;
-    const float2 from = both(-wmean);
-    s2 = both(0.f);
+    for (int i = 0; i < EPT / 2 / CN; ++i)
+      take<T, WHOLE>(R.place(0), sp, static_cast<const T*>(a.x), r, a.tpr, a.d, i, v[i], near);
+    float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < EPT / 2 / CN; ++i)
 #pragma unroll
       for (int c = 0; c < CN; ++c) {
-        const int at = 2 * (i * CN + c);
-        v[i][c] = add2(v[i][c], from);
-        if constexpr (WHOLE) {
-          if (in_row<VN>(r, a.tpr, at, a.d)) s2 = fma2(v[i][c], v[i][c], s2);
-        } else {
-          if (in_row<VN>(r, a.tpr, at, a.d)) s2.x = fmaf(v[i][c].x, v[i][c].x, s2.x);
-          if (in_row<VN>(r, a.tpr, at + 1, a.d)) s2.y = fmaf(v[i][c].y, v[i][c].y, s2.y);
-        }
+        // past the row's end the distance is 0
+        v[i][c] = add2(v[i][c], both(!WHOLE || in_row<VN>(r, a.tpr, 2 * (i * CN + c), a.d) ? -near : 0.f));
+        s1 = add2(s1, v[i][c]);
+        s2 = fma2(v[i][c], v[i][c], s2);
       }
-    float m2 = warp_sum(s2.x + s2.y), mean = wmean;
+    // s1 in the lower half of the lanes, s2 in the upper half, over the warp and then over the warps
+    float m = half_sums(s1.x + s1.y, s2.x + s2.y, upper);
     if (nw > 1) {
-      grp.give(make_float4(ws, m2, wmean, wn), scratch, turn);
+      if ((lane & 15) == 0) scratch[turn][upper][threadIdx.x / 32] = m;
       grp.sync();
-      const float4 w = grp.get(scratch, turn);
+      m = sum_over(scratch[turn][upper][lane & (nw - 1)], nw);
       turn ^= 1;
-      mean = sum_over(w.x, nw) * inv;
-      m2 = sum_over(fmaf(w.w * (w.z - mean), w.z - mean, w.y), nw);
     }
     __syncwarp();
     R.taken(row, r == 0);
-    const float rstd = rsqrtf(fmaf(m2, inv, a.eps));
-    const float2 by = both(rstd), shift = both((wmean - mean) * rstd);
+    m = fmaf(m, inv, eps);
+    const float left = __shfl_sync(0xffffffffu, m, 0), rstd = rsqrtf(fmaf(-left, left, __shfl_sync(0xffffffffu, m, 16)));
+    const float2 by = both(rstd), shift = both(-left * rstd);
 #pragma unroll
     for (int i = 0; i < EPT / 2 / CN; ++i) {
 #pragma unroll
@@ -386,7 +405,7 @@ __global__ void __maxnreg__(FWD_REGS) norm_fwd_kernel(const NormArgs a) {
       put<T, WHOLE>(y + row * a.d, r, a.tpr, a.d, i, v[i]);
     }
     if (r == 0) {
-      if (a.mean) a.mean[row] = mean;
+      if (a.mean) a.mean[row] = near + left;
       if (a.rstd) a.rstd[row] = rstd;
     }
   }
@@ -538,7 +557,9 @@ __global__ void __launch_bounds__(RED_COLS * RED_STRIPS) norm_bwd_reduce_kernel(
 }
 
 // ---- rows of more than MAX_TPR * EPT elements: one CTA a row, walked in a
-// loop, again from cache for each pass; dgamma and dbeta in a pass of their own ----
+// loop, again from cache for each pass; dgamma and dbeta in a pass of their own.
+// The forward takes distances from the rounded mean and what is left of their
+// sum off again. ----
 __device__ __forceinline__ float2 cta_sum(float2 s, float4* scratch, int& turn) {
   const Group<false> all(WIDE_NT);
   all.give(make_float4(warp_sum(s.x), warp_sum(s.y), 0.f, 0.f), scratch, turn);
@@ -592,16 +613,20 @@ __global__ void __launch_bounds__(WIDE_NT) norm_fwd_wide_kernel(const NormArgs a
 #pragma unroll
       for (int j = 0; j < VN; ++j) s += v[j];
     }
-    const float mean = cta_sum(make_float2(s, 0.f), scratch, turn).x * inv;
-    s = 0.f;
+    const float near = cta_sum(make_float2(s, 0.f), scratch, turn).x * inv;
+    float2 q = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int i = threadIdx.x * VN; i < a.d; i += WIDE_NT * VN) {
       float v[VN];
       ld_n<T, VN>(xr + i, v);
 #pragma unroll
-      for (int j = 0; j < VN; ++j) s = fmaf(v[j] - mean, v[j] - mean, s);
+      for (int j = 0; j < VN; ++j) {
+        q.x += v[j] - near;
+        q.y = fmaf(v[j] - near, v[j] - near, q.y);
+      }
     }
-    const float rstd = rsqrtf(fmaf(cta_sum(make_float2(s, 0.f), scratch, turn).x, inv, a.eps));
+    q = cta_sum(q, scratch, turn);
+    const float left = q.x * inv, rstd = rsqrtf(fmaf(q.y, inv, a.eps) - left * left), mean = near + left;
 #pragma unroll 2
     for (int i = threadIdx.x * VN; i < a.d; i += WIDE_NT * VN) {
       float v[VN], g[VN], b[VN];
@@ -609,7 +634,7 @@ __global__ void __launch_bounds__(WIDE_NT) norm_fwd_wide_kernel(const NormArgs a
       ld_w<VN>(a.gamma + i, g);
       ld_w<VN>(a.beta + i, b);
 #pragma unroll
-      for (int j = 0; j < VN; ++j) v[j] = fmaf((v[j] - mean) * rstd, g[j], b[j]);
+      for (int j = 0; j < VN; ++j) v[j] = fmaf(((v[j] - near) - left) * rstd, g[j], b[j]);
       st_n<T, VN>(yr + i, v);
     }
     if (threadIdx.x == 0) {
