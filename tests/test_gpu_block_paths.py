@@ -11,11 +11,12 @@ import numpy as np
 import pytest
 import torch
 
+import _block_ref as ref
 import routing_permute_grouped_router_gb300 as pkg
-from _util import check_no_device_error
+from _util import check_no_device_error, to64
 from routing_permute_grouped_router_gb300 import layer
 from routing_permute_grouped_router_gb300 import workload as W
-from test_gpu_block_ops import check_decode, decode, decode_ref
+from test_gpu_block_ops import TYPES, check_decode, decode, decode_ref, near, norm_inputs
 
 pytestmark = pytest.mark.gpu
 LS = W.LayerShape
@@ -68,6 +69,94 @@ def test_decode_few_rows_with_whole_and_split_tiles(shape):
         r["ws"].fill_(255)
         pkg.moe_layer_decode(r["cfg"], r["w"], r["x"], None, r["y"], r["ids"], r["gates"], r["ws"])
         assert torch.equal(first, r["y"])
+    check_no_device_error()
+
+
+@pytest.mark.parametrize("shape", [LS("long_d", 64, 4096, 1536, 4, 4, 0.0, W.BF16),
+                                   LS("one_row_each", 3, 4096, 1536, 8, 4, 0.0, W.BF16)], ids=lambda s: s.name)
+def test_decode_many_units_a_cta(shape):
+    """A CTA's share of the weights is longer than its ring of stages, whose places are used again."""
+    wl = W.make(shape, seed=18, micro_batches=1, with_dy=False)
+    e = decode_ref(wl, shape.T)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert up_product_split(shape, e["ids"], sms)[1] >= 10  # of at most eight stages
+    check_decode(decode(wl, shape.T), e)
+
+
+# ----------------------------- several rows to a group of threads ---------- #
+LONG = [(3001, 4096), (1500, 8192), (12001, 1021), (24001, 60), (24001, 129), (2000, 10001), (1300, 16384)]
+
+
+def near_sum(name, got, exp, terms, rel=0.0, size=None):
+    """Sums of `terms` comparable fp32 terms: sqrt(terms) roundings, 64 at least, of the largest value (or `size`)."""
+    big = 2.0 ** -24 * max(64.0, terms ** 0.5)
+    scale = 1.0 if size is None else max(1.0, size / max(np.abs(exp).max(), 1e-30))
+    near(name, got, exp, rel, big * scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d", LONG)
+def test_norm_of_many_rows(rows, d, dtype):
+    """Every group of threads takes several rows, more than its ring has places where the ring is used."""
+    x, dy, res, gamma, beta = norm_inputs(rows, d, dtype, seed=rows + d)
+    f = dict(dtype=torch.float32, device="cuda")
+    y, mean, rstd = torch.full_like(x, float("nan")), torch.empty(rows, **f), torch.empty(rows, **f)
+    pkg.moe_norm_fwd(x, gamma, beta, 1e-5, y, mean, rstd)
+    x64, dy64, g64 = to64(x), to64(dy), to64(gamma)
+    ey, emean, erstd = ref.norm_fwd(x64, g64, to64(beta), 1e-5)
+    near_sum("y", y, ey, d)
+    near_sum("mean", mean, emean, d)
+    near_sum("rstd", rstd, erstd, d)
+
+    m64, r64 = to64(mean), to64(rstd)
+    edx, edg, edb = ref.norm_bwd(x64, dy64, g64, m64, r64)
+    size = np.abs(r64[:, None] * dy64 * g64).max()  # of the terms of dx
+    ws = pkg.norm_workspace(rows, d).fill_(255)
+    dg, db = torch.full((d,), 3.0, device="cuda"), torch.full((d,), -2.0, device="cuda")
+    dx = torch.full_like(x, float("nan"))
+    pkg.moe_norm_bwd(x, dy, gamma, mean, rstd, None, dx, dg, db, False, ws)
+    near_sum("dx", dx, edx, d, size=size)
+    near_sum("dgamma", dg, edg, rows)
+    near_sum("dbeta", db, edb, rows)
+    pkg.moe_norm_bwd(x, dy, gamma, mean, rstd, res, dx, dg, db, True, ws)
+    near_sum("dx + dres", dx, edx + to64(res), d, size=size)
+    near_sum("2 dgamma", dg, 2 * edg, rows)
+    near_sum("2 dbeta", db, 2 * edb, rows)
+
+    # in place of each input: the same bits
+    pkg.moe_norm_bwd(x, dy, gamma, mean, rstd, res, dx, dg, db, False, ws)
+    want = [t.clone() for t in (dx, dg, db)]
+    for i in range(3):
+        t = [x.clone(), dy.clone(), res.clone()]
+        pkg.moe_norm_bwd(t[0], t[1], gamma, mean, rstd, t[2], t[i], dg, db, False, ws)
+        assert torch.equal(t[i], want[0]) and torch.equal(dg, want[1]) and torch.equal(db, want[2])
+    z = x.clone()
+    pkg.moe_norm_fwd(z, gamma, beta, 1e-5, z)
+    assert torch.equal(z, y)
+    check_no_device_error()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dropout_of_many_blocks(dtype):
+    """Every thread takes several blocks of eight, the next loaded while this one is drawn for."""
+    n, p, seed, offset = (1 << 23) + 5, 0.3, 0x123456789ABCDEF, 77
+    y, r = (torch.randn(n, device="cuda").to(TYPES[dtype]) for _ in range(2))
+    y[y == 0] = 1
+    e = ref.dropout(to64(y), p, seed, offset)
+    out = torch.full_like(y, float("nan"))
+    pkg.moe_dropout_add(y, None, out, p, seed, offset)
+    assert np.array_equal(to64(out) != 0, e != 0)
+    near("out", out, e, rel=2.0 ** -22, big=0)
+    dy = torch.empty_like(y)
+    pkg.moe_dropout_bwd(y, dy, p, seed, offset)
+    assert torch.equal(out, dy)
+    pkg.moe_dropout_add(y, r, out, p, seed, offset)
+    near("out + residual", out, e + to64(r), rel=2.0 ** -22, big=2.0 ** -22)
+    kept = torch.from_numpy(e != 0).cuda()
+    assert torch.equal(out[~kept], r[~kept])
+    z = r.clone()
+    pkg.moe_dropout_add(y, z, z, p, seed, offset)
+    assert torch.equal(z, out)
     check_no_device_error()
 
 
