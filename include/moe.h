@@ -323,9 +323,10 @@ moe_status moe_decode_workspace_size(const moe_config* cfg, size_t* bytes);
  * wanted) as there.  Only the weights of experts with kept rows are read.  a
  * and b are fp32 sums and are not rounded to the activations' type, so y
  * carries one rounding to it.
- * Deterministic.  It is a cooperative launch of one block an SM: on a GPU that
- * other streams keep busy it starts when all its blocks fit.  residual may
- * be y; x must not overlap y. */
+ * Deterministic.  It is a cooperative launch of one block an SM for bf16 and of
+ * two for float32: on a GPU that other streams keep busy it starts when all its
+ * blocks fit.  Calls that may overlap want a workspace each.  residual may be y;
+ * x must not overlap y. */
 moe_status moe_layer_decode(const moe_config* cfg, const moe_weights* w, const void* x, const void* residual, void* y,
                             int32_t* ids, float* gates, void* ws, size_t ws_bytes, moe_stream_t stream);
 
@@ -338,7 +339,8 @@ moe_status moe_norm_fwd(int64_t rows, int32_t d, int32_t dtype, const void* x, c
                         float eps, void* y, float* mean, float* rstd, moe_stream_t stream);
 
 /* Bytes of workspace that moe_norm_bwd needs: partial sums of dgamma and
- * dbeta, at most two rows of d an SM.  Host only; device as above. */
+ * dbeta, at most two rows of d an SM, four where d > 8192.  Host only; device as
+ * above. */
 moe_status moe_norm_workspace_size(int64_t rows, int32_t d, size_t* bytes);
 
 /* Backward of moe_norm_fwd, n = (x - mean) * rstd, v = dy * gamma:

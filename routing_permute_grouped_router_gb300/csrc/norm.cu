@@ -8,9 +8,10 @@
 //
 // Both passes are bound by HBM: the forward reads and writes a row once, the
 // backward reads x, dy (and dres) and writes dx.  `tpr` threads share a row (a
-// CTA, or a warp of one where 32 are enough), 16 elements each: 64 to 512 rows
-// are in work on an SM's registers while plain copies bring the next ones into
-// a ring in shared memory, up to four rows deep, so the loads' latency is out of
+// CTA, or a warp of one where 32 are enough), 16 elements each: 24 rows of up to
+// 512 elements, three of 4096, one of 8192 are in the registers of an SM in the
+// forward (16, two and one in the backward) while plain copies bring the next
+// ones into a ring in shared memory, up to four rows deep, so the loads' latency is out of
 // the way of the two reductions of a row.  (32768 x 4096 bf16: 87 us forward,
 // 6.2 TB/s, and 168 us backward, 6.4 TB/s; with the loads in registers and no
 // ring 155 and 367.)  The variance is of distances from a point near the mean,
@@ -415,7 +416,7 @@ __global__ void __maxnreg__(FWD_REGS) norm_fwd_kernel(const NormArgs a) {
 // the next row are formed before dx of this one: the reduction's shuffles and
 // barrier run under arithmetic that does not wait for them.  (32768 x 4096 bf16:
 // 168 us; one row after the other 197.  The forward, bound by instruction issue,
-// loses by it: 104 us, not 92.5.)
+// lost by it when it had two reductions a row: 104 us, not 92.5.)
 template <typename T, bool WHOLE, bool RES>
 __global__ void __launch_bounds__(BWD_NT, 1) norm_bwd_kernel(const NormArgs a) {
   constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2, NBUF = RES ? 3 : 2;
