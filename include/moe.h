@@ -371,6 +371,129 @@ moe_status moe_dropout_add(int64_t n, int32_t dtype, const void* y, const void* 
 moe_status moe_dropout_bwd(int64_t n, int32_t dtype, const void* dout, void* dy, float p, uint64_t seed,
                            uint64_t offset, moe_stream_t stream);
 
+/* ---- From blocks to a training step ----
+ * The residual path between two blocks with the norms on either side of it,
+ * the loss at the end of the stack, and the clipping of the accumulated
+ * gradients.  (The pages have no counterpart.)  Conventions as above: dense
+ * rows, tensors of `dtype` 16-byte aligned unless a parameter says otherwise,
+ * float32 vectors 4-byte aligned. */
+
+/* The residual path between two blocks, per row t and channel c:
+ *   u   = y * ry * gamma_post,  ry = 1 / sqrt(sum(y^2) / d + eps)     (gamma_post NULL: u = y)
+ *   out = residual_scale * x + branch_scale * row_gate[t] * gate[c] * u   (a gate that is NULL is 1; y NULL: no branch)
+ *   h   = out * ro * gamma_next,  ro = 1 / sqrt(sum(out^2) / d + eps)  (gamma_next NULL: no h)
+ * y is the block's output, x the residual stream in front of it, h the next
+ * block's input.  Without y it is the norm in front of the first block, without
+ * gamma_next the path behind the last.  Squares are summed in fp32. */
+typedef struct {
+  int64_t rows;
+  int32_t d;                 /* 1 <= d <= 65536, rows * d <= 2^40 */
+  int32_t dtype;             /* of x, y, out, h and their gradients */
+  const float* gamma_post;   /* [d] or NULL */
+  const float* gamma_next;   /* [d] or NULL */
+  const float* gate;         /* [d] or NULL: a gate of each channel */
+  const float* row_gate;     /* [rows] or NULL: a gate of each row */
+  float residual_scale;
+  float branch_scale;
+  float eps;                 /* >= 0 */
+} moe_residual_norm;
+
+/* Gradients of the parameters, float32; each NULL where it is not wanted, and
+ * where the forward has no such parameter. */
+typedef struct {
+  float* dgamma_post;  /* [d] */
+  float* dgamma_next;  /* [d] */
+  float* dgate;        /* [d] */
+  float* drow_gate;    /* [rows], overwritten whatever `accumulate` says */
+} moe_residual_norm_grads;
+
+/* Writes out and h.  out may be NULL where it is not wanted; h is required with
+ * gamma_next and NULL without.  rstd_post and rstd_next [rows] (ry and ro) are
+ * kept for the backward, or NULL.  h is formed from out before its rounding.
+ * out and h may be x or y. */
+moe_status moe_residual_norm_fwd(const moe_residual_norm* p, const void* x, const void* y, void* out, void* h,
+                                 float* rstd_post, float* rstd_next, moe_stream_t stream);
+
+/* Bytes of workspace that moe_residual_norm_bwd needs.  Host only; it scales
+ * with the SM count of the current device. */
+moe_status moe_residual_norm_workspace_size(int64_t rows, int32_t d, size_t* bytes);
+
+/* Backward of moe_residual_norm_fwd from out and y as they are in memory and
+ * the kept ry and ro.  n = out ro, m = y ry (m = y without gamma_post):
+ *   D  = dout + ro (v - n sum(v n) / d),  v = dh gamma_next
+ *   dx = residual_scale D;  G = branch_scale row_gate gate D;  w = G gamma_post
+ *   dy = ry (w - m sum(w m) / d)   (G without gamma_post)
+ *   dgamma_next (+)= sum over rows of dh n;  dgamma_post (+)= sum over rows of G m
+ *   dgate (+)= sum over rows of branch_scale row_gate D u
+ *   drow_gate[t] = sum over channels of branch_scale gate D u
+ * dout (NULL: none) is the gradient that reaches out past the next norm; dh is
+ * required with gamma_next.  dx may be NULL, dout or dh; dy may be dh or dout. out and
+ * rstd_next are read with gamma_next only, y and dy are required where the
+ * forward had a branch and NULL where it had none.  accumulate as in
+ * moe_layer_bwd.  Sums run in an order fixed by the sizes and the device. */
+moe_status moe_residual_norm_bwd(const moe_residual_norm* p, const void* out, const void* y, const void* dh,
+                                 const void* dout, const float* rstd_post, const float* rstd_next, void* dx, void* dy,
+                                 const moe_residual_norm_grads* grads, int accumulate, void* ws, size_t ws_bytes,
+                                 moe_stream_t stream);
+
+/* One gradient tensor: n elements of `dtype` at src, aligned to their own size. */
+typedef struct {
+  const void* src;
+  void* dst;      /* receives the clipped gradient: src itself, another tensor of n elements, or NULL (norm only) */
+  int64_t n;      /* 0 <= n <= 2^40 */
+  int32_t dtype;  /* moe_dtype */
+} moe_grad;
+
+/* Most tensors of one moe_clip_grads call. */
+#define MOE_CLIP_MAX_TENSORS 65536
+
+/* Bytes of workspace that moe_clip_grads needs for `count` tensors.  Host only;
+ * device as above. */
+moe_status moe_clip_workspace_size(int32_t count, size_t* bytes);
+
+/* The 2-norm of all tensors together, and the gradients clipped to it:
+ *   norm = sqrt(sum over tensors of sum(src^2));  dst = src * min(1, max_norm / norm)
+ * `grads` is a HOST array, read during the call alone.  *norm is a device
+ * float.  max_norm is positive; INFINITY clips nothing.  A norm that is not
+ * finite (a gradient holds an infinity or a NaN, or the norm itself passes
+ * float32) clips nothing either: dst = src, and the caller sees *norm.  Where
+ * nothing is clipped a tensor whose dst is its src is not written.  Squares are summed
+ * without overflow or underflow whatever the values, in an order fixed by the
+ * sizes and the device; subnormal float32 gradients count.  A dst must not
+ * overlap another tensor's src or dst, or its own src but for being the same
+ * (MOE_ERR_INVALID_ARG). */
+moe_status moe_clip_grads(const moe_grad* grads, int32_t count, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                          moe_stream_t stream);
+
+/* Softmax cross entropy over a vocabulary of V, x [T, d] and W [V, d] of `dtype`, whose
+ * logits z = x W^T are formed a piece at a time and never kept:
+ *   lse[t] = log sum_v exp(z[t, v]);  loss[t] = lse[t] - z[t, labels[t]]
+ * labels [T] int32.  A token whose label is negative is ignored: loss and lse are
+ * 0, whatever its row of x holds.  A label >= V is ignored too and recorded in
+ * the device error word.  total (NULL: not wanted) receives two floats: the sum
+ * of the losses and the number of labelled tokens.  0 <= T <= 2^24,
+ * 1 <= V <= 2^24, 1 <= d <= 65536, d a multiple of 8 for MOE_BF16 and of 4 for
+ * MOE_F32.  Deterministic. */
+moe_status moe_vocab_loss_fwd(int32_t T, int32_t d, int32_t V, int32_t dtype, const void* x, const void* W,
+                              const int32_t* labels, float* loss, float* lse, float* total, void* ws, size_t ws_bytes,
+                              moe_stream_t stream);
+
+/* Bytes of workspace of moe_vocab_loss_fwd (training = 0) or of both calls
+ * (training = 1).  Host only; device as above. */
+moe_status moe_vocab_loss_workspace_size(int32_t T, int32_t d, int32_t V, int32_t dtype, int training, size_t* bytes);
+
+/* Its gradient, the logits formed again:
+ *   dz[t, v] = dloss[t] (exp(z[t, v] - lse[t]) - [v = labels[t]])   (0 for ignored tokens)
+ *   dx = dz W [T, d] in dtype;  dW (+)= dz^T x [V, d] in dw_dtype
+ * dloss [T] is the gradient that reaches each loss; NULL is that of the mean
+ * over the labelled tokens.  dw_dtype is MOE_F32, or MOE_BF16 in a bf16 call;
+ * in a bf16 call dz is held in 16 significant bits for a float32 dW and in 8 for
+ * dx and a bf16 dW.  dx or dW may be NULL, not both.
+ * accumulate as in moe_layer_bwd, for dW. */
+moe_status moe_vocab_loss_bwd(int32_t T, int32_t d, int32_t V, int32_t dtype, int32_t dw_dtype, const void* x,
+                              const void* W, const int32_t* labels, const float* lse, const float* dloss, void* dx,
+                              void* dW, int accumulate, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Waits for the current device to finish, then reads the device error word:
  * *code is MOE_OK, MOE_ERR_DEVICE_CHECK or MOE_ERR_TIMEOUT, *detail says which
  * kernel and check; clear != 0 resets the word.  Either output may be NULL. */

@@ -6,8 +6,8 @@ current stream to the C ABI of ``libmoe_gb300.so``.  All arithmetic runs in
 the library's CUDA kernels.  If the library has not been built the import of
 any entry point raises; there is no fallback.
 
-Helpers ``allocate_saved``, ``allocate_grads``, ``workspace``, ``decode_workspace``
-and ``norm_workspace`` size buffers with ``moe_max_rows`` and the
+Helpers ``allocate_saved``, ``allocate_grads``, ``workspace`` and the ``*_workspace``
+of single operators size buffers with ``moe_max_rows`` and the
 ``moe_*workspace_size`` calls and allocate them with torch.
 """
 from __future__ import annotations
@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(HERE, "libmoe_gb300.so")
 MOE_F32 = 0
 MOE_BF16 = 1
 MOE_DECODE_MAX_T = 64
+MOE_CLIP_MAX_TENSORS = 65536
 
 STATUS = ["MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_SHAPE", "MOE_ERR_DTYPE", "MOE_ERR_ALIGNMENT",
           "MOE_ERR_WORKSPACE", "MOE_ERR_CUDA", "MOE_ERR_DEVICE_CHECK", "MOE_ERR_TIMEOUT", "MOE_ERR_UNSUPPORTED"]
@@ -52,6 +53,21 @@ class MoeSaved(ctypes.Structure):
 
 class MoeGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dW_r", "dW1", "dW3", "dW2", "aux_loss")]
+
+
+class MoeResidualNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gamma_post", ctypes.c_void_p), ("gamma_next", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("row_gate", ctypes.c_void_p), ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+
+class MoeResidualNormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dgamma_post", "dgamma_next", "dgate", "drow_gate")]
+
+
+class MoeGrad(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -85,6 +101,15 @@ _SIGNATURES = {
     "moe_norm_bwd": [_L, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _Z, _P],
     "moe_dropout_add": [_L, _I, _P, _P, _P, ctypes.c_float, _U, _U, _P],
     "moe_dropout_bwd": [_L, _I, _P, _P, ctypes.c_float, _U, _U, _P],
+    "moe_residual_norm_fwd": [ctypes.POINTER(MoeResidualNorm), _P, _P, _P, _P, _P, _P, _P],
+    "moe_residual_norm_workspace_size": [_L, _I, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_residual_norm_bwd": [ctypes.POINTER(MoeResidualNorm), _P, _P, _P, _P, _P, _P, _P, _P,
+                              ctypes.POINTER(MoeResidualNormGrads), _I, _P, _Z, _P],
+    "moe_clip_workspace_size": [_I, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_clip_grads": [ctypes.POINTER(MoeGrad), _I, ctypes.c_float, _P, _P, _Z, _P],
+    "moe_vocab_loss_fwd": [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _Z, _P],
+    "moe_vocab_loss_workspace_size": [_I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_vocab_loss_bwd": [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _Z, _P],
     "moe_get_device_error": [ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32), _I],
     "moe_launch_count": [],
     "moe_selftest_bounded_wait": [ctypes.c_int64, _I, _P],
@@ -184,6 +209,25 @@ def moe_decode_workspace_size(cfg: MoeConfig) -> int:
 def moe_norm_workspace_size(rows: int, d: int) -> int:
     b = ctypes.c_size_t()
     _check("moe_norm_workspace_size", lib().moe_norm_workspace_size(rows, d, ctypes.byref(b)))
+    return b.value
+
+
+def moe_residual_norm_workspace_size(rows: int, d: int) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_residual_norm_workspace_size", lib().moe_residual_norm_workspace_size(rows, d, ctypes.byref(b)))
+    return b.value
+
+
+def moe_clip_workspace_size(count: int) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_clip_workspace_size", lib().moe_clip_workspace_size(count, ctypes.byref(b)))
+    return b.value
+
+
+def moe_vocab_loss_workspace_size(T: int, d: int, V: int, dtype: int, training: bool) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_vocab_loss_workspace_size",
+           lib().moe_vocab_loss_workspace_size(T, d, V, dtype, int(training), ctypes.byref(b)))
     return b.value
 
 
@@ -390,6 +434,125 @@ def moe_dropout_bwd(dout, dy, p: float, seed: int, offset: int, stream=None) -> 
         n, code, _arg("dout", dout, n, t), _arg("dy", dy, n, t), p, seed, offset, _stream_of(dout, stream)))
 
 
+# ----------------------------- training step ----------------------------- #
+def _residual_norm(x, gamma_post, gamma_next, gate, row_gate, residual_scale, branch_scale, eps):
+    rows, d, code = _rows(x)
+    f32 = _types[0]
+    return rows, d, MoeResidualNorm(rows, d, code, _arg("gamma_post", gamma_post, d, f32),
+                                    _arg("gamma_next", gamma_next, d, f32), _arg("gate", gate, d, f32),
+                                    _arg("row_gate", row_gate, rows, f32), residual_scale, branch_scale, eps)
+
+
+def moe_residual_norm_fwd(x, y, out, h, gamma_post=None, gamma_next=None, gate=None, row_gate=None,
+                          residual_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6, rstd_post=None,
+                          rstd_next=None, stream=None) -> None:
+    """out = residual_scale x + branch_scale row_gate gate norm(y), h = norm(out), over the rows of x [..., d].
+
+    RMS norms with the weights ``gamma_post`` and ``gamma_next`` [d]; without a weight there is no such norm (and no
+    ``h``).  ``gate`` [d] and ``row_gate`` [rows] are float32.  ``y`` None: h = norm(residual_scale x) alone.
+    """
+    rows, d, p = _residual_norm(x, gamma_post, gamma_next, gate, row_gate, residual_scale, branch_scale, eps)
+    f32, t, n = _types[0], x.dtype, rows * d
+    _check("moe_residual_norm_fwd", lib().moe_residual_norm_fwd(
+        p, _arg("x", x, n, t), _arg("y", y, n, t), _arg("out", out, n, t), _arg("h", h, n, t),
+        _arg("rstd_post", rstd_post, rows, f32), _arg("rstd_next", rstd_next, rows, f32), _stream_of(x, stream)))
+
+
+def moe_residual_norm_bwd(out, y, dh, dout, gamma_post, gamma_next, gate, row_gate, residual_scale: float,
+                          branch_scale: float, rstd_post, rstd_next, dx, dy, grads: dict, accumulate: bool, ws,
+                          stream=None) -> None:
+    """dx, dy and the parameters' gradients from what the forward wrote and kept.
+
+    ``grads`` holds those wanted of dgamma_post, dgamma_next, dgate [d] and drow_gate [rows], float32; ``dout`` and
+    ``dx`` may be None, ``out``, ``dh`` and ``rstd_next`` without gamma_next, ``y`` and ``dy`` without a branch.
+    """
+    given = next((t for t in (dh, dout) if t is not None), None)
+    if given is None:
+        raise ValueError("dh or dout is needed")
+    rows, d, p = _residual_norm(given, gamma_post, gamma_next, gate, row_gate, residual_scale, branch_scale, 0.0)
+    f32, t, n = _types[0], given.dtype, rows * d
+    unknown = set(grads) - {f for f, _ in MoeResidualNormGrads._fields_}
+    if unknown:
+        raise ValueError(f"unknown gradients {sorted(unknown)}")
+    g = MoeResidualNormGrads(*[_arg(f, grads.get(f), rows if f == "drow_gate" else d, f32)
+                               for f, _ in MoeResidualNormGrads._fields_])
+    _check("moe_residual_norm_bwd", lib().moe_residual_norm_bwd(
+        p, _arg("out", out, n, t), _arg("y", y, n, t), _arg("dh", dh, n, t), _arg("dout", dout, n, t),
+        _arg("rstd_post", rstd_post, rows, f32), _arg("rstd_next", rstd_next, rows, f32), _arg("dx", dx, n, t),
+        _arg("dy", dy, n, t), g, accumulate, _ptr(ws), ws.numel() * ws.element_size(), _stream_of(given, stream)))
+
+
+class GradList:
+    """Gradient tensors as ``moe_clip_grads`` takes them; holds on to the tensors."""
+
+    def __init__(self, src, dst):
+        codes = _torch_types()[2]
+        self.src, self.dst = list(src), None if dst is None else list(dst)
+        if self.dst is not None and len(self.dst) != len(self.src):
+            raise ValueError(f"{len(self.dst)} destinations for {len(self.src)} gradients")
+        self.entries = (MoeGrad * len(self.src))()
+        for i, t in enumerate(self.src):
+            if t.dtype not in codes:
+                raise TypeError(f"gradient {i} has type {t.dtype}, not bfloat16 or float32")
+            d = None if self.dst is None else self.dst[i]
+            self.entries[i] = MoeGrad(_arg(f"gradient {i}", t, t.numel(), t.dtype),
+                                      _arg(f"destination {i}", d, t.numel(), t.dtype), t.numel(), codes[t.dtype])
+
+
+def grad_list(src, dst=None) -> GradList:
+    """The gradients ``src`` (bfloat16 and float32 tensors), and where the clipped ones go: ``dst`` may be ``src``
+    itself, hold other tensors of the same sizes and types or None for some, or be None (the norm alone)."""
+    return GradList(src, dst)
+
+
+def moe_clip_grads(grads: GradList, max_norm: float, norm, ws, stream=None) -> None:
+    """norm [1] float32 = the 2-norm of all gradients together; each dst = src * min(1, max_norm / norm).
+
+    A norm that is not finite clips nothing.  Nothing is read back: the call can be captured.
+    """
+    _check("moe_clip_grads", lib().moe_clip_grads(
+        grads.entries, len(grads.entries), max_norm, _arg("norm", norm, 1, _torch_types()[0]), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream_of(norm, stream)))
+
+
+def _loss_shape(x, W):
+    T, d, code = _rows(x)
+    if W.dim() != 2 or W.shape[1] != d:
+        raise ValueError(f"W has shape {tuple(W.shape)}, not [V, {d}]")
+    return T, d, W.shape[0], code
+
+
+def moe_vocab_loss_fwd(x, W, labels, loss, lse, ws, total=None, stream=None) -> None:
+    """Cross entropy of x [..., d] over the vocabulary W [V, d]: ``loss`` and ``lse`` of each token, float32.
+
+    ``labels`` int32, negative ones ignored (loss and lse 0).  ``total`` [2]: the sum of the losses and the number of
+    labelled tokens.  The logits are never kept.
+    """
+    T, d, V, code = _loss_shape(x, W)
+    f32, i32, t = _types[0], _types[1], x.dtype
+    _check("moe_vocab_loss_fwd", lib().moe_vocab_loss_fwd(
+        T, d, V, code, _arg("x", x, T * d, t), _arg("W", W, V * d, t), _arg("labels", labels, T, i32),
+        _arg("loss", loss, T, f32), _arg("lse", lse, T, f32), _arg("total", total, 2, f32), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream_of(W, stream)))
+
+
+def moe_vocab_loss_bwd(x, W, labels, lse, dloss, dx, dW, accumulate: bool, ws, stream=None) -> None:
+    """dx (the type of x) and dW [V, d] (float32, or bfloat16 as x) of the loss, the logits formed again.
+
+    ``dloss`` [T] is the gradient of each token's loss; None: of the mean over the labelled tokens.  ``dx`` or ``dW``
+    may be None.
+    """
+    T, d, V, code = _loss_shape(x, W)
+    f32, i32, codes, _ = _types
+    t, tw = x.dtype, f32 if dW is None else dW.dtype
+    if tw not in codes:
+        raise TypeError(f"dW has type {tw}")
+    _check("moe_vocab_loss_bwd", lib().moe_vocab_loss_bwd(
+        T, d, V, code, codes[tw], _arg("x", x, T * d, t), _arg("W", W, V * d, t), _arg("labels", labels, T, i32),
+        _arg("lse", lse, T, f32), _arg("dloss", dloss, T, f32), _arg("dx", dx, T * d, t), _arg("dW", dW, V * d, tw),
+        accumulate, _ptr(ws), ws.numel() * ws.element_size(), _stream_of(W, stream)))
+
+
 def moe_get_device_error(clear: bool = True):
     """(code, detail) from the device error word; waits for the device."""
     c, d = ctypes.c_int32(), ctypes.c_int32()
@@ -496,3 +659,28 @@ def norm_workspace(rows: int, d: int, device="cuda"):
     import torch
 
     return torch.empty(moe_norm_workspace_size(rows, d), dtype=torch.uint8, device=device)
+
+
+def residual_norm_workspace(rows: int, d: int, device="cuda"):
+    """Workspace of ``moe_residual_norm_bwd``, kept from call to call."""
+    import torch
+
+    return torch.empty(moe_residual_norm_workspace_size(rows, d), dtype=torch.uint8, device=device)
+
+
+def clip_workspace(count: int, device="cuda"):
+    """Workspace of ``moe_clip_grads`` for ``count`` tensors, kept from call to call."""
+    import torch
+
+    return torch.empty(moe_clip_workspace_size(count), dtype=torch.uint8, device=device)
+
+
+def vocab_loss_workspace(T: int, d: int, V: int, dtype, training: bool, device="cuda"):
+    """Workspace of ``moe_vocab_loss_fwd``, and with ``training`` of ``moe_vocab_loss_bwd`` too, for x of torch type
+    ``dtype``; kept from call to call."""
+    import torch
+
+    code = _torch_types()[2].get(dtype)
+    if code is None:
+        raise TypeError(f"expected bfloat16 or float32, not {dtype}")
+    return torch.empty(moe_vocab_loss_workspace_size(T, d, V, code, training), dtype=torch.uint8, device=device)

@@ -1,0 +1,273 @@
+// The 2-norm of many gradient tensors together, and the gradients clipped to it.
+//
+//   norm = sqrt(sum_i sum g_i^2),  out_i = g_i * min(1, max_norm / norm)
+//
+// Two kernels over one list of chunks, which is passed by value with the
+// launch (no copy to the device, and a captured graph keeps its own).  The first sums
+// squares; the second adds the CTAs' sums, each CTA all of them in the same
+// order, and scales.  It walks the chunks backwards, so what the first kernel
+// read last comes from L2, and where nothing is clipped in place it ends at
+// once.  Both are bound by HBM.
+//
+// Chunks begin on 16 bytes of the source whatever the tensor's own alignment;
+// the first and last vector of a tensor are read element by element.
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+#include "step.h"
+
+namespace moe {
+namespace {
+
+constexpr int CLIP_NT = 256;
+constexpr int VECS = 8;                       // 16-byte vectors of a chunk that a thread holds
+constexpr int CHUNK_BYTES = CLIP_NT * VECS * 16;
+constexpr int FEW = 96, MANY = 768;           // tensors of a launch: parameters of 3 KB, or of 24 KB for long lists
+constexpr int NORM_CTAS = 4, SCALE_CTAS = 8;  // CTAs an SM
+
+template <int N>
+struct ClipList {
+  const void* src[N];
+  void* dst[N];
+  int64_t n[N];
+  int64_t first[N + 1];  // the tensor's first chunk
+  uint8_t bf16[N];
+  int count;
+};
+struct ClipScale {
+  const double* partial;
+  int parts;
+  float max_norm;
+  float* norm;  // or null: another launch writes it
+};
+
+// Chunks of a tensor of n elements of es bytes at p, counted from the 16-byte boundary at or before it.
+int64_t chunks_of(const void* p, int64_t n, int es) {
+  if (n == 0) return 0;
+  return ((int64_t)(reinterpret_cast<uintptr_t>(p) & 15) + n * es + CHUNK_BYTES - 1) / CHUNK_BYTES;
+}
+
+template <int N>
+__device__ __forceinline__ int tensor_of(const ClipList<N>& l, int64_t chunk) {
+  int lo = 0, hi = l.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.first[mid] <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A thread's part of a chunk: VECS vectors, CLIP_NT apart.  e0 is the element
+// index (in the tensor) of vector j's first element; it may be negative in the
+// first vector and reach past n in the last.
+template <typename T>
+struct Part {
+  const T* src;   // the tensor's first element
+  int64_t n, e0;  // of the thread's first vector
+  static constexpr int VN = Vec<T>::N;
+  __device__ __forceinline__ Part(const void* p, int64_t n_, int64_t chunk) : src(static_cast<const T*>(p)), n(n_) {
+    const int before = (int)(reinterpret_cast<uintptr_t>(p) & 15) / (int)sizeof(T);
+    e0 = chunk * (CHUNK_BYTES / (int)sizeof(T)) + threadIdx.x * VN - before;
+  }
+  __device__ __forceinline__ int64_t at(int j) const { return e0 + (int64_t)j * CLIP_NT * VN; }
+  __device__ __forceinline__ bool whole(int j) const { return at(j) >= 0 && at(j) + VN <= n; }
+  __device__ __forceinline__ void load(uint4 (&u)[VECS]) const {
+#pragma unroll
+    for (int j = 0; j < VECS; ++j) {
+      if (whole(j)) {
+        u[j] = *reinterpret_cast<const uint4*>(src + at(j));
+      } else {
+        T w[VN];
+#pragma unroll
+        for (int i = 0; i < VN; ++i) w[i] = at(j) + i >= 0 && at(j) + i < n ? src[at(j) + i] : from_f32<T>(0.f);
+        memcpy(&u[j], w, 16);
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ double cta_sum(double v, double* scratch) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) scratch[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int i = 0; i < CLIP_NT / 32; ++i) v += scratch[i];
+  return v;
+}
+
+// The sum of squares of a thread's vectors.  fp32 squares are exact enough
+// where the largest value is within 2^50 of 1 either way (nothing that counts
+// underflows, nothing overflows); beyond that they are summed in 64 bits, 32
+// times slower, which no trained model reaches.  A NaN is left out by the
+// maximum and makes either sum a NaN.
+template <typename T>
+__device__ __forceinline__ double squares(const uint4 (&u)[VECS]) {
+  constexpr int VN = Vec<T>::N;
+  float top = 0.f, s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < VECS; ++j) {
+    float v[VN];
+    unpack(u[j], v);
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      top = fmaxf(top, fabsf(v[i]));
+      s[i & 3] = fmaf(v[i], v[i], s[i & 3]);
+    }
+  }
+  if (top > 0x1p50f || (top < 0x1p-50f && top != 0.f)) {
+    double d = 0.0;
+#pragma unroll 1
+    for (int j = 0; j < VECS; ++j) {
+      float v[VN];
+      unpack(u[j], v);
+#pragma unroll
+      for (int i = 0; i < VN; ++i) d += (double)v[i] * (double)v[i];
+    }
+    return d;
+  }
+  return (double)((s[0] + s[1]) + (s[2] + s[3]));
+}
+
+template <int N>
+__global__ void __launch_bounds__(CLIP_NT) grad_norm_kernel(const __grid_constant__ ClipList<N> l, double* partial) {
+  pdl_enter();
+  __shared__ double scratch[CLIP_NT / 32];
+  const int64_t total = l.first[l.count];
+  double sum = 0.0;
+#pragma unroll 1
+  for (int64_t c = blockIdx.x; c < total; c += gridDim.x) {
+    const int t = tensor_of(l, c);
+    uint4 u[VECS];
+    if (l.bf16[t]) {
+      Part<__nv_bfloat16>(l.src[t], l.n[t], c - l.first[t]).load(u);
+      sum += squares<__nv_bfloat16>(u);
+    } else {
+      Part<float>(l.src[t], l.n[t], c - l.first[t]).load(u);
+      sum += squares<float>(u);
+    }
+  }
+  sum = cta_sum(sum, scratch);
+  if (threadIdx.x == 0) partial[blockIdx.x] = sum;
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_chunk(const void* src, void* dst_, int64_t n, int64_t chunk, float scale) {
+  constexpr int VN = Vec<T>::N;
+  const Part<T> p(src, n, chunk);
+  T* dst = static_cast<T*>(dst_);
+  const bool aligned = ((reinterpret_cast<uintptr_t>(src) ^ reinterpret_cast<uintptr_t>(dst_)) & 15) == 0;
+  uint4 u[VECS];
+  p.load(u);
+#pragma unroll
+  for (int j = 0; j < VECS; ++j) {
+    float v[VN];
+    unpack(u[j], v);
+#pragma unroll
+    for (int i = 0; i < VN; ++i) v[i] *= scale;
+    if (aligned && p.whole(j)) {
+      stg16(dst + p.at(j), pack(v));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VN; ++i)
+        if (p.at(j) + i >= 0 && p.at(j) + i < n) dst[p.at(j) + i] = from_f32<T>(v[i]);
+    }
+  }
+}
+
+template <int N>
+__global__ void __launch_bounds__(CLIP_NT) grad_clip_kernel(const __grid_constant__ ClipList<N> l, const ClipScale s) {
+  pdl_enter();
+  __shared__ double scratch[CLIP_NT / 32];
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < s.parts; i += CLIP_NT) sum += s.partial[i];
+  const double norm = sqrt(cta_sum(sum, scratch));
+  const float as_float = (float)norm;
+  if (s.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *s.norm = as_float;
+  const bool clips = isfinite(as_float) && as_float > s.max_norm;
+  const float scale = clips ? (float)((double)s.max_norm / norm) : 1.f;
+  const int64_t total = l.first[l.count];
+#pragma unroll 1
+  for (int64_t c = total - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
+    const int t = tensor_of(l, c);
+    if (l.dst[t] == nullptr || (!clips && l.dst[t] == l.src[t])) continue;
+    if (l.bf16[t]) scale_chunk<__nv_bfloat16>(l.src[t], l.dst[t], l.n[t], c - l.first[t], scale);
+    else scale_chunk<float>(l.src[t], l.dst[t], l.n[t], c - l.first[t], scale);
+  }
+}
+
+// The list of tensors [from, from + N) of the call; its chunks.
+template <int N>
+int64_t fill(ClipList<N>* l, const moe_grad* g, int count, int from) {
+  l->count = 0;
+  l->first[0] = 0;
+  for (int i = from; i < count && i < from + N; ++i) {
+    const int es = g[i].dtype == MOE_BF16 ? 2 : 4, k = l->count;
+    if (g[i].n == 0) continue;
+    l->src[k] = g[i].src;
+    l->dst[k] = g[i].dst;
+    l->n[k] = g[i].n;
+    l->bf16[k] = es == 2;
+    l->first[k + 1] = l->first[k] + chunks_of(g[i].src, g[i].n, es);
+    l->count = k + 1;
+  }
+  return l->first[l->count];
+}
+int norm_ctas(int64_t chunks) {
+  const int64_t most = (int64_t)sm_count() * NORM_CTAS;
+  return (int)(chunks < most ? chunks : most);
+}
+
+template <int N>
+cudaError_t clip_lists(const moe_grad* g, int count, float max_norm, float* norm, double* partial, cudaStream_t st) {
+  ClipList<N> l;
+  int parts = 0;
+  for (int from = 0; from < count; from += N) {
+    const int64_t chunks = fill(&l, g, count, from);
+    if (chunks == 0) continue;
+    LaunchScope ls(KK_GRAD_NORM, st);
+    const cudaError_t e = launch_pdl(grad_norm_kernel<N>, dim3(norm_ctas(chunks)), dim3(CLIP_NT), 0, st, l, partial + parts);
+    if (e != cudaSuccess) return e;
+    parts += norm_ctas(chunks);
+  }
+  bool writes = false;
+  for (int i = 0; i < count; ++i)
+    writes = writes || (g[i].n > 0 && g[i].dst != nullptr && (g[i].dst != g[i].src || !std::isinf(max_norm)));
+  ClipScale s{partial, parts, max_norm, norm};
+  const int last = writes ? (count - 1) / N * N : 0;
+  for (int from = last; from >= 0; from -= N) {  // backwards, as the chunks are
+    int64_t chunks = fill(&l, g, count, from);
+    if (!writes) {
+      l.count = 0;
+      chunks = 1;  // the norm alone
+    } else if (chunks == 0 && s.norm == nullptr) {
+      continue;
+    }
+    const int64_t most = (int64_t)sm_count() * SCALE_CTAS;
+    LaunchScope ls(KK_GRAD_CLIP, st);
+    const cudaError_t e = launch_pdl(grad_clip_kernel<N>, dim3((unsigned)(chunks < 1 ? 1 : chunks < most ? chunks : most)),
+                                     dim3(CLIP_NT), 0, st, l, s);
+    if (e != cudaSuccess) return e;
+    s.norm = nullptr;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t clip_ws_bytes(int count) {
+  const int per = count <= FEW ? FEW : MANY;
+  return (size_t)((count + per - 1) / per + 1) * sm_count() * NORM_CTAS * sizeof(double);
+}
+
+cudaError_t launch_clip(const moe_grad* grads, int count, float max_norm, float* norm, void* ws, cudaStream_t st) {
+  double* partial = static_cast<double*>(ws);
+  return count <= FEW ? clip_lists<FEW>(grads, count, max_norm, norm, partial, st)
+                      : clip_lists<MANY>(grads, count, max_norm, norm, partial, st);
+}
+
+}  // namespace moe

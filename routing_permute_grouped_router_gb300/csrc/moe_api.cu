@@ -11,7 +11,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/moe.h"
-#include "block.h"
+#include "step.h"
 
 namespace moe {
 
@@ -88,12 +88,13 @@ cudaEvent_t pool_event() {
   return e;
 }
 
-const char* const kKernelNames[KK_ALL] = {
+const char* const kKernelNames[KK_END] = {
     "router_topk",  "slot_scan",  "slot_assign",     "permute",      "gemm_up_swiglu", "gemm_down",
     "unpermute_combine", "combine_bwd", "gemm_dgrad_h_swiglu_bwd", "gemm_wgrad", "gemm_dgrad_x",
     "transpose_wr", "dx_router",  "dwr",     "dwr_reduce",   "zero", "split_wr", "selftest_bounded_wait",
     "split_dl", "aux_loss", "aux_grad", "router_logit_grad", "layer_decode", "norm_fwd", "norm_bwd", "norm_bwd_reduce",
-    "dropout_add", "dropout_bwd"};
+    "dropout_add", "dropout_bwd", "residual_norm_fwd", "residual_norm_bwd", "residual_norm_reduce", "grad_norm",
+    "grad_clip", "loss_rows", "loss_logits", "loss_combine", "loss_dlogits", "loss_grads", "loss_finish"};
 
 }  // namespace
 
@@ -774,22 +775,22 @@ moe_status moe_nvtx_enable(int on) {
   return MOE_OK;
 }
 
-int32_t moe_kernel_kinds(void) { return KK_ALL; }
+int32_t moe_kernel_kinds(void) { return KK_END; }
 
 moe_status moe_profiler_filter(int32_t id) {
-  if (id >= KK_ALL) return MOE_ERR_INVALID_ARG;
+  if (id >= KK_END) return MOE_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lk(g_prof_mu);
   g_prof_filter = id < 0 ? -1 : id;
   return MOE_OK;
 }
 
 const char* moe_kernel_name(int32_t id) {
-  if (id < 0 || id >= KK_ALL) return nullptr;
+  if (id < 0 || id >= KK_END) return nullptr;
   return kKernelNames[id];
 }
 
 moe_status moe_profiler_read(int32_t id, int64_t* launches, double* total_ms) {
-  if (id < 0 || id >= KK_ALL) return MOE_ERR_INVALID_ARG;
+  if (id < 0 || id >= KK_END) return MOE_ERR_INVALID_ARG;
   std::lock_guard<std::mutex> lk(g_prof_mu);
   int64_t n = 0;
   double ms = 0.0;
