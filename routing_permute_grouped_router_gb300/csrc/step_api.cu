@@ -81,6 +81,7 @@ moe_status check_overlap(const moe_grad* g, int32_t count) {
 moe_status loss_shape(int32_t T, int32_t d, int32_t V, int32_t dtype) {
   if (!known(dtype)) return MOE_ERR_DTYPE;
   if (T < 0 || T > (1 << 24) || V < 1 || V > (1 << 24) || d < 1 || d > (1 << 16)) return MOE_ERR_SHAPE;
+  if ((int64_t)T * V > (int64_t)1 << 44) return MOE_ERR_SHAPE;
   return d % (dtype == MOE_BF16 ? 8 : 4) == 0 ? MOE_OK : MOE_ERR_SHAPE;
 }
 

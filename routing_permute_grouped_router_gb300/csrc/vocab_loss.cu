@@ -1,297 +1,296 @@
 // Softmax cross entropy over a large vocabulary and its gradient, the logits
 // formed a piece at a time and never kept; formulas are in moe.h.
 //
-// The labelled tokens are listed first (ignored ones cost nothing further).
+// The labelled tokens are listed first and their rows of x packed, padded with
+// zero rows to whole tiles: ignored tokens cost nothing further, and what their
+// rows hold reaches no product.  float32 rows are split into bf16 parts on the
+// way.  The products run on the tensor cores (vocab_loss_tc.cu); the forward's
+// leaves two floats a row and 128 words, which loss_combine_kernel joins.  The
+// backward goes over the vocabulary in equal pieces: dz of a piece, then its
+// part of dx (added up in fp32) and its rows of dW.
 #include "common.cuh"
-#include "step.h"
+#include "vocab_loss.h"
 
 namespace moe {
 namespace {
 
-constexpr int LIST_NT = 1024;
-constexpr int TM = 64, TN = 64, TK = 16, GEMM_NT = 256;  // a tile: 4 x 4 of it a thread
-constexpr int64_t PIECE_VALUES = (int64_t)1 << 26;        // values of dz held at a time
+constexpr int LIST_NT = 1024, LIST_EACH = 8;        // labels a thread takes at a time
+constexpr int ROW_NT = 256;
+constexpr int64_t PIECE_VALUES = (int64_t)1 << 28;  // of a part of dz: 512 MB at most, or a tile's columns
 
-struct LossK {
-  const void *x, *W;
-  const int32_t* labels;
-  float *loss, *lse, *total;
-  const float* dloss;
-  void *dx, *dW;
-  int T, d, V, accumulate, dw_bf16;
-  // workspace
-  int32_t* list;    // [T]: the labelled tokens
-  int32_t* count;   // their number
-  float2* partial;  // [T][tiles]: the largest logit of each tile and the sum of exp of the distances to it
-  float* picked;    // [T]: the label's logit
-  float* dz;        // [T][piece]
-  float* acc;       // [T][d]: dx before its rounding
-  int v0, piece, tiles;
-  uint32_t* err;
-};
-
-// The labelled tokens in order, and their number.
-__global__ void __launch_bounds__(LIST_NT) loss_rows_kernel(const LossK a) {
+// The labelled tokens in order, each token's place among them, their number.
+__global__ void __launch_bounds__(LIST_NT) loss_rows_kernel(const LossWork w, const int32_t* labels) {
   pdl_enter();
   __shared__ int before[32];
-  __shared__ int base;
-  if (threadIdx.x == 0) base = 0;
-  __syncthreads();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  for (int t0 = 0; t0 < a.T; t0 += LIST_NT) {
-    const int t = t0 + threadIdx.x;
-    const int label = t < a.T ? a.labels[t] : -1;
-    if (label >= a.V) report_error(a.err, DEV_BAD_LABEL, (uint32_t)t & 0xFFFFFFu);
-    const bool valid = label >= 0 && label < a.V;
-    const uint32_t votes = __ballot_sync(0xffffffffu, valid);
-    if (lane == 0) before[warp] = __popc(votes);
-    __syncthreads();
-    int at = base, all = 0;
-    for (int w = 0; w < LIST_NT / 32; ++w) {
-      at += w < warp ? before[w] : 0;
-      all += before[w];
-    }
-    if (valid) a.list[at + __popc(votes & ((1u << lane) - 1u))] = t;
-    __syncthreads();
-    if (threadIdx.x == 0) base += all;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) *a.count = base;
-}
-
-// c[4][4] of a 64 x 64 tile of A B, A(m, k) and B(n, k) read through fa and fb (0 outside)
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(int K, FA fa, FB fb, float (&c)[4][4]) {
-  __shared__ float sa[TK][TM + 4], sb[TK][TN + 4];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  int base = 0;
+  for (int t0 = 0; t0 < w.T; t0 += LIST_NT * LIST_EACH) {
+    const int first = t0 + threadIdx.x * LIST_EACH;
+    int label[LIST_EACH], mine = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < LIST_EACH; ++i) label[i] = first + i < w.T ? labels[first + i] : -1;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[i][j] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += TK) {
-    __syncthreads();
-#pragma unroll
-    for (int e = threadIdx.x; e < TM * TK; e += GEMM_NT) {
-      sa[e % TK][e / TK] = k0 + e % TK < K ? fa(e / TK, k0 + e % TK) : 0.f;
-      sb[e % TK][e / TK] = k0 + e % TK < K ? fb(e / TK, k0 + e % TK) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < TK; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], c[i][j]);
-  }
-}
-
-// The logits of a tile: their maximum and sum (GRAD: dz instead).
-template <typename T, bool GRAD>
-__global__ void __launch_bounds__(GEMM_NT) loss_logits_kernel(const LossK a) {
-  pdl_enter();
-  const int n = *a.count, r0 = blockIdx.y * TM, c0 = blockIdx.x * TN;  // of the labelled tokens, of the piece
-  if (r0 >= n) return;
-  const T *x = static_cast<const T*>(a.x), *W = static_cast<const T*>(a.W);
-  float c[4][4];
-  tile_product(
-      a.d,
-      [&](int m, int k) { return r0 + m < n ? to_f32(x[(int64_t)a.list[r0 + m] * a.d + k]) : 0.f; },
-      [&](int v, int k) { return c0 + v < a.piece && a.v0 + c0 + v < a.V ? to_f32(W[(int64_t)(a.v0 + c0 + v) * a.d + k]) : 0.f; }, c);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + ty * 4 + i;
-    const int t = r < n ? a.list[r] : 0, label = r < n ? a.labels[t] : -1;
-    if (GRAD) {
-      const float g = r < n ? (a.dloss ? a.dloss[t] : 1.f / (float)n) : 0.f, lse = r < n ? a.lse[t] : 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int v = c0 + tx * 4 + j;
-        if (r < n && v < a.piece)
-          a.dz[(int64_t)r * a.piece + v] =
-              a.v0 + v < a.V ? g * (expf(c[i][j] - lse) - (a.v0 + v == label ? 1.f : 0.f)) : 0.f;
+    for (int i = 0; i < LIST_EACH; ++i) {
+      if (label[i] >= w.V) {
+        report_error(w.err, DEV_BAD_LABEL, (uint32_t)(first + i) & 0xFFFFFFu);
+        label[i] = -1;
       }
-    } else {
-      float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int v = c0 + tx * 4 + j;
-        if (v >= a.V) continue;
-        top = fmaxf(top, c[i][j]);
-        if (v == label) a.picked[r] = c[i][j];
-      }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float from = top == -INFINITY ? 0.f : top;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (c0 + tx * 4 + j < a.V) sum += expf(c[i][j] - from);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (tx == 0 && r < n) a.partial[(int64_t)r * a.tiles + blockIdx.x] = make_float2(top, sum);
+      mine += label[i] >= 0;
     }
+    int upto = mine;  // in this warp
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      upto += lane >= o ? v : 0;
+    }
+    __syncthreads();
+    if (lane == 31) before[warp] = upto;
+    __syncthreads();
+    int at = base + upto - mine, all = 0;
+    for (int i = 0; i < LIST_NT / 32; ++i) {
+      at += i < warp ? before[i] : 0;
+      all += before[i];
+    }
+#pragma unroll
+    for (int i = 0; i < LIST_EACH; ++i) {
+      if (first + i >= w.T) continue;
+      w.pos[first + i] = label[i] >= 0 ? at : -1;
+      if (label[i] >= 0) w.list[at++] = first + i;
+    }
+    base += all;
+  }
+  if (threadIdx.x == 0) *w.count = base;
+}
+
+// Three bf16 parts of 8 bits each whose sum is v; an infinity is its first part alone.
+__device__ __forceinline__ void split3(float v, __nv_bfloat16 (&p)[MAX_PARTS]) {
+  float rest = v;
+#pragma unroll
+  for (int i = 0; i < MAX_PARTS; ++i) {
+    const float top = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+    p[i] = __float2bfloat16_rn(isnan(v) ? v : top);
+    rest = isfinite(v) ? rest - top : 0.f;
   }
 }
 
-// A warp for each labelled token: its tiles' sums, its loss.
-__global__ void __launch_bounds__(256) loss_combine_kernel(const LossK a) {
+// Four elements of a float32 row as parts at dst, dst + ld, dst + 2 ld.
+__device__ __forceinline__ void put_parts(__nv_bfloat16* dst, int ld, const float (&v)[4]) {
+  __nv_bfloat16 p[4][MAX_PARTS];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split3(v[i], p[i]);
+#pragma unroll
+  for (int j = 0; j < MAX_PARTS; ++j) {
+    __nv_bfloat162 q[2] = {__nv_bfloat162(p[0][j], p[1][j]), __nv_bfloat162(p[2][j], p[3][j])};
+    *reinterpret_cast<uint2*>(dst + (size_t)j * ld) = *reinterpret_cast<uint2*>(q);
+  }
+}
+
+struct PackArgs {
+  const void* x;
+  const int32_t* labels;
+  const float* lse;    // backward
+  const float* dloss;  // backward, or null
+  float* loss;         // forward: 0 for the ignored tokens
+  float* lse_out;
+};
+// A CTA a row at a time: the labelled rows of x, zeros up to a whole tile; what
+// the epilogues want of each row; in the forward 0 for the ignored tokens.
+template <typename T>
+__global__ void __launch_bounds__(ROW_NT) loss_pack_kernel(const LossWork w, const PackArgs a) {
   pdl_enter();
-  const int n = *a.count, lane = threadIdx.x % 32;
-  for (int r = (blockIdx.x * 256 + threadIdx.x) / 32; r < n; r += gridDim.x * 8) {
-    const float2* p = a.partial + (int64_t)r * a.tiles;
+  const int n = *w.count, rows = (n + LOSS_TILE - 1) / LOSS_TILE * LOSS_TILE;
+  constexpr int VN = Vec<T>::N;
+  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+    const int t = r < n ? w.list[r] : 0;
+    const T* src = static_cast<const T*>(a.x) + (int64_t)t * w.d;
+    __nv_bfloat16* dst = w.xp + (int64_t)r * w.parts * w.ldx;
+    for (int i = threadIdx.x * VN; i < w.ldx; i += ROW_NT * VN) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (r < n && i < w.d) u = ldg16(src + i);
+      if constexpr (VN == 8) {
+        stg16(dst + i, u);
+      } else {
+        float v[4];
+        unpack(u, v);
+        put_parts(dst + i, w.ldx, v);
+      }
+    }
+    if (threadIdx.x == 0) {
+      w.label[r] = r < n ? a.labels[t] : -1;
+      if (a.lse != nullptr) {
+        w.lse[r] = r < n ? a.lse[t] : 0.f;
+        w.grad[r] = r < n ? (a.dloss ? a.dloss[t] : 1.f) : 0.f;
+      }
+    }
+  }
+  if (a.loss != nullptr)
+    for (int t = blockIdx.x * ROW_NT + threadIdx.x; t < w.T; t += gridDim.x * ROW_NT)
+      if (w.pos[t] < 0) a.loss[t] = a.lse_out[t] = 0.f;
+}
+
+// The parts of a float32 W, zeros up to ldw.  Infinities count as the largest
+// bf16: as one part they would meet the zeros of the other operand's parts.
+__global__ void __launch_bounds__(ROW_NT) loss_split_kernel(const LossWork w, const float* W, __nv_bfloat16* out) {
+  pdl_enter();
+  const int64_t vecs = w.ldw / 4, all = vecs * w.V;
+  for (int64_t i = (int64_t)blockIdx.x * ROW_NT + threadIdx.x; i < all; i += (int64_t)gridDim.x * ROW_NT) {
+    const int64_t row = i / vecs;
+    const int c = (int)(i - row * vecs) * 4;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (c < w.d) u = ldg16(W + row * w.d + c);
+    float v[4];
+    unpack(u, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (isinf(v[j])) v[j] = copysignf(0x1.fep127f, v[j]);
+    put_parts(out + row * MAX_PARTS * w.ldw + c, w.ldw, v);
+  }
+}
+
+// 32 labelled tokens a CTA, their partial sums in 32 strips: lse, the loss.
+__global__ void __launch_bounds__(1024) loss_combine_kernel(const LossWork w, int parts, float* loss, float* lse) {
+  pdl_enter();
+  __shared__ float tops[32][33], sums[32][33];
+  const int n = *w.count, lane = threadIdx.x % 32, strip = threadIdx.x / 32;
+  for (int r0 = blockIdx.x * 32; r0 < n; r0 += gridDim.x * 32) {
+    const int r = r0 + lane;  // Tp is a multiple of 32: the row is there
     float top = -INFINITY, sum = 0.f;
-    for (int i = lane; i < a.tiles; i += 32) top = fmaxf(top, p[i].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    for (int i = lane; i < a.tiles; i += 32) sum += p[i].x == -INFINITY ? p[i].y : p[i].y * expf(p[i].x - top);
-    sum = warp_sum(sum);
-    if (lane == 0) {
-      const int t = a.list[r];
-      const float lse = top + logf(sum);
-      a.lse[t] = lse;
-      a.loss[t] = lse - a.picked[r];
+#pragma unroll 4
+    for (int i = strip; i < parts; i += 32) {
+      const float2 p = w.partial[(int64_t)i * w.Tp + r];
+      const float best = fmaxf(top, p.x), at = best == -INFINITY ? 0.f : best;
+      sum = sum * expf(top - at) + p.y * expf(p.x - at);
+      top = best;
     }
+    tops[strip][lane] = top;
+    sums[strip][lane] = sum;
+    __syncthreads();
+    // a warp joins one token's strips
+    top = tops[lane][strip];
+    float best = top;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    const float at = best == -INFINITY ? 0.f : best;
+    sum = warp_sum(sums[lane][strip] * expf(top - at));
+    if (lane == 0 && r0 + strip < n) {
+      const int t = w.list[r0 + strip];
+      const float v = best + logf(sum);
+      lse[t] = v;
+      // lse and the logit share the maximum: their difference is formed without it
+      loss[t] = (best - w.picked[r0 + strip]) + logf(sum);
+    }
+    __syncthreads();
   }
 }
 
-// 0 for the ignored tokens; the sum of the losses and the number of the labelled ones.
-__global__ void __launch_bounds__(LIST_NT) loss_total_kernel(const LossK a) {
+// The sum of the losses, in token order within each thread, and the number of labelled tokens.
+__global__ void __launch_bounds__(LIST_NT) loss_total_kernel(const LossWork w, const float* loss, float* total) {
   pdl_enter();
   __shared__ double scratch[32];
   double s = 0.0;
-  for (int t = threadIdx.x; t < a.T; t += LIST_NT) {
-    const int label = a.labels[t];
-    if (label < 0 || label >= a.V) a.loss[t] = a.lse[t] = 0.f;
-    else s += a.loss[t];
-  }
+#pragma unroll 8
+  for (int t = threadIdx.x; t < w.T; t += LIST_NT) s += loss[t];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (threadIdx.x % 32 == 0) scratch[threadIdx.x / 32] = s;
   __syncthreads();
-  if (threadIdx.x == 0 && a.total) {
+  if (threadIdx.x == 0) {
     s = 0.0;
     for (int i = 0; i < LIST_NT / 32; ++i) s += scratch[i];
-    a.total[0] = (float)s;
-    a.total[1] = (float)*a.count;
+    total[0] = (float)s;
+    total[1] = (float)*w.count;
   }
 }
 
-// acc (+)= dz W over the piece
+// dx of the labelled tokens from acc, 0 for the others.  A bf16 dx comes from dz
+// in one part of 8 bits.  One term, the label's, is as large as all the others
+// together, so its rounding would be dx's: what the part left of it is added
+// here (8192 x 2048 x 50257: dx off by 0.17 % with it, its own rounding; 0.36 %
+// without).
 template <typename T>
-__global__ void __launch_bounds__(GEMM_NT) loss_dx_kernel(const LossK a) {
+__global__ void __launch_bounds__(ROW_NT) loss_dx_kernel(const LossWork w, const T* W, T* dx) {
   pdl_enter();
-  const int n = *a.count, r0 = blockIdx.y * TM, c0 = blockIdx.x * TN;
-  if (r0 >= n) return;
-  const T* W = static_cast<const T*>(a.W);
-  float c[4][4];
-  const int K = a.V - a.v0 < a.piece ? a.V - a.v0 : a.piece;
-  tile_product(
-      K, [&](int m, int k) { return r0 + m < n ? a.dz[(int64_t)(r0 + m) * a.piece + k] : 0.f; },
-      [&](int i, int k) { return c0 + i < a.d ? to_f32(W[(int64_t)(a.v0 + k) * a.d + c0 + i]) : 0.f; }, c);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + ty * 4 + i, col = c0 + tx * 4 + j;
-      if (r >= n || col >= a.d) continue;
-      float* p = a.acc + (int64_t)r * a.d + col;
-      *p = a.v0 == 0 ? c[i][j] : *p + c[i][j];
+  constexpr int VN = Vec<T>::N;
+  const float scale = w.mean ? 1.f / (float)*w.count : 1.f;
+  for (int t = blockIdx.x; t < w.T; t += gridDim.x) {
+    const int r = w.pos[t];
+    if (r < 0) {
+      for (int i = threadIdx.x * VN; i < w.d; i += ROW_NT * VN) stg16(dx + (int64_t)t * w.d + i, make_uint4(0, 0, 0, 0));
+      continue;
     }
-}
-// dW (+)= dz^T x of the piece's rows
-template <typename T, typename TW>
-__global__ void __launch_bounds__(GEMM_NT) loss_dw_kernel(const LossK a) {
-  pdl_enter();
-  const int n = *a.count, r0 = blockIdx.y * TM, c0 = blockIdx.x * TN;
-  const T* x = static_cast<const T*>(a.x);
-  float c[4][4];
-  tile_product(
-      n, [&](int m, int k) { return r0 + m < a.piece ? a.dz[(int64_t)k * a.piece + r0 + m] : 0.f; },
-      [&](int i, int k) { return c0 + i < a.d ? to_f32(x[(int64_t)a.list[k] * a.d + c0 + i]) : 0.f; }, c);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    const float* src = w.acc + (int64_t)r * w.d;
+    const T* word = W + (int64_t)w.label[r] * w.d;
+    const float off = sizeof(T) == 2 ? w.off[r] : 0.f;
+    for (int i = threadIdx.x * VN; i < w.d; i += ROW_NT * VN) {
+      float v[VN];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+      for (int j = 0; j < VN; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src + i + j);
+        v[j] = f.x;
+        v[j + 1] = f.y;
+        v[j + 2] = f.z;
+        v[j + 3] = f.w;
+      }
+      if constexpr (sizeof(T) == 2) {
+        float u[VN];
+        unpack(ldg16(word + i), u);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + ty * 4 + i, col = c0 + tx * 4 + j;
-      if (r >= a.piece || a.v0 + r >= a.V || col >= a.d) continue;
-      TW* p = static_cast<TW*>(a.dW) + (int64_t)(a.v0 + r) * a.d + col;
-      *p = from_f32<TW>(a.accumulate ? to_f32(*p) + c[i][j] : c[i][j]);
+        for (int j = 0; j < VN; ++j) v[j] = fmaf(off, u[j], v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < VN; ++j) v[j] *= scale;
+      stg16(dx + (int64_t)t * w.d + i, pack(v));
     }
-}
-// dx of the labelled tokens from acc, 0 for the others
-template <typename T>
-__global__ void __launch_bounds__(256) loss_dx_zero_kernel(const LossK a) {
-  pdl_enter();
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const int label = a.labels[t];
-    if (label >= 0 && label < a.V) continue;
-    for (int i = threadIdx.x; i < a.d; i += 256) static_cast<T*>(a.dx)[(int64_t)t * a.d + i] = from_f32<T>(0.f);
   }
-}
-template <typename T>
-__global__ void __launch_bounds__(256) loss_dx_store_kernel(const LossK a) {
-  pdl_enter();
-  const int n = *a.count;
-  for (int r = blockIdx.x; r < n; r += gridDim.x)
-    for (int i = threadIdx.x; i < a.d; i += 256)
-      static_cast<T*>(a.dx)[(int64_t)a.list[r] * a.d + i] = from_f32<T>(a.acc[(int64_t)r * a.d + i]);
 }
 
-size_t up(size_t n) { return (n + 255) / 256 * 256; }
-int piece_of(int T, int V) {
-  int64_t p = PIECE_VALUES / (T > 0 ? T : 1) / TN * TN;
-  const int64_t all = ((int64_t)V + TN - 1) / TN * TN;
-  if (p < TN) p = TN;
-  return (int)(p < all ? p : all);
+// ------------------------------ host side ---------------------------------- //
+size_t up(size_t n, size_t a = 256) { return (n + a - 1) / a * a; }
+
+// Equal pieces of the vocabulary, whole tiles each.
+int piece_of(int64_t Tp, int64_t V) {
+  const int64_t all = up(V, LOSS_TILE), most = PIECE_VALUES / Tp / LOSS_TILE * LOSS_TILE;
+  if (most >= all) return (int)all;
+  const int64_t pieces = (V + (most < LOSS_TILE ? LOSS_TILE : most) - 1) / (most < LOSS_TILE ? LOSS_TILE : most);
+  return (int)up((V + pieces - 1) / pieces, LOSS_TILE);
 }
-struct Layout {
-  size_t list, count, picked, partial, dz, acc, end;
-};
-Layout layout(int T, int d, int V, bool training) {
-  Layout l{};
-  const size_t t = T;
-  l.list = 0;
-  l.count = l.list + up(t * 4);
-  l.picked = l.count + 256;
-  l.partial = l.picked + up(t * 4);
-  l.end = l.partial + up(t * ((V + TN - 1) / TN) * 8);
-  if (training) {  // the backward's share the place of the forward's
-    l.dz = l.picked;
-    l.acc = l.dz + up(t * piece_of(T, V) * 4);
-    const size_t e = l.acc + up(t * d * 4);
-    l.end = l.end > e ? l.end : e;
+
+// What a call keeps in the workspace, from `base` on (null: its size alone); returns its end.
+size_t lay_out(LossWork* w, char* base, int T, int d, int V, bool bf16, bool backward, int dzp) {
+  size_t end = 0;
+  auto take = [&](size_t bytes) {
+    char* p = base + end;
+    end += up(bytes);
+    return base == nullptr ? nullptr : p;
+  };
+  w->T = T;
+  w->Tp = (int)up(T, LOSS_TILE);
+  w->d = d;
+  w->V = V;
+  w->parts = bf16 ? 1 : MAX_PARTS;
+  w->ldx = w->ldw = bf16 ? d : (int)up(d, 128);
+  w->dzp = dzp;
+  w->piece = piece_of(w->Tp, V);
+  const size_t Tp = w->Tp, parts = w->parts;
+  w->list = reinterpret_cast<int32_t*>(take((size_t)T * 4));
+  w->pos = reinterpret_cast<int32_t*>(take((size_t)T * 4));
+  w->count = reinterpret_cast<int32_t*>(take(4));
+  w->label = reinterpret_cast<int32_t*>(take(Tp * 4));
+  w->xp = reinterpret_cast<__nv_bfloat16*>(take(Tp * parts * w->ldx * 2));
+  if (!bf16) w->wp = reinterpret_cast<__nv_bfloat16*>(take((size_t)V * parts * w->ldw * 2));
+  if (!backward) {
+    w->picked = reinterpret_cast<float*>(take(Tp * 4));
+    w->partial = reinterpret_cast<float2*>(take(up(V, LOSS_TILE) / LOSS_PART * Tp * 8));
+  } else {
+    w->lse = reinterpret_cast<float*>(take(Tp * 4));
+    w->grad = reinterpret_cast<float*>(take(Tp * 4));
+    w->off = reinterpret_cast<float*>(take(Tp * 4));
+    w->dz = reinterpret_cast<__nv_bfloat16*>(take((size_t)dzp * Tp * w->piece * 2));
+    w->acc = reinterpret_cast<float*>(take(Tp * d * 4));
   }
-  return l;
+  return end;
 }
-LossK kernel_args(const LossArgs& a, bool training, uint32_t* err) {
-  const Layout l = layout(a.T, a.d, a.V, training);
-  char* ws = static_cast<char*>(a.ws);
-  LossK k{};
-  k.x = a.x;
-  k.W = a.W;
-  k.labels = a.labels;
-  k.loss = a.loss;
-  k.lse = a.lse;
-  k.total = a.total;
-  k.dloss = a.dloss;
-  k.dx = a.dx;
-  k.dW = a.dW;
-  k.T = a.T;
-  k.d = a.d;
-  k.V = a.V;
-  k.accumulate = a.accumulate;
-  k.list = reinterpret_cast<int32_t*>(ws + l.list);
-  k.count = reinterpret_cast<int32_t*>(ws + l.count);
-  k.picked = reinterpret_cast<float*>(ws + l.picked);
-  k.partial = reinterpret_cast<float2*>(ws + l.partial);
-  k.dz = reinterpret_cast<float*>(ws + l.dz);
-  k.acc = reinterpret_cast<float*>(ws + l.acc);
-  k.tiles = (a.V + TN - 1) / TN;
-  k.err = err;
-  return k;
-}
+
 #define LAUNCH(kind, ...)                            \
   do {                                               \
     LaunchScope ls(kind, st);                        \
@@ -299,47 +298,71 @@ LossK kernel_args(const LossArgs& a, bool training, uint32_t* err) {
     if (e != cudaSuccess) return e;                  \
   } while (0)
 
-template <typename T>
-cudaError_t fwd_t(const LossArgs& args, uint32_t* err, cudaStream_t st) {
-  LossK a = kernel_args(args, false, err);
-  a.piece = a.tiles * TN;
-  LAUNCH(KK_LOSS_ROWS, loss_rows_kernel, dim3(1), dim3(LIST_NT), 0, st, a);
-  LAUNCH(KK_LOSS_LOGITS, loss_logits_kernel<T, false>, dim3(a.tiles, (a.T + TM - 1) / TM), dim3(GEMM_NT), 0, st, a);
-  LAUNCH(KK_LOSS_COMBINE, loss_combine_kernel, dim3((a.T + 7) / 8), dim3(256), 0, st, a);
-  LAUNCH(KK_LOSS_FINISH, loss_total_kernel, dim3(1), dim3(LIST_NT), 0, st, a);
-  return cudaSuccess;
+unsigned few(int64_t n, int per_sm) {
+  const int64_t most = (int64_t)sm_count() * per_sm;
+  return (unsigned)(n < most ? n : most);
 }
-template <typename T>
-cudaError_t bwd_t(const LossArgs& args, uint32_t* err, cudaStream_t st) {
-  LossK a = kernel_args(args, true, err);
-  a.piece = piece_of(a.T, a.V);
-  const int rows = (a.T + TM - 1) / TM, cols = (a.d + TN - 1) / TN;
-  LAUNCH(KK_LOSS_ROWS, loss_rows_kernel, dim3(1), dim3(LIST_NT), 0, st, a);
-  for (a.v0 = 0; a.v0 < a.V; a.v0 += a.piece) {
-    LAUNCH(KK_LOSS_DLOGITS, loss_logits_kernel<T, true>, dim3(a.piece / TN, rows), dim3(GEMM_NT), 0, st, a);
-    if (a.dx) LAUNCH(KK_LOSS_GRADS, loss_dx_kernel<T>, dim3(cols, rows), dim3(GEMM_NT), 0, st, a);
-    const dim3 grid(cols, a.piece / TM);
-    if (a.dW && args.dw_bf16) LAUNCH(KK_LOSS_GRADS, loss_dw_kernel<T, __nv_bfloat16>, grid, dim3(GEMM_NT), 0, st, a);
-    else if (a.dW) LAUNCH(KK_LOSS_GRADS, loss_dw_kernel<T, float>, grid, dim3(GEMM_NT), 0, st, a);
+
+// The labelled tokens' rows and W as the products read them.
+cudaError_t prepare(LossWork* w, const LossArgs& a, const PackArgs& p, cudaStream_t st) {
+  LAUNCH(KK_LOSS_ROWS, loss_rows_kernel, dim3(1), dim3(LIST_NT), 0, st, *w, a.labels);
+  LAUNCH(KK_LOSS_ROWS, a.bf16 ? loss_pack_kernel<__nv_bfloat16> : loss_pack_kernel<float>, dim3(few(w->Tp, 8)),
+         dim3(ROW_NT), 0, st, *w, p);
+  if (a.bf16) {
+    w->wp = static_cast<const __nv_bfloat16*>(a.W);
+    return cudaSuccess;
   }
-  if (!a.dx) return cudaSuccess;
-  const unsigned ctas = a.T < 65536 ? a.T : 65536;
-  LAUNCH(KK_LOSS_FINISH, loss_dx_zero_kernel<T>, dim3(ctas), dim3(256), 0, st, a);
-  LAUNCH(KK_LOSS_FINISH, loss_dx_store_kernel<T>, dim3(ctas), dim3(256), 0, st, a);
+  LAUNCH(KK_LOSS_ROWS, loss_split_kernel, dim3(few((int64_t)w->V * (w->ldw / 4) / ROW_NT + 1, 16)), dim3(ROW_NT), 0, st,
+         *w, static_cast<const float*>(a.W), const_cast<__nv_bfloat16*>(w->wp));
   return cudaSuccess;
 }
 
 }  // namespace
 
 size_t loss_ws_bytes(int T, int d, int V, bool bf16, bool training) {
-  (void)bf16;
-  return layout(T, d, V, training).end;
+  if (T == 0) return 0;
+  LossWork w{};
+  const size_t fwd = lay_out(&w, nullptr, T, d, V, bf16, false, 0);
+  if (!training) return fwd;
+  const size_t bwd = lay_out(&w, nullptr, T, d, V, bf16, true, bf16 ? 2 : MAX_PARTS);
+  return fwd > bwd ? fwd : bwd;
 }
+
 cudaError_t launch_loss_fwd(const LossArgs& a, uint32_t* err, cudaStream_t st) {
-  return a.bf16 ? fwd_t<__nv_bfloat16>(a, err, st) : fwd_t<float>(a, err, st);
+  LossWork w{};
+  w.err = err;
+  lay_out(&w, static_cast<char*>(a.ws), a.T, a.d, a.V, a.bf16, false, 0);
+  cudaError_t e = prepare(&w, a, PackArgs{a.x, a.labels, nullptr, nullptr, a.loss, a.lse}, st);
+  if (e != cudaSuccess) return e;
+  e = tc_loss_logits(w, st);
+  if (e != cudaSuccess) return e;
+  LAUNCH(KK_LOSS_COMBINE, loss_combine_kernel, dim3(few((a.T + 31) / 32, 2)), dim3(1024), 0, st, w,
+         (a.V + LOSS_PART - 1) / LOSS_PART, a.loss, a.lse);
+  if (a.total) LAUNCH(KK_LOSS_FINISH, loss_total_kernel, dim3(1), dim3(LIST_NT), 0, st, w, (const float*)a.loss, a.total);
+  return cudaSuccess;
 }
+
 cudaError_t launch_loss_bwd(const LossArgs& a, uint32_t* err, cudaStream_t st) {
-  return a.bf16 ? bwd_t<__nv_bfloat16>(a, err, st) : bwd_t<float>(a, err, st);
+  LossWork w{};
+  w.err = err;
+  // as many bits of dz as the results can use
+  const int dzp = !a.bf16 ? MAX_PARTS : a.dW != nullptr && !a.dw_bf16 ? 2 : 1;
+  lay_out(&w, static_cast<char*>(a.ws), a.T, a.d, a.V, a.bf16, true, dzp);
+  w.mean = a.dloss == nullptr;
+  cudaError_t e = prepare(&w, a, PackArgs{a.x, a.labels, a.lse, a.dloss, nullptr, nullptr}, st);
+  for (w.v0 = 0; w.v0 < a.V; w.v0 += w.piece) {
+    if (e == cudaSuccess) e = tc_loss_dlogits(w, st);
+    if (e == cudaSuccess) e = tc_loss_grads(w, a.dx != nullptr, a.dW, a.dw_bf16, a.accumulate != 0, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dx == nullptr) return cudaSuccess;
+  if (a.bf16)
+    LAUNCH(KK_LOSS_FINISH, loss_dx_kernel<__nv_bfloat16>, dim3(few(a.T, 8)), dim3(ROW_NT), 0, st, w,
+           static_cast<const __nv_bfloat16*>(a.W), static_cast<__nv_bfloat16*>(a.dx));
+  else
+    LAUNCH(KK_LOSS_FINISH, loss_dx_kernel<float>, dim3(few(a.T, 8)), dim3(ROW_NT), 0, st, w,
+           static_cast<const float*>(a.W), static_cast<float*>(a.dx));
+  return cudaSuccess;
 }
 
 }  // namespace moe

@@ -1,0 +1,44 @@
+// What the two halves of the vocabulary loss share: the token lists and
+// epilogue data that vocab_loss.cu prepares, and the products of
+// vocab_loss_tc.cu.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "step.h"
+
+namespace moe {
+
+constexpr int LOSS_TILE = 256;   // rows and columns of a product's tile
+constexpr int LOSS_PART = 128;   // columns of a partial sum of the forward
+constexpr int MAX_PARTS = 3;     // bf16 parts of a float32 value
+
+// Labelled tokens only, in token order, padded with zero rows to a whole tile.
+struct LossWork {
+  int32_t* list;    // [T]: the labelled tokens
+  int32_t* pos;     // [T]: a token's place among them, -1 for the others
+  int32_t* count;   // their number
+  int32_t* label;   // [Tp], of the labelled tokens; -1 on padding
+  float* picked;    // [Tp]: the label's logit
+  float* lse;       // [Tp]
+  float* grad;      // [Tp]: the gradient that reaches the token's loss
+  float* off;       // [Tp]: what the first part of dz leaves of the label's
+  __nv_bfloat16* xp;  // [Tp][parts][ldx]: the labelled rows of x
+  const __nv_bfloat16* wp;  // [V][parts][ldw]: W itself, or its parts
+  float2* partial;  // [V / LOSS_PART, whole tiles][Tp]: the largest logit and the sum of exp of the distances to it
+  __nv_bfloat16* dz;  // [dz parts][Tp][piece]
+  float* acc;       // [Tp][d]: dx before its rounding
+  int T, Tp, d, V, parts, ldx, ldw;
+  int mean;         // that gradient is 1 / count for every token: dz goes without it, dx and dW get it at the end
+  int v0, piece, dzp;  // the piece of the vocabulary in work; bf16 parts of dz
+  uint32_t* err;
+};
+
+// Logits of all labelled tokens, tile by tile: partial and picked.
+cudaError_t tc_loss_logits(const LossWork& w, cudaStream_t st);
+// Logits of a piece again, and from them dz.
+cudaError_t tc_loss_dlogits(const LossWork& w, cudaStream_t st);
+// acc (+)= dz W (dx), dW[piece] (+)= dz^T x (dW not null); acc is overwritten by the first piece.
+cudaError_t tc_loss_grads(const LossWork& w, bool dx, void* dW, bool dw_bf16, bool accumulate, cudaStream_t st);
+
+}  // namespace moe
