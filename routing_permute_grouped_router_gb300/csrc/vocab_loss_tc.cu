@@ -40,8 +40,9 @@ namespace {
 constexpr int BM = 128, BN = 256, BK = 64;  // rows of a CTA (a pair has twice that), columns of a tile, a k-block
 constexpr int BNH = BN / 2;
 constexpr int KB = 2;                       // k-blocks of a stage
-constexpr int A_BYTES = BM * BK * 2, B_BYTES = BNH * BK * 2, BLOCK_BYTES = A_BYTES + B_BYTES;
-constexpr int STAGE = KB * BLOCK_BYTES;
+constexpr int BLOCK_BYTES = BM * BK * 2;    // a loaded box
+constexpr int A_BYTES = KB * BLOCK_BYTES, STAGE = 2 * A_BYTES;
+static_assert(BM == BNH && KB == 2, "boxes of A and B are alike");
 constexpr int NST = 3;
 constexpr int CHAIN = 8;                    // stages added up in TMEM
 constexpr int EPI_WARPS = 8;
@@ -168,28 +169,34 @@ __device__ __forceinline__ bool tile_of(const Deal& d, int pair, int npairs, int
   return true;
 }
 
-// This CTA's half of one k-block: its 128 rows of A and its 128 columns of B.
+// This CTA's half of one stage: its 128 rows of A and its 128 columns of B over a K
+// of 128, in boxes of 16 KB.  K-major operands: a box a k-block.  MN-major ones:
+// a box 64 rows (columns) for all of the stage's K; boxes of one k-block each,
+// twice as many, bound the products with W and x (TMA issue: 1.45 and 1.27
+// PFLOP/s against the logits' 1.93).
 template <int KIND>
-__device__ __forceinline__ void load_block(const Maps& maps, const TcArgs& a, const Tile& t, int seg, int kb,
-                                           uint32_t sA, uint32_t sB, uint32_t bar, uint32_t rank) {
+__device__ __forceinline__ void load_stage(const Maps& maps, const TcArgs& a, const Tile& t, int seg, int b, uint32_t sA,
+                                           uint32_t bar, uint32_t rank) {
   auto ld = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {
     if (rank == 0) tma_load_2d(dst, m, bar, c0, c1);
     else tma_load_2d_pair(dst, m, bar, c0, c1);
   };
-  const int m0 = t.m0 + (int)rank * BM, n0 = t.n0 + (int)rank * BNH, k0 = kb * BK;
+  const uint32_t sB = sA + A_BYTES;
+  const int m0 = t.m0 + (int)rank * BM, n0 = t.n0 + (int)rank * BNH, k0 = b * (BK * KB);
   const Segs& s = a.seg[KIND == GRADS ? t.what : 0];
-  if (KIND != GRADS) {
-    ld(sA, &maps.m[0], s.a[seg] + k0, m0);
-    ld(sB, &maps.m[1], s.b[seg] + k0, (KIND == DLOGITS ? a.w.v0 : 0) + n0);
-  } else if (t.what == 0) {
-    ld(sA, &maps.m[0], k0, s.a[seg] + m0);
-    ld(sB, &maps.m[1], s.b[seg] + n0, a.w.v0 + k0);
-    ld(sB + 8192, &maps.m[1], s.b[seg] + n0 + 64, a.w.v0 + k0);
-  } else {
-    ld(sA, &maps.m[2], m0, s.a[seg] + k0);
-    ld(sA + 8192, &maps.m[2], m0 + 64, s.a[seg] + k0);
-    ld(sB, &maps.m[3], s.b[seg] + n0, k0);
-    ld(sB + 8192, &maps.m[3], s.b[seg] + n0 + 64, k0);
+#pragma unroll
+  for (int i = 0; i < KB; ++i) {
+    const uint32_t dA = sA + i * BLOCK_BYTES, dB = sB + i * BLOCK_BYTES;
+    if (KIND != GRADS) {
+      ld(dA, &maps.m[0], s.a[seg] + k0 + i * BK, m0);
+      ld(dB, &maps.m[1], s.b[seg] + k0 + i * BK, (KIND == DLOGITS ? a.w.v0 : 0) + n0);
+    } else if (t.what == 0) {
+      ld(dA, &maps.m[0], k0 + i * BK, s.a[seg] + m0);
+      ld(dB, &maps.m[1], s.b[seg] + n0 + i * 64, a.w.v0 + k0);
+    } else {
+      ld(dA, &maps.m[2], m0 + i * 64, s.a[seg] + k0);
+      ld(dB, &maps.m[3], s.b[seg] + n0 + i * 64, k0);
+    }
   }
 }
 
@@ -408,11 +415,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
             const uint32_t fb_local = smem_addr(&full_bar[stage]);
             if (rank == 0) mbar_expect_tx(fb_local, 2 * STAGE);
             const uint32_t fb = rank == 0 ? fb_local : mapa_shared(fb_local, 0);
-#pragma unroll
-            for (int kk = 0; kk < KB; ++kk) {
-              const uint32_t sA = smem_base + stage * STAGE + kk * BLOCK_BYTES;
-              load_block<KIND>(maps, a, t, s, b * KB + kk, sA, sA + A_BYTES, fb, rank);
-            }
+            load_stage<KIND>(maps, a, t, s, b, smem_base + stage * STAGE, fb, rank);
             ++issued;
             if (++stage == NST) {
               stage = 0;
@@ -469,15 +472,13 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
               break;
             }
             tc_fence_after();
+            const uint32_t sA = smem_base + stage * STAGE, sB = sA + A_BYTES;
 #pragma unroll
-            for (int kk = 0; kk < KB; ++kk) {
-              const uint32_t sA = smem_base + stage * STAGE + kk * BLOCK_BYTES, sB = sA + A_BYTES;
-#pragma unroll
-              for (int k16 = 0; k16 < BK / 16; ++k16) {
-                const uint64_t ad = a_mn ? sdesc(sA + k16 * 2048, 8192, 1024) : sdesc(sA + k16 * 32, 16, 1024);
-                const uint64_t bd = b_mn ? sdesc(sB + k16 * 2048, 8192, 1024) : sdesc(sB + k16 * 32, 16, 1024);
-                umma_bf16_pair(d_tmem, ad, bd, id, ((b - b0) | kk | k16) != 0 ? 1u : 0u);
-              }
+            for (int k16 = 0; k16 < KB * BK / 16; ++k16) {
+              const uint32_t at = k16 / 4 * BLOCK_BYTES + k16 % 4 * 32;  // K-major
+              const uint64_t ad = a_mn ? sdesc(sA + k16 * 2048, BLOCK_BYTES, 1024) : sdesc(sA + at, 16, 1024);
+              const uint64_t bd = b_mn ? sdesc(sB + k16 * 2048, BLOCK_BYTES, 1024) : sdesc(sB + at, 16, 1024);
+              umma_bf16_pair(d_tmem, ad, bd, id, ((b - b0) | k16) != 0 ? 1u : 0u);
             }
             umma_commit_pair(smem_addr(&empty_bar[stage]), 0x3);
             if (++stage == NST) {
@@ -687,9 +688,9 @@ cudaError_t tc_loss_grads(const LossWork& w, bool dx, void* dW, bool dw_bf16, bo
   a.seg[0] = segs(w.parts == 1 ? 1 : w.dzp, w.parts, w.Tp, w.ldw);
   a.seg[1] = segs(w.dzp, w.parts, w.Tp, w.ldx);
   const uint64_t planes = (uint64_t)w.dzp * w.Tp;
-  bool ok = make_map(&maps.m[0], w.dz, planes, w.piece, BK, BM) && make_map(&maps.m[2], w.dz, planes, w.piece, 64, BK) &&
-            make_map(&maps.m[1], w.wp, w.V, (uint64_t)w.parts * w.ldw, 64, BK) &&
-            make_map(&maps.m[3], w.xp, w.Tp, (uint64_t)w.parts * w.ldx, 64, BK);
+  bool ok = make_map(&maps.m[0], w.dz, planes, w.piece, BK, BM) && make_map(&maps.m[2], w.dz, planes, w.piece, 64, KB * BK) &&
+            make_map(&maps.m[1], w.wp, w.V, (uint64_t)w.parts * w.ldw, 64, KB * BK) &&
+            make_map(&maps.m[3], w.xp, w.Tp, (uint64_t)w.parts * w.ldx, 64, KB * BK);
   if (dx) ok = ok && make_map(&maps.m[4], w.acc, w.Tp, w.d, 32, 32, true);
   if (dW) ok = ok && make_map(&maps.m[5], dW, w.V, w.d, dw_bf16 ? 64 : 32, 32, !dw_bf16);
   if (!ok) return cudaErrorInvalidValue;
