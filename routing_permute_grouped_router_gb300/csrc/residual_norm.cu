@@ -4,16 +4,31 @@
 //
 // and its backward; formulas are in moe.h.
 //
-// A row has one CTA and is walked in a loop, again from cache for each pass.
-// The columns' sums are taken in a pass of their own before anything is written
-// (dx and dy may be dh or dout).  All statistics and sums are fp32.
-#include "common.cuh"
+// Both passes are bound by HBM: the forward reads x and y and writes out and h,
+// the backward reads dh, out, dout and y and writes dx and dy.  Up to 512 threads
+// share a row, 16 elements each, while copies bring the next rows into a ring in
+// shared memory.  A row has two reductions, of which the second needs the first:
+// the second of a row and the first of the row after it share one barrier.
+// Threads keep their columns' weights and, in the backward, the columns' sums in
+// registers over all rows of the CTA; a second kernel adds the CTAs' sums in
+// CTA order, so results do not depend on timing.  Statistics and sums are fp32.
+//
+// Rows that the ring has no room for (over 8192 elements; in the backward float32
+// rows of all four tensors from about 6900) have one CTA each and are walked in a
+// loop, again from cache for each pass.  There the columns' sums are taken in a
+// pass of their own before anything is written (dx and dy may be dh or dout).
+#include <algorithm>
+
+#include "row_ring.cuh"
 #include "step.h"
 
 namespace moe {
 namespace {
 
-constexpr int WIDE_NT = 512;   // threads of a row's CTA
+constexpr int FWD_REGS = 80;   // a thread's in the forward: three CTAs of 256 fit an SM
+constexpr int BWD_NT = 512;    // most threads of the backward's CTAs, one an SM
+constexpr int MAX_GROUPS = BWD_NT / 32;
+constexpr int WIDE_NT = 512;   // threads of a wide row's CTA
 constexpr int COL_NT = 128;
 constexpr int RED_COLS = 32, RED_STRIPS = 32;
 
@@ -27,10 +42,338 @@ struct JoinK {
   float* partial;  // [parts][2][d]: sums of dh n, and of row_gate D m
   int64_t rows;
   int d, parts, accumulate;
+  int tpr, slot, ring;  // threads that share a row, bytes of a tensor's row in the ring, places
   float rs, bs, eps;
   uint32_t* err;
 };
 
+// ------------------------------ rows in the ring --------------------------- //
+// A group of tpr threads, its rows (first, first + step, ...) of up to four
+// tensors, and its ring.  The group's first thread starts the copies.
+template <typename T, bool WHOLE>
+struct JoinRows {
+  const void *t0, *t1, *t2, *t3;  // null where there is none; the others follow one another in a place
+  int nbuf;
+  char* base;
+  uint64_t* bars;
+  int64_t first, step, rows;
+  int d, slot, ring;
+  int at = 0;          // the place of the row in work
+  uint32_t phase = 0;  // and its barrier's phase
+  __device__ __forceinline__ JoinRows(const void* a, const void* b, const void* c, const void* e)
+      : t0(a), t1(b), t2(c), t3(e), nbuf((a != nullptr) + (b != nullptr) + (c != nullptr) + (e != nullptr)) {}
+  __device__ __forceinline__ void start(int64_t row, int p) const {
+    if (row >= rows) return;
+    const Span sp = row_span<T, WHOLE>(row, rows, d);
+    const uint32_t bar = sm_addr(bars + p);
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(sp.bytes * nbuf) : "memory");
+    if (sp.bytes <= 0) return;
+    uint32_t to = sm_addr(place(p, 0));
+    auto copy = [&](const void* t) {
+      if (t == nullptr) return;
+      copy_row(to, static_cast<const char*>(t) + sp.at, sp.bytes, bar);
+      to += slot;
+    };
+    copy(t0);
+    copy(t1);
+    copy(t2);
+    copy(t3);
+  }
+  __device__ __forceinline__ void wait(uint32_t* err) const {
+    if (!ring_ready(sm_addr(bars + at), phase)) ring_wait(sm_addr(bars + at), phase, err);
+  }
+  __device__ __forceinline__ char* place(int p, int b) const { return base + (size_t)(p * nbuf + b) * slot; }
+  __device__ __forceinline__ void next() {
+    if (++at == ring) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+extern __shared__ __align__(128) char join_smem[];
+
+// The barriers, and the first rows on their way.
+template <typename T, bool WHOLE>
+__device__ __forceinline__ void begin(JoinRows<T, WHOLE>& R, const JoinK& a, uint64_t* bars, int r) {
+  const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr;  // rows go to all CTAs before a second group of any
+  R.base = join_smem + (size_t)g * a.ring * R.nbuf * a.slot;
+  R.bars = bars + g * RING;
+  R.first = (int64_t)g * gridDim.x + blockIdx.x;
+  R.step = (int64_t)gridDim.x * groups;
+  R.rows = a.rows;
+  R.d = a.d;
+  R.slot = a.slot;
+  R.ring = a.ring;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < groups * RING; ++i)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(sm_addr(bars + i)) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  pdl_enter();  // see pdl_wait: no global access before this
+  if (r == 0)
+    for (int i = 0; i < a.ring; ++i) R.start(R.first + i * R.step, i);
+}
+
+// The columns' weights times `by` in pairs, `by` where there are none; 0 past the row's end.
+template <int VN>
+__device__ __forceinline__ void weights_or(const float* w, const float* w2, float by, int r, int tpr, int d,
+                                           float2 (&v)[EPT / 2]) {
+#pragma unroll
+  for (int c = 0; c < EPT; ++c) {
+    float u = 0.f;
+    if (in_row<VN>(r, tpr, c, d)) {
+      const int i = column<VN>(r, tpr, c);
+      u = by * (w ? __ldg(w + i) : 1.f) * (w2 ? __ldg(w2 + i) : 1.f);
+    }
+    (c & 1 ? v[c / 2].y : v[c / 2].x) = u;
+  }
+}
+
+template <typename T, bool WHOLE>
+__global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
+  constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2;
+  __shared__ float scratch[2][2][16];
+  __shared__ uint64_t bars[MAX_GROUPS * RING];
+  int turn = 0;
+  const Group<false> grp(a.tpr);
+  const int r = grp.r, nw = grp.warps, lane = threadIdx.x % 32;
+  const bool upper = lane >= 16, post = a.gamma_post != nullptr, following = a.gamma_next != nullptr, branch = a.y != nullptr;
+  JoinRows<T, WHOLE> R(a.x, a.y, nullptr, nullptr);
+  constexpr int bx = 0, by_ = 1;
+  begin<T, WHOLE>(R, a, bars, r);
+  const T *x = static_cast<const T*>(a.x), *y = static_cast<const T*>(a.y);
+  const float inv = 1.f / (float)a.d;
+  float2 ga[EPT / 2], gn[EPT / 2];
+  weights_or<VN>(a.gamma_post, a.gate, a.bs, r, a.tpr, a.d, ga);
+  weights_or<VN>(a.gamma_next, nullptr, 1.f, r, a.tpr, a.d, gn);
+  // both sums over the group, the first in the lower half of the lanes
+  auto sums = [&](float u, float v) {
+    float m = half_sums(u, v, upper);
+    if (nw > 1) {
+      if ((lane & 15) == 0) scratch[turn][upper][threadIdx.x / 32] = m;
+      grp.sync();
+      m = sum_over(scratch[turn][upper][lane & (nw - 1)], nw);
+      turn ^= 1;
+    }
+    __syncwarp();
+    return m;
+  };
+  // the thread's part of sum(y^2) of the row at place R.at
+  auto squares = [&](int64_t row) {
+    const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
+    float2 s = both(0.f);
+#pragma unroll
+    for (int i = 0; i < EPT / 2 / CN; ++i) {
+      float2 v[CN];
+      take<T, WHOLE>(R.place(R.at, by_), sp, y, r, a.tpr, a.d, i, v);
+#pragma unroll
+      for (int c = 0; c < CN; ++c) s = fma2(v[c], v[c], s);
+    }
+    return s.x + s.y;
+  };
+  float first = 0.f;  // the mean of y^2 of the row in work
+  if (R.first < a.rows) {
+    R.wait(a.err);
+    if (post) first = __shfl_sync(0xffffffffu, sums(squares(R.first), 0.f), 0) * inv;
+  }
+#pragma unroll 1
+  for (int64_t row = R.first; row < a.rows; row += R.step) {
+    const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
+    const float ry = post ? rsqrtf(first + a.eps) : 1.f;
+    const float2 by = both(ry * (a.row_gate ? __ldg(a.row_gate + row) : 1.f)), rs = both(a.rs);
+    float2 o[EPT / 2 / CN][CN], s2 = both(0.f);
+#pragma unroll
+    for (int i = 0; i < EPT / 2 / CN; ++i) {
+      take<T, WHOLE>(R.place(R.at, bx), sp, x, r, a.tpr, a.d, i, o[i]);
+      float2 v[CN];
+      if (branch) take<T, WHOLE>(R.place(R.at, by_), sp, y, r, a.tpr, a.d, i, v);
+#pragma unroll
+      for (int c = 0; c < CN; ++c) {
+        o[i][c] = mul2(o[i][c], rs);
+        if (branch) o[i][c] = fma2(mul2(v[c], by), ga[i * CN + c], o[i][c]);
+        s2 = fma2(o[i][c], o[i][c], s2);
+      }
+    }
+    const int place = R.at;
+    float s1 = 0.f;
+    R.next();
+    if (row + R.step < a.rows) {
+      R.wait(a.err);
+      if (post) s1 = squares(row + R.step);
+    }
+    const float m = sums(s2.x + s2.y, s1) * inv;
+    if (r == 0) R.start(row + R.ring * R.step, place);  // everyone has read the row
+    const float ro = rsqrtf(__shfl_sync(0xffffffffu, m, 0) + a.eps);
+    first = __shfl_sync(0xffffffffu, m, 16);
+    const float2 ro2 = both(ro);
+#pragma unroll
+    for (int i = 0; i < EPT / 2 / CN; ++i) {
+      if (a.out) put<T, WHOLE>(static_cast<T*>(a.out) + row * a.d, r, a.tpr, a.d, i, o[i]);
+      if (following) {
+#pragma unroll
+        for (int c = 0; c < CN; ++c) o[i][c] = mul2(mul2(o[i][c], ro2), gn[i * CN + c]);
+        put<T, WHOLE>(static_cast<T*>(a.h) + row * a.d, r, a.tpr, a.d, i, o[i]);
+      }
+    }
+    if (r == 0) {
+      if (a.rstd_post) a.rstd_post[row] = ry;
+      if (a.rstd_next) a.rstd_next[row] = ro;
+    }
+  }
+}
+
+template <typename T, bool WHOLE>
+__global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
+  constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2, NC = EPT / 2 / CN;
+  __shared__ float4 scratch[2 * 16];
+  __shared__ uint64_t bars[MAX_GROUPS * RING];
+  const Group<true> grp(a.tpr);
+  const int r = grp.r;
+  const bool post = a.gamma_post != nullptr, following = a.gamma_next != nullptr, branch = a.y != nullptr;
+  JoinRows<T, WHOLE> R(following ? a.dh : nullptr, following ? a.out : nullptr, a.dout, a.y);
+  constexpr int bh = 0, bo = 1;
+  const int bd = following ? 2 : 0, by_ = R.nbuf - 1;
+  begin<T, WHOLE>(R, a, bars, r);
+  const T *dh = static_cast<const T*>(a.dh), *out = static_cast<const T*>(a.out), *dout = static_cast<const T*>(a.dout);
+  const T* y = static_cast<const T*>(a.y);
+  const float inv = 1.f / (float)a.d;
+  float2 gn[EPT / 2], ga[EPT / 2], sn[EPT / 2], sm[EPT / 2];  // weights; the columns' sums of dh n and row_gate D m
+  weights_or<VN>(a.gamma_next, nullptr, 1.f, r, a.tpr, a.d, gn);
+  weights_or<VN>(a.gamma_post, a.gate, a.bs, r, a.tpr, a.d, ga);
+#pragma unroll
+  for (int c = 0; c < EPT / 2; ++c) sn[c] = sm[c] = both(0.f);
+  // ro, ry and the gate of a row, loaded two rows ahead of their use
+  auto stats = [&](int64_t row) {
+    const bool in = row < a.rows;
+    return make_float3(in && following ? __ldg(a.rstd_next + row) : 0.f, in && post ? __ldg(a.rstd_post + row) : 1.f,
+                       in && a.row_gate ? __ldg(a.row_gate + row) : 1.f);
+  };
+  // the warp's sum of v n of the row at place R.at, and its part of the columns' sums
+  auto along = [&](int64_t row, float ro) {
+    R.wait(a.err);
+    if (!following) return 0.f;
+    const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
+    float2 s = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      float2 n[CN], v[CN];
+      take<T, WHOLE>(R.place(R.at, bo), sp, out, r, a.tpr, a.d, i, n);
+      take<T, WHOLE>(R.place(R.at, bh), sp, dh, r, a.tpr, a.d, i, v);
+#pragma unroll
+      for (int c = 0; c < CN; ++c) {  // past the row's end dh is 0
+        v[c] = mul2(mul2(n[c], both(ro)), v[c]);
+        sn[i * CN + c] = add2(sn[i * CN + c], v[c]);
+        s = fma2(v[c], gn[i * CN + c], s);
+      }
+    }
+    return warp_sum(s.x + s.y);
+  };
+  const bool alone = grp.warps == 1;
+  int turn = 0;
+  // both sums over the group
+  auto sums = [&](float u, float v) {
+    if (alone) {
+      __syncwarp();
+      return make_float2(u, v);
+    }
+    grp.give(make_float4(u, v, 0.f, 0.f), scratch, turn);
+    grp.sync();
+    const float4 w = grp.get(scratch, turn);
+    turn ^= 1;
+    return make_float2(sum_over(w.x, grp.warps), sum_over(w.y, grp.warps));
+  };
+  float3 st = stats(R.first), st1 = stats(R.first + R.step);
+  float mvn = 0.f;
+  if (R.first < a.rows) mvn = sums(0.f, along(R.first, st.x)).y * inv;
+#pragma unroll 1
+  for (int64_t row = R.first; row < a.rows; row += R.step) {
+    const float3 st2 = stats(row + 2 * R.step);
+    const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
+    const float2 ro = both(st.x), ry = both(st.y), rg = both(st.z), k = both(-mvn * st.x);
+    float2 D[NC][CN], m[NC][CN], s = both(0.f);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if (dout != nullptr) {
+        take<T, WHOLE>(R.place(R.at, bd), sp, dout, r, a.tpr, a.d, i, D[i]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < CN; ++c) D[i][c] = both(0.f);
+      }
+      if (following) {
+        float2 n[CN], v[CN];
+        take<T, WHOLE>(R.place(R.at, bo), sp, out, r, a.tpr, a.d, i, n);
+        take<T, WHOLE>(R.place(R.at, bh), sp, dh, r, a.tpr, a.d, i, v);
+#pragma unroll
+        for (int c = 0; c < CN; ++c)
+          D[i][c] = fma2(ro, fma2(v[c], gn[i * CN + c], mul2(n[c], k)), D[i][c]);
+      }
+      if (branch) {
+        take<T, WHOLE>(R.place(R.at, by_), sp, y, r, a.tpr, a.d, i, m[i]);
+#pragma unroll
+        for (int c = 0; c < CN; ++c) {
+          m[i][c] = mul2(m[i][c], ry);
+          const float2 t = mul2(D[i][c], m[i][c]);
+          sm[i * CN + c] = fma2(t, rg, sm[i * CN + c]);
+          s = fma2(t, ga[i * CN + c], s);
+        }
+      }
+    }
+    const int place = R.at;
+    float ahead = 0.f;
+    R.next();
+    const float mine = branch ? warp_sum(s.x + s.y) : 0.f;
+    if (row + R.step < a.rows) ahead = along(row + R.step, st1.x);
+    const float2 t = sums(mine, ahead);
+    if (r == 0) {
+      R.start(row + R.ring * R.step, place);  // everyone has read the row
+      if (a.drow_gate) a.drow_gate[row] = t.x;
+    }
+    mvn = t.y * inv;
+    const float2 rs = both(a.rs), mwm = both(post ? -t.x * st.z * inv : 0.f);
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      if (branch) {
+#pragma unroll
+        for (int c = 0; c < CN; ++c)
+          m[i][c] = mul2(fma2(mul2(D[i][c], rg), ga[i * CN + c], mul2(m[i][c], mwm)), ry);
+        put<T, WHOLE>(static_cast<T*>(a.dy) + row * a.d, r, a.tpr, a.d, i, m[i]);
+      }
+      if (a.dx) {
+#pragma unroll
+        for (int c = 0; c < CN; ++c) D[i][c] = mul2(D[i][c], rs);
+        put<T, WHOLE>(static_cast<T*>(a.dx) + row * a.d, r, a.tpr, a.d, i, D[i]);
+      }
+    }
+    st = st1;
+    st1 = st2;
+  }
+  __syncthreads();
+  // the CTA's sums, over its groups in order, are one row pair of the partials
+  const int groups = blockDim.x / a.tpr;
+  float* dst = a.partial + (size_t)blockIdx.x * 2 * a.d;
+  float* own = groups == 1 ? dst : reinterpret_cast<float*>(join_smem) + (size_t)grp.g * 2 * a.d;
+#pragma unroll
+  for (int c = 0; c < EPT; ++c) {
+    const int col = column<VN>(r, a.tpr, c);
+    if (in_row<VN>(r, a.tpr, c, a.d)) {
+      own[col] = c & 1 ? sn[c / 2].y : sn[c / 2].x;
+      own[a.d + col] = c & 1 ? sm[c / 2].y : sm[c / 2].x;
+    }
+  }
+  if (groups == 1) return;
+  __syncthreads();
+  const float* all = reinterpret_cast<const float*>(join_smem);
+  for (int i = threadIdx.x; i < 2 * a.d; i += blockDim.x) {
+    float u = 0.f;
+#pragma unroll 4
+    for (int g = 0; g < groups; ++g) u += all[(size_t)g * 2 * a.d + i];
+    dst[i] = u;
+  }
+}
+
+// ------------------------------ wide rows ---------------------------------- //
 __device__ __forceinline__ float row_sum(float v, float* scratch, int& turn) {
   v = warp_sum(v);
   if (threadIdx.x % 32 == 0) scratch[turn * 16 + threadIdx.x / 32] = v;
@@ -39,19 +382,9 @@ __device__ __forceinline__ float row_sum(float v, float* scratch, int& turn) {
   turn ^= 1;
   return v;
 }
-template <typename T, int VN>
-__device__ __forceinline__ void ld_n(const T* p, float (&v)[VN]) {
-  if constexpr (VN == 1) v[0] = to_f32(*p);
-  else unpack(*reinterpret_cast<const uint4*>(p), v);
-}
-template <typename T, int VN>
-__device__ __forceinline__ void st_n(T* p, const float (&v)[VN]) {
-  if constexpr (VN == 1) *p = from_f32<T>(v[0]);
-  else stg16(p, pack(v));
-}
 // a weight of each channel, 1 where there is none (vectors need not be aligned)
 template <int VN>
-__device__ __forceinline__ void ld_w(const float* p, int i, float (&v)[VN]) {
+__device__ __forceinline__ void ld_or_one(const float* p, int i, float (&v)[VN]) {
 #pragma unroll
   for (int j = 0; j < VN; ++j) v[j] = p == nullptr ? 1.f : __ldg(p + i + j);
 }
@@ -84,8 +417,8 @@ __global__ void __launch_bounds__(WIDE_NT) join_fwd_wide_kernel(const JoinK a) {
       if (a.y) {
         float v[VN], g[VN], w[VN];
         ld_n<T, VN>(y + i, v);
-        ld_w<VN>(a.gamma_post, i, g);
-        ld_w<VN>(a.gate, i, w);
+        ld_or_one<VN>(a.gamma_post, i, g);
+        ld_or_one<VN>(a.gate, i, w);
 #pragma unroll
         for (int j = 0; j < VN; ++j) o[j] = fmaf(v[j] * by, g[j] * w[j], o[j]);
       }
@@ -106,7 +439,7 @@ __global__ void __launch_bounds__(WIDE_NT) join_fwd_wide_kernel(const JoinK a) {
       if (a.out) st_n<T, VN>(static_cast<T*>(a.out) + row * a.d + i, o);
       if (a.gamma_next) {
         float g[VN];
-        ld_w<VN>(a.gamma_next, i, g);
+        ld_or_one<VN>(a.gamma_next, i, g);
 #pragma unroll
         for (int j = 0; j < VN; ++j) o[j] *= ro * g[j];
         st_n<T, VN>(static_cast<T*>(a.h) + row * a.d + i, o);
@@ -132,7 +465,7 @@ __device__ __forceinline__ void stream_grad(const JoinK& a, int64_t row, int i, 
     float n[VN], v[VN], g[VN];
     ld_n<T, VN>(static_cast<const T*>(a.out) + row * a.d + i, n);
     ld_n<T, VN>(static_cast<const T*>(a.dh) + row * a.d + i, v);
-    ld_w<VN>(a.gamma_next, i, g);
+    ld_or_one<VN>(a.gamma_next, i, g);
 #pragma unroll
     for (int j = 0; j < VN; ++j) D[j] = fmaf(ro, fmaf(v[j], g[j], -(n[j] * ro) * mvn), D[j]);
   }
@@ -151,7 +484,7 @@ __global__ void __launch_bounds__(WIDE_NT) join_bwd_stats_kernel(const JoinK a) 
         float n[VN], v[VN], g[VN];
         ld_n<T, VN>(static_cast<const T*>(a.out) + row * a.d + i, n);
         ld_n<T, VN>(static_cast<const T*>(a.dh) + row * a.d + i, v);
-        ld_w<VN>(a.gamma_next, i, g);
+        ld_or_one<VN>(a.gamma_next, i, g);
 #pragma unroll
         for (int j = 0; j < VN; ++j) s = fmaf(v[j] * g[j], n[j], s);
       }
@@ -213,8 +546,8 @@ __global__ void __launch_bounds__(WIDE_NT) join_bwd_wide_kernel(const JoinK a) {
         float D[VN], m[VN], g[VN], w[VN];
         stream_grad<T, VN>(a, row, i, ro, mvn, D);
         ld_n<T, VN>(y + i, m);
-        ld_w<VN>(a.gate, i, g);
-        ld_w<VN>(a.gamma_post, i, w);
+        ld_or_one<VN>(a.gate, i, g);
+        ld_or_one<VN>(a.gamma_post, i, w);
 #pragma unroll
         for (int j = 0; j < VN; ++j) s = fmaf(a.bs * D[j] * g[j] * w[j], m[j] * ry, s);
       }
@@ -227,8 +560,8 @@ __global__ void __launch_bounds__(WIDE_NT) join_bwd_wide_kernel(const JoinK a) {
       stream_grad<T, VN>(a, row, i, ro, mvn, D);
       if (a.y) {
         ld_n<T, VN>(y + i, m);
-        ld_w<VN>(a.gate, i, g);
-        ld_w<VN>(a.gamma_post, i, w);
+        ld_or_one<VN>(a.gate, i, g);
+        ld_or_one<VN>(a.gamma_post, i, w);
 #pragma unroll
         for (int j = 0; j < VN; ++j) {
           const float G = a.bs * rg * g[j] * D[j];
@@ -334,15 +667,75 @@ cudaError_t bwd_wide(JoinK& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   return launch_pdl(join_bwd_wide_kernel<T, VN>, dim3(row_ctas(a.rows)), dim3(WIDE_NT), 0, st, a);
 }
+// Sizes of a launch over rows in the ring of `bufs` tensors.  Forward: CTAs of one
+// group of threads, or of four warps with rows of their own, as many as the
+// registers allow.  Backward: one CTA an SM, of as many groups as leave the ring
+// three places.  ring < 2: no room, the wide kernels.
+struct Grid {
+  int threads, ctas, tpr, slot, ring;
+  size_t smem;
+};
+Grid grid_of(int64_t rows, int d, int es, int bufs, bool bwd) {
+  Grid g{};
+  if (d > MAX_TPR * EPT) return g;
+  g.tpr = threads_per_row(d);
+  g.slot = (d * es + 15) / 16 * 16 + (d * es % 16 ? 16 : 0);
+  const size_t place = (size_t)bufs * g.slot;
+  int groups = bwd ? BWD_NT / g.tpr : (g.tpr == 32 ? 4 : 1), per = bwd ? 1 : 65536 / (g.tpr * groups * FWD_REGS);
+  while (bwd && groups > 1 && groups * 3 * place > SMEM_SM - 1024) groups /= 2;
+  while (per > 1 && per * 2 * (groups * place + 1024) > SMEM_SM) --per;
+  g.ring = (int)std::min<size_t>(RING, (SMEM_SM / per - 1024) / (groups * place));
+  g.threads = g.tpr * groups;
+  g.smem = g.ring * groups * place;
+  const size_t sums = groups > 1 ? (size_t)groups * 2 * d * 4 : 0;  // the backward's groups' sums take the ring's place
+  if (bwd && g.smem < sums) g.smem = sums;
+  const int64_t need = bwd ? rows : (rows + groups - 1) / groups;
+  g.ctas = (int)std::min<int64_t>(need, (int64_t)sm_count() * per);
+  return g;
+}
+
+template <typename K>
+cudaError_t launch_ring(K kernel, const Grid& g, JoinK& a, bool* attr_done, cudaStream_t st) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!attr_done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_SM);
+    if (e != cudaSuccess) return e;
+    attr_done[dev] = true;
+  }
+  a.tpr = g.tpr;
+  a.slot = g.slot;
+  a.ring = g.ring;
+  a.parts = g.ctas;
+  return launch_pdl(kernel, dim3(g.ctas), dim3(g.threads), g.smem, st, a);
+}
+template <typename T, bool WHOLE>
+cudaError_t fwd_w(JoinK& a, cudaStream_t st) {
+  static bool done[64] = {false};
+  const Grid g = grid_of(a.rows, a.d, sizeof(T), a.y ? 2 : 1, false);
+  if (g.ring < 2) return fwd_wide<T, WHOLE ? Vec<T>::N : 1>(a, st);
+  return launch_ring(join_fwd_kernel<T, WHOLE>, g, a, done, st);
+}
+template <typename T, bool WHOLE>
+cudaError_t bwd_w(JoinK& a, cudaStream_t st) {
+  static bool done[64] = {false};
+  const int bufs = (a.gamma_next ? 2 : 0) + (a.dout ? 1 : 0) + (a.y ? 1 : 0);
+  const Grid g = grid_of(a.rows, a.d, sizeof(T), bufs, true);
+  if (g.ring < 2) return bwd_wide<T, WHOLE ? Vec<T>::N : 1>(a, st);
+  return launch_ring(join_bwd_kernel<T, WHOLE>, g, a, done, st);
+}
 template <typename T>
-cudaError_t fwd_t(const JoinK& a, cudaStream_t st) {
-  return a.d % Vec<T>::N == 0 ? fwd_wide<T, Vec<T>::N>(a, st) : fwd_wide<T, 1>(a, st);
+cudaError_t fwd_t(JoinK& a, cudaStream_t st) {
+  return a.d % Vec<T>::N == 0 ? fwd_w<T, true>(a, st) : fwd_w<T, false>(a, st);
 }
 template <typename T>
 cudaError_t bwd_t(JoinK& a, cudaStream_t st) {
-  return a.d % Vec<T>::N == 0 ? bwd_wide<T, Vec<T>::N>(a, st) : bwd_wide<T, 1>(a, st);
+  return a.d % Vec<T>::N == 0 ? bwd_w<T, true>(a, st) : bwd_w<T, false>(a, st);
 }
-size_t partial_bytes(int64_t rows, int d) { return (size_t)wide_slices(rows, d) * 2 * d * 4; }
+size_t partial_bytes(int64_t rows, int d) {
+  return (size_t)std::max<int64_t>(wide_slices(rows, d), std::min<int64_t>(rows, sm_count())) * 2 * d * 4;
+}
 
 }  // namespace
 
@@ -351,7 +744,7 @@ size_t join_ws_bytes(int64_t rows, int d) {
 }
 
 cudaError_t launch_join_fwd(const JoinArgs& args, uint32_t* err, cudaStream_t st) {
-  const JoinK a = kernel_args(args, err);
+  JoinK a = kernel_args(args, err);
   LaunchScope ls(KK_RESIDUAL_NORM_FWD, st);
   return args.p.dtype == MOE_BF16 ? fwd_t<__nv_bfloat16>(a, st) : fwd_t<float>(a, st);
 }
