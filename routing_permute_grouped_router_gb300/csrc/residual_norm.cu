@@ -28,6 +28,7 @@ namespace {
 constexpr int FWD_REGS = 80;   // a thread's in the forward: three CTAs of 256 fit an SM
 constexpr int BWD_NT = 512;    // most threads of the backward's CTAs, one an SM
 constexpr int MAX_GROUPS = BWD_NT / 32;
+constexpr int BWD_SMEM = 230400;  // a CTA's dynamic shared memory there: 227 KB less its static part
 constexpr int WIDE_NT = 512;   // threads of a wide row's CTA
 constexpr int COL_NT = 128;
 constexpr int RED_COLS = 32, RED_STRIPS = 32;
@@ -93,11 +94,87 @@ struct JoinRows {
 
 extern __shared__ __align__(128) char join_smem[];
 
+// A thread's chunks of rows in the ring.  Whole vectors: their offsets are the
+// same in every row, and one past the row's end is read from 16 bytes of zeros,
+// which leaves a load a chunk and no branch.  (A checked load each and addresses
+// of 64 bits: the backward 347 us at 32768 x 4096 bf16.)
+template <typename T, bool WHOLE>
+struct Mine {
+  static constexpr int CN = Chunk<T, WHOLE>::N / 2, NC = EPT / 2 / CN;
+  int r, tpr, d, slot;
+  uint32_t zeros, off[WHOLE ? NC : 1];
+  bool in[WHOLE ? NC : 1];
+  __device__ __forceinline__ Mine(const JoinK& a, int r_, uint32_t zeros_) : r(r_), tpr(a.tpr), d(a.d), slot(a.slot), zeros(zeros_) {
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        off[i] = (r + i * tpr) * 16;
+        in[i] = (r + i * tpr) * Vec<T>::N < d;
+      }
+    }
+  }
+  // chunk i of tensor b of the place at `at`; `tensor` is where its rows are (whose last one a copy may cut off)
+  __device__ __forceinline__ void get(const char* at, int b, const Span& sp, const void* tensor, int i, float2 (&v)[CN]) const {
+    if constexpr (WHOLE) {
+      const uint4 u = lds(in[i] ? sm_addr(at) + b * slot + off[i] : zeros);
+      float w[2 * CN];
+      unpack(u, w);
+#pragma unroll
+      for (int c = 0; c < CN; ++c) v[c] = make_float2(w[2 * c], w[2 * c + 1]);
+    } else {
+      take<T, WHOLE>(at + b * slot, sp, static_cast<const T*>(tensor), r, tpr, d, i, v);
+    }
+  }
+  __device__ __forceinline__ void set(void* tensor, int64_t row, int i, const float2 (&v)[CN]) const {
+    if constexpr (WHOLE) {
+      float w[2 * CN];
+#pragma unroll
+      for (int c = 0; c < CN; ++c) {
+        w[2 * c] = v[c].x;
+        w[2 * c + 1] = v[c].y;
+      }
+      if (in[i]) stg16(static_cast<char*>(tensor) + row * d * (int64_t)sizeof(T) + off[i], pack(w));
+    } else {
+      put<T, WHOLE>(static_cast<T*>(tensor) + row * d, r, tpr, d, i, v);
+    }
+  }
+  // a columns' weight in shared memory, 16 bytes of a chunk at a time so that neighbouring lanes read neighbouring ones
+  __device__ __forceinline__ void weights(uint32_t w, int i, float2 (&v)[CN]) const {
+#pragma unroll
+    for (int j = 0; j < CN / 2; ++j) {
+      const uint4 u = lds(w + j * (NC * tpr * 16) + (r + i * tpr) * 16);
+      v[2 * j] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+      v[2 * j + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+    }
+  }
+  // the same where whole vectors are not, from registers
+  template <int N>
+  __device__ __forceinline__ void weights(uint32_t w, const float2 (&regs)[N], int i, float2 (&v)[CN]) const {
+    if constexpr (WHOLE) {
+      weights(w, i, v);
+    } else {
+#pragma unroll
+      for (int c = 0; c < CN; ++c) v[c] = regs[i * CN + c];
+    }
+  }
+  __device__ __forceinline__ void keep_weights(float* w, const float* p, const float* p2, float by) const {
+    for (int c = threadIdx.x; c < EPT * tpr; c += blockDim.x) {
+      const int q = c / (2 * CN), j = c % (2 * CN);
+      w[(j / 4 * NC * tpr + q) * 4 + j % 4] = c < d ? by * (p ? __ldg(p + c) : 1.f) * (p2 ? __ldg(p2 + c) : 1.f) : 0.f;
+    }
+  }
+  __device__ __forceinline__ static uint4 lds(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+  }
+};
+
 // The barriers, and the first rows on their way.
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void begin(JoinRows<T, WHOLE>& R, const JoinK& a, uint64_t* bars, int r) {
+__device__ __forceinline__ void begin(JoinRows<T, WHOLE>& R, const JoinK& a, uint64_t* bars, int r, int before = 0) {
   const int groups = blockDim.x / a.tpr, g = threadIdx.x / a.tpr;  // rows go to all CTAs before a second group of any
-  R.base = join_smem + (size_t)g * a.ring * R.nbuf * a.slot;
+  R.base = join_smem + before + (size_t)g * a.ring * R.nbuf * a.slot;
   R.bars = bars + g * RING;
   R.first = (int64_t)g * gridDim.x + blockIdx.x;
   R.step = (int64_t)gridDim.x * groups;
@@ -131,19 +208,23 @@ __device__ __forceinline__ void weights_or(const float* w, const float* w2, floa
   }
 }
 
-template <typename T, bool WHOLE>
+// BRANCH: there is a y; FOLLOWING: there is an h.  (As run-time flags they cost
+// branches in every chunk of a row: the backward 371 us at 32768 x 4096 bf16, not 347.)
+template <typename T, bool WHOLE, bool BRANCH, bool FOLLOWING>
 __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
   constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2;
   __shared__ float scratch[2][2][16];
   __shared__ uint64_t bars[MAX_GROUPS * RING];
+  __shared__ __align__(16) uint4 zeros;
+  if (threadIdx.x == 0) zeros = make_uint4(0, 0, 0, 0);
   int turn = 0;
   const Group<false> grp(a.tpr);
   const int r = grp.r, nw = grp.warps, lane = threadIdx.x % 32;
-  const bool upper = lane >= 16, post = a.gamma_post != nullptr, following = a.gamma_next != nullptr, branch = a.y != nullptr;
-  JoinRows<T, WHOLE> R(a.x, a.y, nullptr, nullptr);
+  const bool upper = lane >= 16, post = BRANCH && a.gamma_post != nullptr;
+  JoinRows<T, WHOLE> R(a.x, BRANCH ? a.y : nullptr, nullptr, nullptr);
   constexpr int bx = 0, by_ = 1;
   begin<T, WHOLE>(R, a, bars, r);
-  const T *x = static_cast<const T*>(a.x), *y = static_cast<const T*>(a.y);
+  const Mine<T, WHOLE> mine(a, r, sm_addr(&zeros));
   const float inv = 1.f / (float)a.d;
   float2 ga[EPT / 2], gn[EPT / 2];
   weights_or<VN>(a.gamma_post, a.gate, a.bs, r, a.tpr, a.d, ga);
@@ -167,7 +248,7 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
 #pragma unroll
     for (int i = 0; i < EPT / 2 / CN; ++i) {
       float2 v[CN];
-      take<T, WHOLE>(R.place(R.at, by_), sp, y, r, a.tpr, a.d, i, v);
+      mine.get(R.place(R.at, 0), by_, sp, a.y, i, v);
 #pragma unroll
       for (int c = 0; c < CN; ++c) s = fma2(v[c], v[c], s);
     }
@@ -186,13 +267,13 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
     float2 o[EPT / 2 / CN][CN], s2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < EPT / 2 / CN; ++i) {
-      take<T, WHOLE>(R.place(R.at, bx), sp, x, r, a.tpr, a.d, i, o[i]);
+      mine.get(R.place(R.at, 0), bx, sp, a.x, i, o[i]);
       float2 v[CN];
-      if (branch) take<T, WHOLE>(R.place(R.at, by_), sp, y, r, a.tpr, a.d, i, v);
+      if (BRANCH) mine.get(R.place(R.at, 0), by_, sp, a.y, i, v);
 #pragma unroll
       for (int c = 0; c < CN; ++c) {
         o[i][c] = mul2(o[i][c], rs);
-        if (branch) o[i][c] = fma2(mul2(v[c], by), ga[i * CN + c], o[i][c]);
+        if (BRANCH) o[i][c] = fma2(mul2(v[c], by), ga[i * CN + c], o[i][c]);
         s2 = fma2(o[i][c], o[i][c], s2);
       }
     }
@@ -210,11 +291,11 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
     const float2 ro2 = both(ro);
 #pragma unroll
     for (int i = 0; i < EPT / 2 / CN; ++i) {
-      if (a.out) put<T, WHOLE>(static_cast<T*>(a.out) + row * a.d, r, a.tpr, a.d, i, o[i]);
-      if (following) {
+      if (a.out) mine.set(a.out, row, i, o[i]);
+      if (FOLLOWING) {
 #pragma unroll
         for (int c = 0; c < CN; ++c) o[i][c] = mul2(mul2(o[i][c], ro2), gn[i * CN + c]);
-        put<T, WHOLE>(static_cast<T*>(a.h) + row * a.d, r, a.tpr, a.d, i, o[i]);
+        mine.set(a.h, row, i, o[i]);
       }
     }
     if (r == 0) {
@@ -224,51 +305,64 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
   }
 }
 
-template <typename T, bool WHOLE>
+// Whole vectors: the columns' weights are in shared memory.  With the two sums,
+// D and y they are more than the 128 registers of 512 threads, and what is
+// spilled is waited for in every chunk (32768 x 4096 bf16: 411 us).
+template <typename T, bool WHOLE, bool BRANCH, bool FOLLOWING, bool DOUT>
 __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
   constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2, NC = EPT / 2 / CN;
   __shared__ float4 scratch[2 * 16];
   __shared__ uint64_t bars[MAX_GROUPS * RING];
+  __shared__ __align__(16) uint4 zeros;
+  if (threadIdx.x == 0) zeros = make_uint4(0, 0, 0, 0);
   const Group<true> grp(a.tpr);
   const int r = grp.r;
-  const bool post = a.gamma_post != nullptr, following = a.gamma_next != nullptr, branch = a.y != nullptr;
-  JoinRows<T, WHOLE> R(following ? a.dh : nullptr, following ? a.out : nullptr, a.dout, a.y);
-  constexpr int bh = 0, bo = 1;
-  const int bd = following ? 2 : 0, by_ = R.nbuf - 1;
-  begin<T, WHOLE>(R, a, bars, r);
-  const T *dh = static_cast<const T*>(a.dh), *out = static_cast<const T*>(a.out), *dout = static_cast<const T*>(a.dout);
-  const T* y = static_cast<const T*>(a.y);
+  const bool post = BRANCH && a.gamma_post != nullptr;
+  JoinRows<T, WHOLE> R(FOLLOWING ? a.dh : nullptr, FOLLOWING ? a.out : nullptr, DOUT ? a.dout : nullptr, BRANCH ? a.y : nullptr);
+  constexpr int bh = 0, bo = 1, bd = FOLLOWING ? 2 : 0, by_ = bd + DOUT;
+  const int wbytes = WHOLE ? EPT * a.tpr * 4 : 0;
+  begin<T, WHOLE>(R, a, bars, r, 2 * wbytes);
+  const Mine<T, WHOLE> mine(a, r, sm_addr(&zeros));
   const float inv = 1.f / (float)a.d;
-  float2 gn[EPT / 2], ga[EPT / 2], sn[EPT / 2], sm[EPT / 2];  // weights; the columns' sums of dh n and row_gate D m
-  weights_or<VN>(a.gamma_next, nullptr, 1.f, r, a.tpr, a.d, gn);
-  weights_or<VN>(a.gamma_post, a.gate, a.bs, r, a.tpr, a.d, ga);
+  float2 gn_r[WHOLE ? 1 : EPT / 2], ga_r[WHOLE ? 1 : EPT / 2];  // weights
+  float2 sn[EPT / 2], sm[EPT / 2];                              // the columns' sums of dh n and row_gate D m
+  const uint32_t gn_s = sm_addr(join_smem), ga_s = gn_s + wbytes;
+  if constexpr (WHOLE) {
+    mine.keep_weights(reinterpret_cast<float*>(join_smem), a.gamma_next, nullptr, 1.f);
+    mine.keep_weights(reinterpret_cast<float*>(join_smem + wbytes), a.gamma_post, a.gate, a.bs);
+    __syncthreads();
+  } else {
+    weights_or<VN>(a.gamma_next, nullptr, 1.f, r, a.tpr, a.d, gn_r);
+    weights_or<VN>(a.gamma_post, a.gate, a.bs, r, a.tpr, a.d, ga_r);
+  }
 #pragma unroll
   for (int c = 0; c < EPT / 2; ++c) sn[c] = sm[c] = both(0.f);
   // ro, ry and the gate of a row, loaded two rows ahead of their use
   auto stats = [&](int64_t row) {
     const bool in = row < a.rows;
-    return make_float3(in && following ? __ldg(a.rstd_next + row) : 0.f, in && post ? __ldg(a.rstd_post + row) : 1.f,
+    return make_float3(in && FOLLOWING ? __ldg(a.rstd_next + row) : 0.f, in && post ? __ldg(a.rstd_post + row) : 1.f,
                        in && a.row_gate ? __ldg(a.row_gate + row) : 1.f);
   };
   // the warp's sum of v n of the row at place R.at, and its part of the columns' sums
   auto along = [&](int64_t row, float ro) {
     R.wait(a.err);
-    if (!following) return 0.f;
+    if (!FOLLOWING) return 0.f;
     const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
     float2 s = both(0.f);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      float2 n[CN], v[CN];
-      take<T, WHOLE>(R.place(R.at, bo), sp, out, r, a.tpr, a.d, i, n);
-      take<T, WHOLE>(R.place(R.at, bh), sp, dh, r, a.tpr, a.d, i, v);
+      float2 n[CN], v[CN], gn[CN];
+      mine.weights(gn_s, gn_r, i, gn);
+      mine.get(R.place(R.at, 0), bo, sp, a.out, i, n);
+      mine.get(R.place(R.at, 0), bh, sp, a.dh, i, v);
 #pragma unroll
       for (int c = 0; c < CN; ++c) {  // past the row's end dh is 0
-        v[c] = mul2(mul2(n[c], both(ro)), v[c]);
-        sn[i * CN + c] = add2(sn[i * CN + c], v[c]);
-        s = fma2(v[c], gn[i * CN + c], s);
+        v[c] = mul2(n[c], v[c]);
+        sn[i * CN + c] = fma2(v[c], both(ro), sn[i * CN + c]);
+        s = fma2(v[c], gn[c], s);
       }
     }
-    return warp_sum(s.x + s.y);
+    return warp_sum(s.x + s.y) * ro;
   };
   const bool alone = grp.warps == 1;
   int turn = 0;
@@ -291,59 +385,61 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
   for (int64_t row = R.first; row < a.rows; row += R.step) {
     const float3 st2 = stats(row + 2 * R.step);
     const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
-    const float2 ro = both(st.x), ry = both(st.y), rg = both(st.z), k = both(-mvn * st.x);
-    float2 D[NC][CN], m[NC][CN], s = both(0.f);
+    const float2 ro = both(st.x), by = both(st.y * st.z), k = both(-mvn * st.x);
+    float2 D[NC][CN], y[NC][CN], s = both(0.f);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      if (dout != nullptr) {
-        take<T, WHOLE>(R.place(R.at, bd), sp, dout, r, a.tpr, a.d, i, D[i]);
+      if (DOUT) {
+        mine.get(R.place(R.at, 0), bd, sp, a.dout, i, D[i]);
       } else {
 #pragma unroll
         for (int c = 0; c < CN; ++c) D[i][c] = both(0.f);
       }
-      if (following) {
-        float2 n[CN], v[CN];
-        take<T, WHOLE>(R.place(R.at, bo), sp, out, r, a.tpr, a.d, i, n);
-        take<T, WHOLE>(R.place(R.at, bh), sp, dh, r, a.tpr, a.d, i, v);
+      if (FOLLOWING) {
+        float2 n[CN], v[CN], gn[CN];
+        mine.weights(gn_s, gn_r, i, gn);
+        mine.get(R.place(R.at, 0), bo, sp, a.out, i, n);
+        mine.get(R.place(R.at, 0), bh, sp, a.dh, i, v);
 #pragma unroll
-        for (int c = 0; c < CN; ++c)
-          D[i][c] = fma2(ro, fma2(v[c], gn[i * CN + c], mul2(n[c], k)), D[i][c]);
+        for (int c = 0; c < CN; ++c) D[i][c] = fma2(ro, fma2(v[c], gn[c], mul2(n[c], k)), D[i][c]);
       }
-      if (branch) {
-        take<T, WHOLE>(R.place(R.at, by_), sp, y, r, a.tpr, a.d, i, m[i]);
+      if (BRANCH) {
+        float2 ga[CN];
+        mine.weights(ga_s, ga_r, i, ga);
+        mine.get(R.place(R.at, 0), by_, sp, a.y, i, y[i]);
 #pragma unroll
-        for (int c = 0; c < CN; ++c) {
-          m[i][c] = mul2(m[i][c], ry);
-          const float2 t = mul2(D[i][c], m[i][c]);
-          sm[i * CN + c] = fma2(t, rg, sm[i * CN + c]);
-          s = fma2(t, ga[i * CN + c], s);
+        for (int c = 0; c < CN; ++c) {  // m = y ry
+          const float2 t = mul2(D[i][c], y[i][c]);
+          sm[i * CN + c] = fma2(t, by, sm[i * CN + c]);
+          s = fma2(t, ga[c], s);
         }
       }
     }
     const int place = R.at;
     float ahead = 0.f;
     R.next();
-    const float mine = branch ? warp_sum(s.x + s.y) : 0.f;
+    const float own = BRANCH ? warp_sum(s.x + s.y) * st.y : 0.f;
     if (row + R.step < a.rows) ahead = along(row + R.step, st1.x);
-    const float2 t = sums(mine, ahead);
+    const float2 t = sums(own, ahead);
     if (r == 0) {
       R.start(row + R.ring * R.step, place);  // everyone has read the row
       if (a.drow_gate) a.drow_gate[row] = t.x;
     }
     mvn = t.y * inv;
-    const float2 rs = both(a.rs), mwm = both(post ? -t.x * st.z * inv : 0.f);
+    const float2 rs = both(a.rs), ky = both(post ? -t.x * st.z * inv * st.y * st.y : 0.f);  // of y in dy
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-      if (branch) {
+      if (BRANCH) {
+        float2 ga[CN];
+        mine.weights(ga_s, ga_r, i, ga);
 #pragma unroll
-        for (int c = 0; c < CN; ++c)
-          m[i][c] = mul2(fma2(mul2(D[i][c], rg), ga[i * CN + c], mul2(m[i][c], mwm)), ry);
-        put<T, WHOLE>(static_cast<T*>(a.dy) + row * a.d, r, a.tpr, a.d, i, m[i]);
+        for (int c = 0; c < CN; ++c) y[i][c] = fma2(mul2(D[i][c], ga[c]), by, mul2(y[i][c], ky));
+        mine.set(a.dy, row, i, y[i]);
       }
       if (a.dx) {
 #pragma unroll
         for (int c = 0; c < CN; ++c) D[i][c] = mul2(D[i][c], rs);
-        put<T, WHOLE>(static_cast<T*>(a.dx) + row * a.d, r, a.tpr, a.d, i, D[i]);
+        mine.set(a.dx, row, i, D[i]);
       }
     }
     st = st1;
@@ -353,13 +449,13 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
   // the CTA's sums, over its groups in order, are one row pair of the partials
   const int groups = blockDim.x / a.tpr;
   float* dst = a.partial + (size_t)blockIdx.x * 2 * a.d;
-  float* own = groups == 1 ? dst : reinterpret_cast<float*>(join_smem) + (size_t)grp.g * 2 * a.d;
+  float* sums_at = groups == 1 ? dst : reinterpret_cast<float*>(join_smem) + (size_t)grp.g * 2 * a.d;
 #pragma unroll
   for (int c = 0; c < EPT; ++c) {
     const int col = column<VN>(r, a.tpr, c);
     if (in_row<VN>(r, a.tpr, c, a.d)) {
-      own[col] = c & 1 ? sn[c / 2].y : sn[c / 2].x;
-      own[a.d + col] = c & 1 ? sm[c / 2].y : sm[c / 2].x;
+      sums_at[col] = c & 1 ? sn[c / 2].y : sn[c / 2].x;
+      sums_at[a.d + col] = c & 1 ? sm[c / 2].y : sm[c / 2].x;
     }
   }
   if (groups == 1) return;
@@ -680,13 +776,14 @@ Grid grid_of(int64_t rows, int d, int es, int bufs, bool bwd) {
   if (d > MAX_TPR * EPT) return g;
   g.tpr = threads_per_row(d);
   g.slot = (d * es + 15) / 16 * 16 + (d * es % 16 ? 16 : 0);
-  const size_t place = (size_t)bufs * g.slot;
+  const size_t place = (size_t)bufs * g.slot, weights = bwd && d * es % 16 == 0 ? 2 * EPT * g.tpr * 4 : 0;
   int groups = bwd ? BWD_NT / g.tpr : (g.tpr == 32 ? 4 : 1), per = bwd ? 1 : 65536 / (g.tpr * groups * FWD_REGS);
-  while (bwd && groups > 1 && groups * 3 * place > SMEM_SM - 1024) groups /= 2;
-  while (per > 1 && per * 2 * (groups * place + 1024) > SMEM_SM) --per;
-  g.ring = (int)std::min<size_t>(RING, (SMEM_SM / per - 1024) / (groups * place));
+  const size_t room = bwd ? BWD_SMEM - weights : SMEM_SM;
+  while (bwd && groups > 1 && groups * 3 * place > room) groups /= 2;
+  while (per > 1 && per * 2 * (groups * place + 1024) > room) --per;
+  g.ring = (int)std::min<size_t>(RING, (bwd ? room : SMEM_SM / per - 1024) / (groups * place));
   g.threads = g.tpr * groups;
-  g.smem = g.ring * groups * place;
+  g.smem = weights + g.ring * groups * place;
   const size_t sums = groups > 1 ? (size_t)groups * 2 * d * 4 : 0;  // the backward's groups' sums take the ring's place
   if (bwd && g.smem < sums) g.smem = sums;
   const int64_t need = bwd ? rows : (rows + groups - 1) / groups;
@@ -700,7 +797,7 @@ cudaError_t launch_ring(K kernel, const Grid& g, JoinK& a, bool* attr_done, cuda
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
   if (!attr_done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_SM);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, std::max(SMEM_SM, BWD_SMEM));
     if (e != cudaSuccess) return e;
     attr_done[dev] = true;
   }
@@ -710,20 +807,32 @@ cudaError_t launch_ring(K kernel, const Grid& g, JoinK& a, bool* attr_done, cuda
   a.parts = g.ctas;
   return launch_pdl(kernel, dim3(g.ctas), dim3(g.threads), g.smem, st, a);
 }
+template <typename T, bool WHOLE, bool BRANCH, bool FOLLOWING>
+cudaError_t fwd_ring(const Grid& g, JoinK& a, cudaStream_t st) {
+  static bool done[64] = {false};
+  return launch_ring(join_fwd_kernel<T, WHOLE, BRANCH, FOLLOWING>, g, a, done, st);
+}
+template <typename T, bool WHOLE, bool BRANCH, bool FOLLOWING, bool DOUT>
+cudaError_t bwd_ring(const Grid& g, JoinK& a, cudaStream_t st) {
+  static bool done[64] = {false};
+  return launch_ring(join_bwd_kernel<T, WHOLE, BRANCH, FOLLOWING, DOUT>, g, a, done, st);
+}
 template <typename T, bool WHOLE>
 cudaError_t fwd_w(JoinK& a, cudaStream_t st) {
-  static bool done[64] = {false};
   const Grid g = grid_of(a.rows, a.d, sizeof(T), a.y ? 2 : 1, false);
   if (g.ring < 2) return fwd_wide<T, WHOLE ? Vec<T>::N : 1>(a, st);
-  return launch_ring(join_fwd_kernel<T, WHOLE>, g, a, done, st);
+  if (!a.y) return a.gamma_next ? fwd_ring<T, WHOLE, false, true>(g, a, st) : fwd_ring<T, WHOLE, false, false>(g, a, st);
+  return a.gamma_next ? fwd_ring<T, WHOLE, true, true>(g, a, st) : fwd_ring<T, WHOLE, true, false>(g, a, st);
 }
 template <typename T, bool WHOLE>
 cudaError_t bwd_w(JoinK& a, cudaStream_t st) {
-  static bool done[64] = {false};
   const int bufs = (a.gamma_next ? 2 : 0) + (a.dout ? 1 : 0) + (a.y ? 1 : 0);
   const Grid g = grid_of(a.rows, a.d, sizeof(T), bufs, true);
   if (g.ring < 2) return bwd_wide<T, WHOLE ? Vec<T>::N : 1>(a, st);
-  return launch_ring(join_bwd_kernel<T, WHOLE>, g, a, done, st);
+  if (!a.gamma_next)  // dout is there then
+    return a.y ? bwd_ring<T, WHOLE, true, false, true>(g, a, st) : bwd_ring<T, WHOLE, false, false, true>(g, a, st);
+  if (a.y) return a.dout ? bwd_ring<T, WHOLE, true, true, true>(g, a, st) : bwd_ring<T, WHOLE, true, true, false>(g, a, st);
+  return a.dout ? bwd_ring<T, WHOLE, false, true, true>(g, a, st) : bwd_ring<T, WHOLE, false, true, false>(g, a, st);
 }
 template <typename T>
 cudaError_t fwd_t(JoinK& a, cudaStream_t st) {
