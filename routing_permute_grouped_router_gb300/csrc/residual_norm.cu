@@ -94,73 +94,83 @@ struct JoinRows {
 
 extern __shared__ __align__(128) char join_smem[];
 
-// A thread's chunks of rows in the ring.  Whole vectors: their offsets are the
-// same in every row, and one past the row's end is read from 16 bytes of zeros,
-// which leaves a load a chunk and no branch.  (A checked load each and addresses
-// of 64 bits: the backward 347 us at 32768 x 4096 bf16.)
+// A thread's chunks of rows in the ring: 16-byte units of the tensor, of which
+// the first and the last may hold elements of the rows around.  A CTA's rows are
+// a multiple of VN apart, so they all begin as many elements, `skip`, into their
+// first unit, and a thread has the same columns in each (rows that are whole
+// units, WHOLE, have no skip).  What is past the row's end is read from 16 bytes
+// of zeros: a load a chunk and no branch.
 template <typename T, bool WHOLE>
 struct Mine {
-  static constexpr int CN = Chunk<T, WHOLE>::N / 2, NC = EPT / 2 / CN;
-  int r, tpr, d, slot;
-  uint32_t zeros, off[WHOLE ? NC : 1];
-  bool in[WHOLE ? NC : 1];
-  __device__ __forceinline__ Mine(const JoinK& a, int r_, uint32_t zeros_) : r(r_), tpr(a.tpr), d(a.d), slot(a.slot), zeros(zeros_) {
-    if constexpr (WHOLE) {
+  static constexpr int VN = Vec<T>::N, CN = VN / 2, NC = EPT / VN;
+  int r, tpr, d, slot, skip;
+  uint32_t zeros, off[NC];
+  bool in[NC], edge[NC];  // the chunk has elements of the row; and others
+  __device__ __forceinline__ Mine(const JoinK& a, int r_, uint32_t zeros_)
+      : r(r_), tpr(a.tpr), d(a.d), slot(a.slot), skip(WHOLE ? 0 : (int)((int64_t)blockIdx.x * a.d % VN)), zeros(zeros_) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        off[i] = (r + i * tpr) * 16;
-        in[i] = (r + i * tpr) * Vec<T>::N < d;
-      }
+    for (int i = 0; i < NC; ++i) {
+      off[i] = (r + i * tpr) * 16;
+      in[i] = column(i) < d;
+      edge[i] = !WHOLE && in[i] && (column(i) < 0 || column(i) + VN > d);
     }
   }
-  // chunk i of tensor b of the place at `at`; `tensor` is where its rows are (whose last one a copy may cut off)
+  // of the chunk's first element; the elements of the row are 0 to d - 1
+  __device__ __forceinline__ int column(int i) const { return (r + i * tpr) * VN - skip; }
+  // chunk i of tensor b of the place at `at`; `tensor` is where its rows are, whose last unit a copy cuts off
   __device__ __forceinline__ void get(const char* at, int b, const Span& sp, const void* tensor, int i, float2 (&v)[CN]) const {
-    if constexpr (WHOLE) {
-      const uint4 u = lds(in[i] ? sm_addr(at) + b * slot + off[i] : zeros);
-      float w[2 * CN];
-      unpack(u, w);
+    float w[VN];
+    unpack(lds(in[i] ? sm_addr(at) + b * slot + off[i] : zeros), w);
+    if (!WHOLE && edge[i]) {
+      const bool cut = (int)off[i] + 16 > sp.bytes;
+      const T* p = static_cast<const T*>(tensor) + (sp.at + off[i]) / (int64_t)sizeof(T);
 #pragma unroll
-      for (int c = 0; c < CN; ++c) v[c] = make_float2(w[2 * c], w[2 * c + 1]);
-    } else {
-      take<T, WHOLE>(at + b * slot, sp, static_cast<const T*>(tensor), r, tpr, d, i, v);
-    }
-  }
-  __device__ __forceinline__ void set(void* tensor, int64_t row, int i, const float2 (&v)[CN]) const {
-    if constexpr (WHOLE) {
-      float w[2 * CN];
-#pragma unroll
-      for (int c = 0; c < CN; ++c) {
-        w[2 * c] = v[c].x;
-        w[2 * c + 1] = v[c].y;
+      for (int j = 0; j < VN; ++j) {
+        const bool own = column(i) + j >= 0 && column(i) + j < d;
+        if (cut && own) w[j] = to_f32(p[j]);
+        if (!own) w[j] = 0.f;
       }
-      if (in[i]) stg16(static_cast<char*>(tensor) + row * d * (int64_t)sizeof(T) + off[i], pack(w));
-    } else {
-      put<T, WHOLE>(static_cast<T*>(tensor) + row * d, r, tpr, d, i, v);
+    }
+#pragma unroll
+    for (int c = 0; c < CN; ++c) v[c] = make_float2(w[2 * c], w[2 * c + 1]);
+  }
+  __device__ __forceinline__ void set(void* tensor, const Span& sp, int i, const float2 (&v)[CN]) const {
+    float w[VN];
+#pragma unroll
+    for (int c = 0; c < CN; ++c) {
+      w[2 * c] = v[c].x;
+      w[2 * c + 1] = v[c].y;
+    }
+    char* to = static_cast<char*>(tensor) + sp.at + off[i];
+    if (!WHOLE && edge[i]) {
+#pragma unroll
+      for (int j = 0; j < VN; ++j)
+        if (column(i) + j >= 0 && column(i) + j < d) reinterpret_cast<T*>(to)[j] = from_f32<T>(w[j]);
+    } else if (in[i]) {
+      stg16(to, pack(w));
     }
   }
-  // a columns' weight in shared memory, 16 bytes of a chunk at a time so that neighbouring lanes read neighbouring ones
+  // the columns' weights times `by`, `by` where there are none; 0 outside the row
+  __device__ __forceinline__ float weight(const float* p, const float* p2, float by, int col) const {
+    return col < 0 || col >= d ? 0.f : by * (p ? __ldg(p + col) : 1.f) * (p2 ? __ldg(p2 + col) : 1.f);
+  }
+  __device__ __forceinline__ void take_weights(const float* p, const float* p2, float by, float2 (&v)[EPT / 2]) const {
+#pragma unroll
+    for (int c = 0; c < EPT; ++c) (c & 1 ? v[c / 2].y : v[c / 2].x) = weight(p, p2, by, column(c / VN) + c % VN);
+  }
+  // the same in shared memory, 16 bytes of a chunk at a time so that neighbouring lanes read neighbouring ones
+  __device__ __forceinline__ void keep_weights(float* w, const float* p, const float* p2, float by) const {
+    for (int c = threadIdx.x; c < EPT * tpr; c += blockDim.x) {
+      const int q = c / VN, j = c % VN;
+      w[(j / 4 * NC * tpr + q) * 4 + j % 4] = weight(p, p2, by, c - skip);
+    }
+  }
   __device__ __forceinline__ void weights(uint32_t w, int i, float2 (&v)[CN]) const {
 #pragma unroll
     for (int j = 0; j < CN / 2; ++j) {
-      const uint4 u = lds(w + j * (NC * tpr * 16) + (r + i * tpr) * 16);
+      const uint4 u = lds(w + j * (NC * tpr * 16) + off[i]);
       v[2 * j] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
       v[2 * j + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
-    }
-  }
-  // the same where whole vectors are not, from registers
-  template <int N>
-  __device__ __forceinline__ void weights(uint32_t w, const float2 (&regs)[N], int i, float2 (&v)[CN]) const {
-    if constexpr (WHOLE) {
-      weights(w, i, v);
-    } else {
-#pragma unroll
-      for (int c = 0; c < CN; ++c) v[c] = regs[i * CN + c];
-    }
-  }
-  __device__ __forceinline__ void keep_weights(float* w, const float* p, const float* p2, float by) const {
-    for (int c = threadIdx.x; c < EPT * tpr; c += blockDim.x) {
-      const int q = c / (2 * CN), j = c % (2 * CN);
-      w[(j / 4 * NC * tpr + q) * 4 + j % 4] = c < d ? by * (p ? __ldg(p + c) : 1.f) * (p2 ? __ldg(p2 + c) : 1.f) : 0.f;
     }
   }
   __device__ __forceinline__ static uint4 lds(uint32_t addr) {
@@ -193,26 +203,11 @@ __device__ __forceinline__ void begin(JoinRows<T, WHOLE>& R, const JoinK& a, uin
     for (int i = 0; i < a.ring; ++i) R.start(R.first + i * R.step, i);
 }
 
-// The columns' weights times `by` in pairs, `by` where there are none; 0 past the row's end.
-template <int VN>
-__device__ __forceinline__ void weights_or(const float* w, const float* w2, float by, int r, int tpr, int d,
-                                           float2 (&v)[EPT / 2]) {
-#pragma unroll
-  for (int c = 0; c < EPT; ++c) {
-    float u = 0.f;
-    if (in_row<VN>(r, tpr, c, d)) {
-      const int i = column<VN>(r, tpr, c);
-      u = by * (w ? __ldg(w + i) : 1.f) * (w2 ? __ldg(w2 + i) : 1.f);
-    }
-    (c & 1 ? v[c / 2].y : v[c / 2].x) = u;
-  }
-}
-
 // BRANCH: there is a y; FOLLOWING: there is an h.  (As run-time flags they cost
 // branches in every chunk of a row: the backward 371 us at 32768 x 4096 bf16, not 347.)
 template <typename T, bool WHOLE, bool BRANCH, bool FOLLOWING>
 __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
-  constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2;
+  constexpr int CN = Mine<T, WHOLE>::CN;
   __shared__ float scratch[2][2][16];
   __shared__ uint64_t bars[MAX_GROUPS * RING];
   __shared__ __align__(16) uint4 zeros;
@@ -227,8 +222,8 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
   const Mine<T, WHOLE> mine(a, r, sm_addr(&zeros));
   const float inv = 1.f / (float)a.d;
   float2 ga[EPT / 2], gn[EPT / 2];
-  weights_or<VN>(a.gamma_post, a.gate, a.bs, r, a.tpr, a.d, ga);
-  weights_or<VN>(a.gamma_next, nullptr, 1.f, r, a.tpr, a.d, gn);
+  mine.take_weights(a.gamma_post, a.gate, a.bs, ga);
+  mine.take_weights(a.gamma_next, nullptr, 1.f, gn);
   // both sums over the group, the first in the lower half of the lanes
   auto sums = [&](float u, float v) {
     float m = half_sums(u, v, upper);
@@ -291,11 +286,11 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
     const float2 ro2 = both(ro);
 #pragma unroll
     for (int i = 0; i < EPT / 2 / CN; ++i) {
-      if (a.out) mine.set(a.out, row, i, o[i]);
+      if (a.out) mine.set(a.out, sp, i, o[i]);
       if (FOLLOWING) {
 #pragma unroll
         for (int c = 0; c < CN; ++c) o[i][c] = mul2(mul2(o[i][c], ro2), gn[i * CN + c]);
-        mine.set(a.h, row, i, o[i]);
+        mine.set(a.h, sp, i, o[i]);
       }
     }
     if (r == 0) {
@@ -305,12 +300,12 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
   }
 }
 
-// Whole vectors: the columns' weights are in shared memory.  With the two sums,
+// The columns' weights are in shared memory.  With the two sums,
 // D and y they are more than the 128 registers of 512 threads, and what is
 // spilled is waited for in every chunk (32768 x 4096 bf16: 411 us).
 template <typename T, bool WHOLE, bool BRANCH, bool FOLLOWING, bool DOUT>
 __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
-  constexpr int VN = WHOLE ? Vec<T>::N : 1, CN = Chunk<T, WHOLE>::N / 2, NC = EPT / 2 / CN;
+  constexpr int VN = Vec<T>::N, CN = Mine<T, WHOLE>::CN, NC = EPT / VN;
   __shared__ float4 scratch[2 * 16];
   __shared__ uint64_t bars[MAX_GROUPS * RING];
   __shared__ __align__(16) uint4 zeros;
@@ -320,21 +315,15 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
   const bool post = BRANCH && a.gamma_post != nullptr;
   JoinRows<T, WHOLE> R(FOLLOWING ? a.dh : nullptr, FOLLOWING ? a.out : nullptr, DOUT ? a.dout : nullptr, BRANCH ? a.y : nullptr);
   constexpr int bh = 0, bo = 1, bd = FOLLOWING ? 2 : 0, by_ = bd + DOUT;
-  const int wbytes = WHOLE ? EPT * a.tpr * 4 : 0;
+  const int wbytes = EPT * a.tpr * 4;
   begin<T, WHOLE>(R, a, bars, r, 2 * wbytes);
   const Mine<T, WHOLE> mine(a, r, sm_addr(&zeros));
   const float inv = 1.f / (float)a.d;
-  float2 gn_r[WHOLE ? 1 : EPT / 2], ga_r[WHOLE ? 1 : EPT / 2];  // weights
-  float2 sn[EPT / 2], sm[EPT / 2];                              // the columns' sums of dh n and row_gate D m
-  const uint32_t gn_s = sm_addr(join_smem), ga_s = gn_s + wbytes;
-  if constexpr (WHOLE) {
-    mine.keep_weights(reinterpret_cast<float*>(join_smem), a.gamma_next, nullptr, 1.f);
-    mine.keep_weights(reinterpret_cast<float*>(join_smem + wbytes), a.gamma_post, a.gate, a.bs);
-    __syncthreads();
-  } else {
-    weights_or<VN>(a.gamma_next, nullptr, 1.f, r, a.tpr, a.d, gn_r);
-    weights_or<VN>(a.gamma_post, a.gate, a.bs, r, a.tpr, a.d, ga_r);
-  }
+  const uint32_t gn_s = sm_addr(join_smem), ga_s = gn_s + wbytes;  // weights
+  mine.keep_weights(reinterpret_cast<float*>(join_smem), a.gamma_next, nullptr, 1.f);
+  mine.keep_weights(reinterpret_cast<float*>(join_smem + wbytes), a.gamma_post, a.gate, a.bs);
+  __syncthreads();
+  float2 sn[EPT / 2], sm[EPT / 2];  // the columns' sums of dh n and row_gate D m
 #pragma unroll
   for (int c = 0; c < EPT / 2; ++c) sn[c] = sm[c] = both(0.f);
   // ro, ry and the gate of a row, loaded two rows ahead of their use
@@ -352,7 +341,7 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       float2 n[CN], v[CN], gn[CN];
-      mine.weights(gn_s, gn_r, i, gn);
+      mine.weights(gn_s, i, gn);
       mine.get(R.place(R.at, 0), bo, sp, a.out, i, n);
       mine.get(R.place(R.at, 0), bh, sp, a.dh, i, v);
 #pragma unroll
@@ -397,7 +386,7 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
       }
       if (FOLLOWING) {
         float2 n[CN], v[CN], gn[CN];
-        mine.weights(gn_s, gn_r, i, gn);
+        mine.weights(gn_s, i, gn);
         mine.get(R.place(R.at, 0), bo, sp, a.out, i, n);
         mine.get(R.place(R.at, 0), bh, sp, a.dh, i, v);
 #pragma unroll
@@ -405,7 +394,7 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
       }
       if (BRANCH) {
         float2 ga[CN];
-        mine.weights(ga_s, ga_r, i, ga);
+        mine.weights(ga_s, i, ga);
         mine.get(R.place(R.at, 0), by_, sp, a.y, i, y[i]);
 #pragma unroll
         for (int c = 0; c < CN; ++c) {  // m = y ry
@@ -431,15 +420,15 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
     for (int i = 0; i < NC; ++i) {
       if (BRANCH) {
         float2 ga[CN];
-        mine.weights(ga_s, ga_r, i, ga);
+        mine.weights(ga_s, i, ga);
 #pragma unroll
         for (int c = 0; c < CN; ++c) y[i][c] = fma2(mul2(D[i][c], ga[c]), by, mul2(y[i][c], ky));
-        mine.set(a.dy, row, i, y[i]);
+        mine.set(a.dy, sp, i, y[i]);
       }
       if (a.dx) {
 #pragma unroll
         for (int c = 0; c < CN; ++c) D[i][c] = mul2(D[i][c], rs);
-        mine.set(a.dx, row, i, D[i]);
+        mine.set(a.dx, sp, i, D[i]);
       }
     }
     st = st1;
@@ -452,8 +441,8 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
   float* sums_at = groups == 1 ? dst : reinterpret_cast<float*>(join_smem) + (size_t)grp.g * 2 * a.d;
 #pragma unroll
   for (int c = 0; c < EPT; ++c) {
-    const int col = column<VN>(r, a.tpr, c);
-    if (in_row<VN>(r, a.tpr, c, a.d)) {
+    const int col = mine.column(c / VN) + c % VN;
+    if (col >= 0 && col < a.d) {
       sums_at[col] = c & 1 ? sn[c / 2].y : sn[c / 2].x;
       sums_at[a.d + col] = c & 1 ? sm[c / 2].y : sm[c / 2].x;
     }
@@ -773,10 +762,12 @@ struct Grid {
 };
 Grid grid_of(int64_t rows, int d, int es, int bufs, bool bwd) {
   Grid g{};
-  if (d > MAX_TPR * EPT) return g;
-  g.tpr = threads_per_row(d);
-  g.slot = (d * es + 15) / 16 * 16 + (d * es % 16 ? 16 : 0);
-  const size_t place = (size_t)bufs * g.slot, weights = bwd && d * es % 16 == 0 ? 2 * EPT * g.tpr * 4 : 0;
+  const bool whole = d * es % 16 == 0;
+  const int most_units = whole ? d * es / 16 : (d * es + 15 + 16 - es) / 16;  // of a row
+  if (most_units * 16 > MAX_TPR * EPT * es) return g;
+  g.tpr = threads_per_row(most_units * 16 / es);
+  g.slot = most_units * 16;
+  const size_t place = (size_t)bufs * g.slot, weights = bwd ? 2 * EPT * g.tpr * 4 : 0;
   int groups = bwd ? BWD_NT / g.tpr : (g.tpr == 32 ? 4 : 1), per = bwd ? 1 : 65536 / (g.tpr * groups * FWD_REGS);
   const size_t room = bwd ? BWD_SMEM - weights : SMEM_SM;
   while (bwd && groups > 1 && groups * 3 * place > room) groups /= 2;
@@ -788,6 +779,8 @@ Grid grid_of(int64_t rows, int d, int es, int bufs, bool bwd) {
   if (bwd && g.smem < sums) g.smem = sums;
   const int64_t need = bwd ? rows : (rows + groups - 1) / groups;
   g.ctas = (int)std::min<int64_t>(need, (int64_t)sm_count() * per);
+  // the rows of a CTA are as many CTAs apart, and begin alike in their first units: a multiple of a unit's elements
+  if (!whole) g.ctas = g.ctas < 8 ? 8 : std::min(g.ctas + 7, sm_count() * per) / 8 * 8;
   return g;
 }
 
@@ -843,7 +836,7 @@ cudaError_t bwd_t(JoinK& a, cudaStream_t st) {
   return a.d % Vec<T>::N == 0 ? bwd_w<T, true>(a, st) : bwd_w<T, false>(a, st);
 }
 size_t partial_bytes(int64_t rows, int d) {
-  return (size_t)std::max<int64_t>(wide_slices(rows, d), std::min<int64_t>(rows, sm_count())) * 2 * d * 4;
+  return (size_t)std::max<int64_t>(wide_slices(rows, d), std::min<int64_t>(rows + 7, std::max(sm_count(), 8))) * 2 * d * 4;
 }
 
 }  // namespace
