@@ -94,6 +94,19 @@ struct JoinRows {
 
 extern __shared__ __align__(128) char join_smem[];
 
+// The elements of a row in the unit at p, whose first one is the row's c-th, where a copy has cut the unit off.
+template <typename T>
+__device__ __noinline__ uint4 load_cut(const T* p, int c, int d) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < Vec<T>::N; ++j)
+    if (c + j >= 0 && c + j < d) {
+      if constexpr (sizeof(T) == 2) w[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + j) << (j % 2 * 16);
+      else w[j] = *reinterpret_cast<const uint32_t*>(p + j);
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A thread's chunks of rows in the ring: 16-byte units of the tensor, of which
 // the first and the last may hold elements of the rows around.  A CTA's rows are
 // a multiple of VN apart, so they all begin as many elements, `skip`, into their
@@ -119,20 +132,26 @@ struct Mine {
   __device__ __forceinline__ int column(int i) const { return (r + i * tpr) * VN - skip; }
   // chunk i of tensor b of the place at `at`; `tensor` is where its rows are, whose last unit a copy cuts off
   __device__ __forceinline__ void get(const char* at, int b, const Span& sp, const void* tensor, int i, float2 (&v)[CN]) const {
+    uint4 u = lds(in[i] ? sm_addr(at) + b * slot + off[i] : zeros);
+    if (!WHOLE && edge[i]) u = trim(u, sp, tensor, i);
     float w[VN];
-    unpack(lds(in[i] ? sm_addr(at) + b * slot + off[i] : zeros), w);
-    if (!WHOLE && edge[i]) {
-      const bool cut = (int)off[i] + 16 > sp.bytes;
-      const T* p = static_cast<const T*>(tensor) + (sp.at + off[i]) / (int64_t)sizeof(T);
-#pragma unroll
-      for (int j = 0; j < VN; ++j) {
-        const bool own = column(i) + j >= 0 && column(i) + j < d;
-        if (cut && own) w[j] = to_f32(p[j]);
-        if (!own) w[j] = 0.f;
-      }
-    }
+    unpack(u, w);
 #pragma unroll
     for (int c = 0; c < CN; ++c) v[c] = make_float2(w[2 * c], w[2 * c + 1]);
+  }
+  // the row's elements of a unit, zeros for the others: a mask of its bits from lo to hi
+  __device__ __forceinline__ uint4 trim(uint4 u, const Span& sp, const void* tensor, int i) const {
+    const int c = column(i), lo = c < 0 ? -c * 8 * (int)sizeof(T) : 0, hi = c + VN > d ? (d - c) * 8 * (int)sizeof(T) : 128;
+    if ((int)off[i] + 16 > sp.bytes) u = load_cut(static_cast<const T*>(tensor) + (sp.at + off[i]) / (int64_t)sizeof(T), c, d);
+    uint64_t m0 = lo < 64 ? ~0ull << lo : 0ull, m1 = lo < 64 ? ~0ull : ~0ull << (lo - 64);
+    if (hi <= 64) m1 = 0ull;
+    else if (hi < 128) m1 &= (1ull << (hi - 64)) - 1;
+    if (hi < 64) m0 &= (1ull << hi) - 1;
+    u.x &= (uint32_t)m0;
+    u.y &= (uint32_t)(m0 >> 32);
+    u.z &= (uint32_t)m1;
+    u.w &= (uint32_t)(m1 >> 32);
+    return u;
   }
   __device__ __forceinline__ void set(void* tensor, const Span& sp, int i, const float2 (&v)[CN]) const {
     float w[VN];
@@ -755,7 +774,7 @@ cudaError_t bwd_wide(JoinK& a, cudaStream_t st) {
 // Sizes of a launch over rows in the ring of `bufs` tensors.  Forward: CTAs of one
 // group of threads, or of four warps with rows of their own, as many as the
 // registers allow.  Backward: one CTA an SM, of as many groups as leave the ring
-// three places.  ring < 2: no room, the wide kernels.
+// two places (three: 46 us at 4099 x 1021 float32, not 40).  ring < 2: no room, the wide kernels.
 struct Grid {
   int threads, ctas, tpr, slot, ring;
   size_t smem;
@@ -770,7 +789,7 @@ Grid grid_of(int64_t rows, int d, int es, int bufs, bool bwd) {
   const size_t place = (size_t)bufs * g.slot, weights = bwd ? 2 * EPT * g.tpr * 4 : 0;
   int groups = bwd ? BWD_NT / g.tpr : (g.tpr == 32 ? 4 : 1), per = bwd ? 1 : 65536 / (g.tpr * groups * FWD_REGS);
   const size_t room = bwd ? BWD_SMEM - weights : SMEM_SM;
-  while (bwd && groups > 1 && groups * 3 * place > room) groups /= 2;
+  if (bwd) groups = std::max(1, std::min(groups, (int)(room / (2 * place))));
   while (per > 1 && per * 2 * (groups * place + 1024) > room) --per;
   g.ring = (int)std::min<size_t>(RING, (bwd ? room : SMEM_SM / per - 1024) / (groups * place));
   g.threads = g.tpr * groups;
