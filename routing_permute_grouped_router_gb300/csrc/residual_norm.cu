@@ -69,7 +69,7 @@ struct JoinRows {
     const uint32_t bar = sm_addr(bars + p);
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(sp.bytes * nbuf) : "memory");
     if (sp.bytes <= 0) return;
-    uint32_t to = sm_addr(place(p, 0));
+    uint32_t to = sm_addr(place(p, sp));
     auto copy = [&](const void* t) {
       if (t == nullptr) return;
       copy_row(to, static_cast<const char*>(t) + sp.at, sp.bytes, bar);
@@ -83,7 +83,10 @@ struct JoinRows {
   __device__ __forceinline__ void wait(uint32_t* err) const {
     if (!ring_ready(sm_addr(bars + at), phase)) ring_wait(sm_addr(bars + at), phase, err);
   }
-  __device__ __forceinline__ char* place(int p, int b) const { return base + (size_t)(p * nbuf + b) * slot; }
+  // of the first tensor's row: as far into a 128-byte line as it is in memory
+  __device__ __forceinline__ char* place(int p, const Span& sp) const {
+    return base + (size_t)(p * nbuf) * slot + (WHOLE ? 0 : (int)(sp.at & 112));
+  }
   __device__ __forceinline__ void next() {
     if (++at == ring) {
       at = 0;
@@ -94,17 +97,58 @@ struct JoinRows {
 
 extern __shared__ __align__(128) char join_smem[];
 
-// The elements of a row in the unit at p, whose first one is the row's c-th, where a copy has cut the unit off.
+// The ends of rows that are no whole units, in functions of their own: they are
+// few, and as part of the kernels their registers and branches slow every row
+// (32768 x 1007 bf16 backward: 143 us).
+//
+// Zeros for the elements of other rows in a unit of nbuf tensors in shared
+// memory, `slot` apart; c is the unit's first element in the row of d.
+template <int ES>
+__device__ __noinline__ void trim_unit(uint32_t at, int slot, int nbuf, int c, int d) {
+  constexpr int VN = 16 / ES;
+  const int lo = c < 0 ? -c * 8 * ES : 0, hi = c + VN > d ? (d - c) * 8 * ES : 128;  // the row's bits
+  uint64_t m0 = lo < 64 ? ~0ull << lo : 0ull, m1 = lo < 64 ? ~0ull : ~0ull << (lo - 64);
+  if (hi <= 64) m1 = 0ull;
+  else if (hi < 128) m1 &= (1ull << (hi - 64)) - 1;
+  if (hi < 64) m0 &= (1ull << hi) - 1;
+  for (int b = 0; b < nbuf; ++b, at += slot)
+    asm volatile(
+        "{\n\t.reg .b64 x, y;\n\tld.shared.v2.b64 {x, y}, [%0];\n\tand.b64 x, x, %1;\n\tand.b64 y, y, %2;\n\t"
+        "st.shared.v2.b64 [%0], {x, y};\n\t}" ::"r"(at), "l"(m0), "l"(m1)
+        : "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a copy will write there again
+}
+// The same for a unit that the copy has cut off at the tensors' end: from memory, `byte` bytes into the tensors.
 template <typename T>
-__device__ __noinline__ uint4 load_cut(const T* p, int c, int d) {
-  uint32_t w[4] = {0, 0, 0, 0};
+__device__ __noinline__ void load_cut(const void* t0, const void* t1, const void* t2, const void* t3, int64_t byte,
+                                      uint32_t at, int slot, int c, int d) {
+  const void* t[4] = {t0, t1, t2, t3};
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    if (t[b] == nullptr) continue;
+    const T* p = reinterpret_cast<const T*>(static_cast<const char*>(t[b]) + byte);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j)
+      if (c + j >= 0 && c + j < d) {
+        if constexpr (sizeof(T) == 2) w[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + j) << (j % 2 * 16);
+        else w[j] = *reinterpret_cast<const uint32_t*>(p + j);
+      }
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    at += slot;
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// The row's elements of a unit to memory.
+template <typename T>
+__device__ __noinline__ void store_edge(T* to, uint4 u, int c, int d) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int j = 0; j < Vec<T>::N; ++j)
     if (c + j >= 0 && c + j < d) {
-      if constexpr (sizeof(T) == 2) w[j / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + j) << (j % 2 * 16);
-      else w[j] = *reinterpret_cast<const uint32_t*>(p + j);
+      if constexpr (sizeof(T) == 2) *reinterpret_cast<uint16_t*>(to + j) = (uint16_t)(w[j / 2] >> (j % 2 * 16));
+      else *reinterpret_cast<uint32_t*>(to + j) = w[j];
     }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // A thread's chunks of rows in the ring: 16-byte units of the tensor, of which
@@ -130,28 +174,28 @@ struct Mine {
   }
   // of the chunk's first element; the elements of the row are 0 to d - 1
   __device__ __forceinline__ int column(int i) const { return (r + i * tpr) * VN - skip; }
-  // chunk i of tensor b of the place at `at`; `tensor` is where its rows are, whose last unit a copy cuts off
-  __device__ __forceinline__ void get(const char* at, int b, const Span& sp, const void* tensor, int i, float2 (&v)[CN]) const {
-    uint4 u = lds(in[i] ? sm_addr(at) + b * slot + off[i] : zeros);
-    if (!WHOLE && edge[i]) u = trim(u, sp, tensor, i);
+  __device__ __forceinline__ void get(const char* at, int b, int i, float2 (&v)[CN]) const {
     float w[VN];
-    unpack(u, w);
+    unpack(lds(in[i] ? sm_addr(at) + b * slot + off[i] : zeros), w);
 #pragma unroll
     for (int c = 0; c < CN; ++c) v[c] = make_float2(w[2 * c], w[2 * c + 1]);
   }
-  // the row's elements of a unit, zeros for the others: a mask of its bits from lo to hi
-  __device__ __forceinline__ uint4 trim(uint4 u, const Span& sp, const void* tensor, int i) const {
-    const int c = column(i), lo = c < 0 ? -c * 8 * (int)sizeof(T) : 0, hi = c + VN > d ? (d - c) * 8 * (int)sizeof(T) : 128;
-    if ((int)off[i] + 16 > sp.bytes) u = load_cut(static_cast<const T*>(tensor) + (sp.at + off[i]) / (int64_t)sizeof(T), c, d);
-    uint64_t m0 = lo < 64 ? ~0ull << lo : 0ull, m1 = lo < 64 ? ~0ull : ~0ull << (lo - 64);
-    if (hi <= 64) m1 = 0ull;
-    else if (hi < 128) m1 &= (1ull << (hi - 64)) - 1;
-    if (hi < 64) m0 &= (1ull << hi) - 1;
-    u.x &= (uint32_t)m0;
-    u.y &= (uint32_t)(m0 >> 32);
-    u.z &= (uint32_t)m1;
-    u.w &= (uint32_t)(m1 >> 32);
-    return u;
+  // Once a row is there: the thread's own units of it get zeros where they have
+  // elements of other rows, and what a copy has cut off at the tensor's end.
+  __device__ __forceinline__ void patch(const JoinRows<T, WHOLE>& R, int64_t row) const {
+    if constexpr (!WHOLE) {
+      const Span sp = row_span<T, WHOLE>(row, R.rows, d);
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (edge[i]) {
+          const uint32_t at = sm_addr(R.place(R.at, sp)) + off[i];
+          if ((int)off[i] + 16 > sp.bytes) {
+            load_cut<T>(R.t0, R.t1, R.t2, R.t3, sp.at + off[i], at, slot, column(i), d);
+          } else {
+            trim_unit<sizeof(T)>(at, slot, R.nbuf, column(i), d);
+          }
+        }
+    }
   }
   __device__ __forceinline__ void set(void* tensor, const Span& sp, int i, const float2 (&v)[CN]) const {
     float w[VN];
@@ -161,13 +205,9 @@ struct Mine {
       w[2 * c + 1] = v[c].y;
     }
     char* to = static_cast<char*>(tensor) + sp.at + off[i];
-    if (!WHOLE && edge[i]) {
-#pragma unroll
-      for (int j = 0; j < VN; ++j)
-        if (column(i) + j >= 0 && column(i) + j < d) reinterpret_cast<T*>(to)[j] = from_f32<T>(w[j]);
-    } else if (in[i]) {
-      stg16(to, pack(w));
-    }
+    const uint4 u = pack(w);
+    if (!WHOLE && edge[i]) store_edge<T>(reinterpret_cast<T*>(to), u, column(i), d);
+    else if (in[i]) stg16(to, u);
   }
   // the columns' weights times `by`, `by` where there are none; 0 outside the row
   __device__ __forceinline__ float weight(const float* p, const float* p2, float by, int col) const {
@@ -262,7 +302,7 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
 #pragma unroll
     for (int i = 0; i < EPT / 2 / CN; ++i) {
       float2 v[CN];
-      mine.get(R.place(R.at, 0), by_, sp, a.y, i, v);
+      mine.get(R.place(R.at, sp), by_, i, v);
 #pragma unroll
       for (int c = 0; c < CN; ++c) s = fma2(v[c], v[c], s);
     }
@@ -271,6 +311,7 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
   float first = 0.f;  // the mean of y^2 of the row in work
   if (R.first < a.rows) {
     R.wait(a.err);
+    mine.patch(R, R.first);
     if (post) first = __shfl_sync(0xffffffffu, sums(squares(R.first), 0.f), 0) * inv;
   }
 #pragma unroll 1
@@ -281,9 +322,9 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
     float2 o[EPT / 2 / CN][CN], s2 = both(0.f);
 #pragma unroll
     for (int i = 0; i < EPT / 2 / CN; ++i) {
-      mine.get(R.place(R.at, 0), bx, sp, a.x, i, o[i]);
+      mine.get(R.place(R.at, sp), bx, i, o[i]);
       float2 v[CN];
-      if (BRANCH) mine.get(R.place(R.at, 0), by_, sp, a.y, i, v);
+      if (BRANCH) mine.get(R.place(R.at, sp), by_, i, v);
 #pragma unroll
       for (int c = 0; c < CN; ++c) {
         o[i][c] = mul2(o[i][c], rs);
@@ -296,6 +337,7 @@ __global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
     R.next();
     if (row + R.step < a.rows) {
       R.wait(a.err);
+      mine.patch(R, row + R.step);
       if (post) s1 = squares(row + R.step);
     }
     const float m = sums(s2.x + s2.y, s1) * inv;
@@ -354,6 +396,7 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
   // the warp's sum of v n of the row at place R.at, and its part of the columns' sums
   auto along = [&](int64_t row, float ro) {
     R.wait(a.err);
+    mine.patch(R, row);
     if (!FOLLOWING) return 0.f;
     const Span sp = row_span<T, WHOLE>(row, a.rows, a.d);
     float2 s = both(0.f);
@@ -361,8 +404,8 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
     for (int i = 0; i < NC; ++i) {
       float2 n[CN], v[CN], gn[CN];
       mine.weights(gn_s, i, gn);
-      mine.get(R.place(R.at, 0), bo, sp, a.out, i, n);
-      mine.get(R.place(R.at, 0), bh, sp, a.dh, i, v);
+      mine.get(R.place(R.at, sp), bo, i, n);
+      mine.get(R.place(R.at, sp), bh, i, v);
 #pragma unroll
       for (int c = 0; c < CN; ++c) {  // past the row's end dh is 0
         v[c] = mul2(n[c], v[c]);
@@ -398,7 +441,7 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       if (DOUT) {
-        mine.get(R.place(R.at, 0), bd, sp, a.dout, i, D[i]);
+        mine.get(R.place(R.at, sp), bd, i, D[i]);
       } else {
 #pragma unroll
         for (int c = 0; c < CN; ++c) D[i][c] = both(0.f);
@@ -406,15 +449,15 @@ __global__ void __launch_bounds__(BWD_NT, 1) join_bwd_kernel(const JoinK a) {
       if (FOLLOWING) {
         float2 n[CN], v[CN], gn[CN];
         mine.weights(gn_s, i, gn);
-        mine.get(R.place(R.at, 0), bo, sp, a.out, i, n);
-        mine.get(R.place(R.at, 0), bh, sp, a.dh, i, v);
+        mine.get(R.place(R.at, sp), bo, i, n);
+        mine.get(R.place(R.at, sp), bh, i, v);
 #pragma unroll
         for (int c = 0; c < CN; ++c) D[i][c] = fma2(ro, fma2(v[c], gn[c], mul2(n[c], k)), D[i][c]);
       }
       if (BRANCH) {
         float2 ga[CN];
         mine.weights(ga_s, i, ga);
-        mine.get(R.place(R.at, 0), by_, sp, a.y, i, y[i]);
+        mine.get(R.place(R.at, sp), by_, i, y[i]);
 #pragma unroll
         for (int c = 0; c < CN; ++c) {  // m = y ry
           const float2 t = mul2(D[i][c], y[i][c]);
@@ -785,7 +828,7 @@ Grid grid_of(int64_t rows, int d, int es, int bufs, bool bwd) {
   const int most_units = whole ? d * es / 16 : (d * es + 15 + 16 - es) / 16;  // of a row
   if (most_units * 16 > MAX_TPR * EPT * es) return g;
   g.tpr = threads_per_row(most_units * 16 / es);
-  g.slot = most_units * 16;
+  g.slot = whole ? most_units * 16 : (most_units * 16 + 112 + 127) / 128 * 128;
   const size_t place = (size_t)bufs * g.slot, weights = bwd ? 2 * EPT * g.tpr * 4 : 0;
   int groups = bwd ? BWD_NT / g.tpr : (g.tpr == 32 ? 4 : 1), per = bwd ? 1 : 65536 / (g.tpr * groups * FWD_REGS);
   const size_t room = bwd ? BWD_SMEM - weights : SMEM_SM;
