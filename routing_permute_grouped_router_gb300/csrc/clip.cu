@@ -24,7 +24,7 @@ constexpr int CLIP_NT = 256;
 constexpr int VECS = 8;                       // 16-byte vectors of a chunk that a thread holds
 constexpr int CHUNK_BYTES = CLIP_NT * VECS * 16;
 constexpr int FEW = 96, MANY = 768;           // tensors of a launch: parameters of 3 KB, or of 24 KB for long lists
-constexpr int NORM_CTAS = 4, SCALE_CTAS = 8;  // CTAs an SM
+constexpr int NORM_CTAS = 4, SCALE_CTAS = 4;  // CTAs an SM, all resident
 
 template <int N>
 struct ClipList {
@@ -100,14 +100,29 @@ __device__ __forceinline__ double cta_sum(double v, double* scratch) {
   return v;
 }
 
-// The sum of squares of a thread's vectors.  fp32 squares are exact enough
-// where the largest value is within 2^50 of 1 either way (nothing that counts
-// underflows, nothing overflows); beyond that they are summed in 64 bits, 32
-// times slower, which no trained model reaches.  A NaN is left out by the
-// maximum and makes either sum a NaN.
+// The sum of squares of a thread's part of a chunk in 64 bits, read again.
 template <typename T>
-__device__ __forceinline__ double squares(const uint4 (&u)[VECS]) {
+__device__ __noinline__ double squares64(const void* src, int64_t n, int64_t chunk) {
   constexpr int VN = Vec<T>::N;
+  const Part<T> p(src, n, chunk);
+  double d = 0.0;
+  for (int j = 0; j < VECS; ++j)
+    for (int i = 0; i < VN; ++i) {
+      const int64_t at = p.at(j) + i;
+      const double v = at >= 0 && at < n ? (double)to_f32(p.src[at]) : 0.0;
+      d += v * v;
+    }
+  return d;
+}
+// The same, in fp32 where that is exact enough: where the largest value is
+// within 2^50 of 1 either way nothing that counts underflows and nothing
+// overflows.  Beyond that no trained model is.  A NaN is left out by the maximum
+// and makes either sum a NaN.
+template <typename T>
+__device__ __forceinline__ double squares(const void* src, int64_t n, int64_t chunk) {
+  constexpr int VN = Vec<T>::N;
+  uint4 u[VECS];
+  Part<T>(src, n, chunk).load(u);
   float top = 0.f, s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < VECS; ++j) {
@@ -119,22 +134,12 @@ __device__ __forceinline__ double squares(const uint4 (&u)[VECS]) {
       s[i & 3] = fmaf(v[i], v[i], s[i & 3]);
     }
   }
-  if (top > 0x1p50f || (top < 0x1p-50f && top != 0.f)) {
-    double d = 0.0;
-#pragma unroll 1
-    for (int j = 0; j < VECS; ++j) {
-      float v[VN];
-      unpack(u[j], v);
-#pragma unroll
-      for (int i = 0; i < VN; ++i) d += (double)v[i] * (double)v[i];
-    }
-    return d;
-  }
+  if (top > 0x1p50f || (top < 0x1p-50f && top != 0.f)) return squares64<T>(src, n, chunk);
   return (double)((s[0] + s[1]) + (s[2] + s[3]));
 }
 
 template <int N>
-__global__ void __launch_bounds__(CLIP_NT) grad_norm_kernel(const __grid_constant__ ClipList<N> l, double* partial) {
+__global__ void __launch_bounds__(CLIP_NT, NORM_CTAS) grad_norm_kernel(const __grid_constant__ ClipList<N> l, double* partial) {
   pdl_enter();
   __shared__ double scratch[CLIP_NT / 32];
   const int64_t total = l.first[l.count];
@@ -142,14 +147,7 @@ __global__ void __launch_bounds__(CLIP_NT) grad_norm_kernel(const __grid_constan
 #pragma unroll 1
   for (int64_t c = blockIdx.x; c < total; c += gridDim.x) {
     const int t = tensor_of(l, c);
-    uint4 u[VECS];
-    if (l.bf16[t]) {
-      Part<__nv_bfloat16>(l.src[t], l.n[t], c - l.first[t]).load(u);
-      sum += squares<__nv_bfloat16>(u);
-    } else {
-      Part<float>(l.src[t], l.n[t], c - l.first[t]).load(u);
-      sum += squares<float>(u);
-    }
+    sum += l.bf16[t] ? squares<__nv_bfloat16>(l.src[t], l.n[t], c - l.first[t]) : squares<float>(l.src[t], l.n[t], c - l.first[t]);
   }
   sum = cta_sum(sum, scratch);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -180,7 +178,7 @@ __device__ __forceinline__ void scale_chunk(const void* src, void* dst_, int64_t
 }
 
 template <int N>
-__global__ void __launch_bounds__(CLIP_NT) grad_clip_kernel(const __grid_constant__ ClipList<N> l, const ClipScale s) {
+__global__ void __launch_bounds__(CLIP_NT, SCALE_CTAS) grad_clip_kernel(const __grid_constant__ ClipList<N> l, const ClipScale s) {
   pdl_enter();
   __shared__ double scratch[CLIP_NT / 32];
   double sum = 0.0;
