@@ -20,20 +20,25 @@
 namespace moe {
 namespace {
 
-constexpr int CLIP_NT = 256;
+constexpr int CLIP_NT = 256;                  // threads of a chunk
+constexpr int GROUPS = 4;                     // chunks that an SM has in work
 constexpr int VECS = 8;                       // 16-byte vectors of a chunk that a thread holds
 constexpr int CHUNK_BYTES = CLIP_NT * VECS * 16;
 constexpr int FEW = 96, MANY = 768;           // tensors of a launch: parameters of 3 KB, or of 24 KB for long lists
-constexpr int NORM_CTAS = 4, SCALE_CTAS = 4;  // CTAs an SM, all resident
 
+// A tensor's entry is one line of the constant cache: a miss there is a latency
+// of its own (fields in arrays of their own: 700 small tensors 20 us, both kernels).
+struct alignas(32) ClipEntry {
+  const void* src;
+  void* dst;
+  int64_t n;
+  int64_t first_bf16;  // twice the tensor's first chunk, plus 1 for bf16
+};
 template <int N>
 struct ClipList {
-  const void* src[N];
-  void* dst[N];
-  int64_t n[N];
-  int64_t first[N + 1];  // the tensor's first chunk
-  uint8_t bf16[N];
+  ClipEntry t[N + 1];  // the last one's first chunk is the number of chunks
   int count;
+  __host__ __device__ int64_t first(int i) const { return t[i].first_bf16 >> 1; }
 };
 struct ClipScale {
   const double* partial;
@@ -48,13 +53,31 @@ int64_t chunks_of(const void* p, int64_t n, int es) {
   return ((int64_t)(reinterpret_cast<uintptr_t>(p) & 15) + n * es + CHUNK_BYTES - 1) / CHUNK_BYTES;
 }
 
+// The tensor of a chunk: searched from where it would be among tensors of equal
+// length, in growing steps (each look at the list is a latency of its own: 300
+// small tensors 20.7 us by halving, both kernels).
 template <int N>
 __device__ __forceinline__ int tensor_of(const ClipList<N>& l, int64_t chunk) {
-  int lo = 0, hi = l.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (l.first[mid] <= chunk) lo = mid;
-    else hi = mid - 1;
+  int lo = (int)((float)chunk / (float)l.first(l.count) * (float)l.count), hi, step = 1;
+  if (lo >= l.count) lo = l.count - 1;
+  if (l.first(lo) <= chunk) {
+    while (lo + step < l.count && l.first(lo + step) <= chunk) {
+      lo += step;
+      step *= 2;
+    }
+    hi = lo + step < l.count ? lo + step : l.count;
+  } else {
+    hi = lo;
+    while (hi - step > 0 && l.first(hi - step) > chunk) {
+      hi -= step;
+      step *= 2;
+    }
+    lo = hi - step > 0 ? hi - step : 0;
+  }
+  while (lo + 1 < hi) {  // first[lo] <= chunk < first[hi]
+    const int mid = (lo + hi) >> 1;
+    if (l.first(mid) <= chunk) lo = mid;
+    else hi = mid;
   }
   return lo;
 }
@@ -69,7 +92,7 @@ struct Part {
   static constexpr int VN = Vec<T>::N;
   __device__ __forceinline__ Part(const void* p, int64_t n_, int64_t chunk) : src(static_cast<const T*>(p)), n(n_) {
     const int before = (int)(reinterpret_cast<uintptr_t>(p) & 15) / (int)sizeof(T);
-    e0 = chunk * (CHUNK_BYTES / (int)sizeof(T)) + threadIdx.x * VN - before;
+    e0 = chunk * (CHUNK_BYTES / (int)sizeof(T)) + (int)(threadIdx.x % CLIP_NT) * VN - before;
   }
   __device__ __forceinline__ int64_t at(int j) const { return e0 + (int64_t)j * CLIP_NT * VN; }
   __device__ __forceinline__ bool whole(int j) const { return at(j) >= 0 && at(j) + VN <= n; }
@@ -87,18 +110,6 @@ struct Part {
     }
   }
 };
-
-__device__ __forceinline__ double cta_sum(double v, double* scratch) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) scratch[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = 0.0;
-#pragma unroll
-  for (int i = 0; i < CLIP_NT / 32; ++i) v += scratch[i];
-  return v;
-}
 
 // The sum of squares of a thread's part of a chunk in 64 bits, read again.
 template <typename T>
@@ -138,18 +149,34 @@ __device__ __forceinline__ double squares(const void* src, int64_t n, int64_t ch
   return (double)((s[0] + s[1]) + (s[2] + s[3]));
 }
 
+// Sums in 64 bits are few and made by one warp: the SM adds two doubles a clock
+// (with all threads in a tree, and CTAs of 256, 700 small tensors took 20 us).
+__device__ __forceinline__ double warp_sum64(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// CTAs of a chunk at a time (one of four: 350 us for 604 M float32, not 337)
 template <int N>
-__global__ void __launch_bounds__(CLIP_NT, NORM_CTAS) grad_norm_kernel(const __grid_constant__ ClipList<N> l, double* partial) {
+__global__ void __launch_bounds__(CLIP_NT, GROUPS) grad_norm_kernel(const __grid_constant__ ClipList<N> l, double* partial) {
   pdl_enter();
-  __shared__ double scratch[CLIP_NT / 32];
-  const int64_t total = l.first[l.count];
+  __shared__ double each[CLIP_NT];
+  const int64_t total = l.first(l.count);
   double sum = 0.0;
 #pragma unroll 1
   for (int64_t c = blockIdx.x; c < total; c += gridDim.x) {
-    const int t = tensor_of(l, c);
-    sum += l.bf16[t] ? squares<__nv_bfloat16>(l.src[t], l.n[t], c - l.first[t]) : squares<float>(l.src[t], l.n[t], c - l.first[t]);
+    const ClipEntry& e = l.t[tensor_of(l, c)];
+    sum += (e.first_bf16 & 1) ? squares<__nv_bfloat16>(e.src, e.n, c - (e.first_bf16 >> 1))
+                              : squares<float>(e.src, e.n, c - (e.first_bf16 >> 1));
   }
-  sum = cta_sum(sum, scratch);
+  each[threadIdx.x] = sum;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < CLIP_NT; i += 32) sum += each[i + threadIdx.x];
+  sum = warp_sum64(sum);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
@@ -177,47 +204,56 @@ __device__ __forceinline__ void scale_chunk(const void* src, void* dst_, int64_t
   }
 }
 
+// One CTA an SM: each makes the norm for itself.
 template <int N>
-__global__ void __launch_bounds__(CLIP_NT, SCALE_CTAS) grad_clip_kernel(const __grid_constant__ ClipList<N> l, const ClipScale s) {
+__global__ void __launch_bounds__(CLIP_NT* GROUPS, 1) grad_clip_kernel(const __grid_constant__ ClipList<N> l, const ClipScale s) {
   pdl_enter();
-  __shared__ double scratch[CLIP_NT / 32];
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < s.parts; i += CLIP_NT) sum += s.partial[i];
-  const double norm = sqrt(cta_sum(sum, scratch));
-  const float as_float = (float)norm;
-  if (s.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *s.norm = as_float;
-  const bool clips = isfinite(as_float) && as_float > s.max_norm;
-  const float scale = clips ? (float)((double)s.max_norm / norm) : 1.f;
-  const int64_t total = l.first[l.count];
+  __shared__ float by;
+  __shared__ bool clip;
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < s.parts; i += 32) sum += s.partial[i];
+    sum = warp_sum64(sum);
+    if (threadIdx.x == 0) {
+      const double norm = sqrt(sum);
+      const float as_float = (float)norm;
+      if (s.norm != nullptr && blockIdx.x == 0) *s.norm = as_float;
+      clip = isfinite(as_float) && as_float > s.max_norm;
+      by = clip ? (float)((double)s.max_norm / norm) : 1.f;
+    }
+  }
+  __syncthreads();
+  const bool clips = clip;
+  const float scale = by;
+  const int64_t total = l.first(l.count);
 #pragma unroll 1
-  for (int64_t c = total - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
-    const int t = tensor_of(l, c);
-    if (l.dst[t] == nullptr || (!clips && l.dst[t] == l.src[t])) continue;
-    if (l.bf16[t]) scale_chunk<__nv_bfloat16>(l.src[t], l.dst[t], l.n[t], c - l.first[t], scale);
-    else scale_chunk<float>(l.src[t], l.dst[t], l.n[t], c - l.first[t], scale);
+  for (int64_t c = total - 1 - blockIdx.x - (int64_t)(threadIdx.x / CLIP_NT) * gridDim.x; c >= 0; c -= GROUPS * gridDim.x) {
+    const ClipEntry& e = l.t[tensor_of(l, c)];
+    if (e.dst == nullptr || (!clips && e.dst == e.src)) continue;
+    if (e.first_bf16 & 1) scale_chunk<__nv_bfloat16>(e.src, e.dst, e.n, c - (e.first_bf16 >> 1), scale);
+    else scale_chunk<float>(e.src, e.dst, e.n, c - (e.first_bf16 >> 1), scale);
   }
 }
 
 // The list of tensors [from, from + N) of the call; its chunks.
 template <int N>
 int64_t fill(ClipList<N>* l, const moe_grad* g, int count, int from) {
-  l->count = 0;
-  l->first[0] = 0;
+  int k = 0;
+  int64_t chunks = 0;
   for (int i = from; i < count && i < from + N; ++i) {
-    const int es = g[i].dtype == MOE_BF16 ? 2 : 4, k = l->count;
+    const int es = g[i].dtype == MOE_BF16 ? 2 : 4;
     if (g[i].n == 0) continue;
-    l->src[k] = g[i].src;
-    l->dst[k] = g[i].dst;
-    l->n[k] = g[i].n;
-    l->bf16[k] = es == 2;
-    l->first[k + 1] = l->first[k] + chunks_of(g[i].src, g[i].n, es);
-    l->count = k + 1;
+    l->t[k++] = {g[i].src, g[i].dst, g[i].n, chunks * 2 + (es == 2)};
+    chunks += chunks_of(g[i].src, g[i].n, es);
   }
-  return l->first[l->count];
+  l->t[k].first_bf16 = chunks * 2;
+  l->count = k;
+  return chunks;
 }
-int norm_ctas(int64_t chunks) {
-  const int64_t most = (int64_t)sm_count() * NORM_CTAS;
-  return (int)(chunks < most ? chunks : most);
+unsigned ctas(int64_t chunks, int an_sm) {
+  const int64_t most = (int64_t)sm_count() * an_sm;
+  return (unsigned)(chunks < most ? chunks : most);
 }
 
 template <int N>
@@ -228,9 +264,10 @@ cudaError_t clip_lists(const moe_grad* g, int count, float max_norm, float* norm
     const int64_t chunks = fill(&l, g, count, from);
     if (chunks == 0) continue;
     LaunchScope ls(KK_GRAD_NORM, st);
-    const cudaError_t e = launch_pdl(grad_norm_kernel<N>, dim3(norm_ctas(chunks)), dim3(CLIP_NT), 0, st, l, partial + parts);
+    const cudaError_t e = launch_pdl(grad_norm_kernel<N>, dim3(ctas(chunks, GROUPS)), dim3(CLIP_NT), 0, st, l,
+                                     partial + parts);
     if (e != cudaSuccess) return e;
-    parts += norm_ctas(chunks);
+    parts += (int)ctas(chunks, GROUPS);
   }
   bool writes = false;
   for (int i = 0; i < count; ++i)
@@ -241,14 +278,14 @@ cudaError_t clip_lists(const moe_grad* g, int count, float max_norm, float* norm
     int64_t chunks = fill(&l, g, count, from);
     if (!writes) {
       l.count = 0;
+      l.t[0].first_bf16 = 0;
       chunks = 1;  // the norm alone
     } else if (chunks == 0 && s.norm == nullptr) {
       continue;
     }
-    const int64_t most = (int64_t)sm_count() * SCALE_CTAS;
     LaunchScope ls(KK_GRAD_CLIP, st);
-    const cudaError_t e = launch_pdl(grad_clip_kernel<N>, dim3((unsigned)(chunks < 1 ? 1 : chunks < most ? chunks : most)),
-                                     dim3(CLIP_NT), 0, st, l, s);
+    const cudaError_t e = launch_pdl(grad_clip_kernel<N>, dim3(ctas(chunks < 1 ? 1 : chunks, 1)),
+                                     dim3(CLIP_NT * GROUPS), 0, st, l, s);
     if (e != cudaSuccess) return e;
     s.norm = nullptr;
   }
@@ -259,7 +296,7 @@ cudaError_t clip_lists(const moe_grad* g, int count, float max_norm, float* norm
 
 size_t clip_ws_bytes(int count) {
   const int per = count <= FEW ? FEW : MANY;
-  return (size_t)((count + per - 1) / per + 1) * sm_count() * NORM_CTAS * sizeof(double);
+  return (size_t)((count + per - 1) / per + 1) * sm_count() * GROUPS * sizeof(double);
 }
 
 cudaError_t launch_clip(const moe_grad* grads, int count, float max_norm, float* norm, void* ws, cudaStream_t st) {
