@@ -8,6 +8,8 @@
 // leaves two floats a row and 128 words, which loss_combine_kernel joins.  The
 // backward goes over the vocabulary in equal pieces: dz of a piece, then its
 // part of dx (added up in fp32) and its rows of dW.
+#include <algorithm>
+
 #include "common.cuh"
 #include "vocab_loss.h"
 
@@ -16,6 +18,7 @@ namespace {
 
 constexpr int LIST_NT = 1024, LIST_EACH = 8;        // labels a thread takes at a time
 constexpr int ROW_NT = 256;
+constexpr int MAX_SLICES = 64;
 constexpr int64_t PIECE_VALUES = (int64_t)1 << 28;  // of a part of dz: 512 MB at most, or a tile's columns
 
 // The labelled tokens in order, each token's place among them, their number.
@@ -224,12 +227,18 @@ __global__ void __launch_bounds__(ROW_NT) loss_dx_kernel(const LossWork w, const
     for (int i = threadIdx.x * VN; i < w.d; i += ROW_NT * VN) {
       float v[VN];
 #pragma unroll
-      for (int j = 0; j < VN; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src + i + j);
-        v[j] = f.x;
-        v[j + 1] = f.y;
-        v[j + 2] = f.z;
-        v[j + 3] = f.w;
+      for (int j = 0; j < VN; ++j) v[j] = 0.f;
+#pragma unroll 4
+      for (int s = 0; s < w.slices; ++s) {
+        const float* from = src + (int64_t)s * w.Tp * w.d + i;
+#pragma unroll
+        for (int j = 0; j < VN; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(from + j);
+          v[j] += f.x;
+          v[j + 1] += f.y;
+          v[j + 2] += f.z;
+          v[j + 3] += f.w;
+        }
       }
       if constexpr (sizeof(T) == 2) {
         float u[VN];
@@ -253,6 +262,18 @@ int piece_of(int64_t Tp, int64_t V) {
   if (most >= all) return (int)all;
   const int64_t pieces = (V + (most < LOSS_TILE ? LOSS_TILE : most) - 1) / (most < LOSS_TILE ? LOSS_TILE : most);
   return (int)up((V + pieces - 1) / pieces, LOSS_TILE);
+}
+
+// Slices of a piece for dx: two tiles of it are at most a pair's share of both
+// gradients' work.  (64 tokens, d 4096, V 128000: 16 tiles of dx alone kept 16 of
+// the 76 pairs busy for 800 us.)  It goes by T, not by how many tokens are labelled.
+int slices_of(const LossWork& w) {
+  const int64_t cols = (w.d + 255) / 256, k = w.piece / 128;
+  const int64_t seg = w.parts == 1 ? 1 : 6, dx = w.Tp / LOSS_TILE * cols * k * seg;
+  const int64_t both = dx + w.piece / LOSS_TILE * cols * (w.Tp / 128) * (w.parts == 1 ? w.dzp : 6);
+  const int64_t s = (2 * k * seg * (sm_count() / 2) + both - 1) / both;
+  const int64_t most = std::min<int64_t>(std::min<int64_t>(MAX_SLICES, k), ((int64_t)1 << 28) / ((int64_t)w.Tp * w.d));
+  return (int)std::max<int64_t>(1, std::min(s, most));
 }
 
 // What a call keeps in the workspace, from `base` on (null: its size alone); returns its end.
@@ -286,7 +307,8 @@ size_t lay_out(LossWork* w, char* base, int T, int d, int V, bool bf16, bool bac
     w->grad = reinterpret_cast<float*>(take(Tp * 4));
     w->off = reinterpret_cast<float*>(take(Tp * 4));
     w->dz = reinterpret_cast<__nv_bfloat16*>(take((size_t)dzp * Tp * w->piece * 2));
-    w->acc = reinterpret_cast<float*>(take(Tp * d * 4));
+    w->slices = slices_of(*w);
+    w->acc = reinterpret_cast<float*>(take(w->slices * Tp * d * 4));
   }
   return end;
 }
@@ -324,8 +346,10 @@ size_t loss_ws_bytes(int T, int d, int V, bool bf16, bool training) {
   LossWork w{};
   const size_t fwd = lay_out(&w, nullptr, T, d, V, bf16, false, 0);
   if (!training) return fwd;
-  const size_t bwd = lay_out(&w, nullptr, T, d, V, bf16, true, bf16 ? 2 : MAX_PARTS);
-  return fwd > bwd ? fwd : bwd;
+  size_t most = fwd;
+  for (int dzp = bf16 ? 1 : MAX_PARTS; dzp <= (bf16 ? 2 : MAX_PARTS); ++dzp)
+    most = std::max(most, lay_out(&w, nullptr, T, d, V, bf16, true, dzp));
+  return most;
 }
 
 cudaError_t launch_loss_fwd(const LossArgs& a, uint32_t* err, cudaStream_t st) {

@@ -27,7 +27,8 @@ struct LossWork {
   const __nv_bfloat16* wp;  // [V][parts][ldw]: W itself, or its parts
   float2* partial;  // [V / LOSS_PART, whole tiles][Tp]: the largest logit and the sum of exp of the distances to it
   __nv_bfloat16* dz;  // [dz parts][Tp][piece]
-  float* acc;       // [Tp][d]: dx before its rounding
+  float* acc;       // [slices][Tp][d]: dx before its rounding
+  int slices;       // of each piece, summed apart where dx alone has too few tiles
   int T, Tp, d, V, parts, ldx, ldw;
   int mean;         // that gradient is 1 / count for every token: dz goes without it, dx and dW get it at the end
   int v0, piece, dzp;  // the piece of the vocabulary in work; bf16 parts of dz

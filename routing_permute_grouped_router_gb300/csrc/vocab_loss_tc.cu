@@ -81,6 +81,7 @@ __host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn) {
          ((uint32_t)(BN >> 3) << 17) | ((uint32_t)((2 * BM) >> 4) << 24);
 }
 
+// 16-byte chunk j of row `lane` of a box, in the 128-byte swizzle of its tensor map
 __device__ __forceinline__ uint32_t box_chunk(uint32_t box, int lane, int j) {
   return box + lane * 128 + (((uint32_t)j ^ (uint32_t)(lane & 7)) << 4);
 }
@@ -95,6 +96,8 @@ __device__ __forceinline__ float exp_from(float z, float from) {
 struct Tile {
   int what;    // GRADS: 0 acc, 1 dW
   int m0, n0;  // the pair's first row, the first column
+  int slice;   // of K: acc has a sum of its own for each
+  int b0;      // the first stage
   int blocks;  // stages of one pair of parts
 };
 // How the tiles are dealt to the pairs.  LOGITS, DLOGITS: one after the other.
@@ -105,7 +108,7 @@ struct Deal {
   int len[2];    // their stages
   int first;     // the kind that comes first
   int extra, early;
-  int nm, nn;    // row and column tiles of the logits
+  int nm, nn;    // row and column tiles of the logits; of acc
 };
 
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
@@ -122,9 +125,10 @@ __device__ __forceinline__ Deal deal_of(const TcArgs& a, int n, int npairs) {
     return d;
   }
   const int cols = cdiv(a.w.d, BN);
+  d.nm = rows;
   d.nn = cols;
-  d.count[0] = a.with_dx ? rows * cols : 0;
-  d.len[0] = a.w.piece / (BK * KB);
+  d.count[0] = a.with_dx ? rows * cols * a.w.slices : 0;
+  d.len[0] = cdiv(a.w.piece / (BK * KB), a.w.slices);
   d.count[1] = a.with_dw ? a.w.piece / BN * cols : 0;
   d.len[1] = cdiv(n, BK * KB);
   const int c0 = d.len[0] * a.seg[0].n, c1 = d.len[1] * a.seg[1].n;
@@ -139,10 +143,10 @@ __device__ __forceinline__ Deal deal_of(const TcArgs& a, int n, int npairs) {
   return d;
 }
 
-// The j-th tile of a pair; false past the last.
+// The j-th tile of a pair; false past the last.  `stages` are the piece's.
 template <int KIND>
-__device__ __forceinline__ bool tile_of(const Deal& d, int pair, int npairs, int j, Tile* t) {
-  t->what = 0;
+__device__ __forceinline__ bool tile_of(const Deal& d, int pair, int npairs, int stages, int j, Tile* t) {
+  t->what = t->slice = t->b0 = 0;
   if (KIND != GRADS) {
     const int i = pair + j * npairs;
     if (i >= d.count[0]) return false;
@@ -163,9 +167,17 @@ __device__ __forceinline__ bool tile_of(const Deal& d, int pair, int npairs, int
     if (i >= d.count[kind]) return false;
   }
   t->what = kind;
-  t->m0 = i / d.nn * 2 * BM;
   t->n0 = i % d.nn * BN;
+  int m = i / d.nn;
   t->blocks = d.len[kind];
+  if (kind == 0) {
+    t->slice = m / d.nm;
+    m -= t->slice * d.nm;
+    t->b0 = t->slice * d.len[0];
+    const int left = stages - t->b0;  // fewer in the last slice; perhaps none
+    t->blocks = left < t->blocks ? (left > 0 ? left : 0) : t->blocks;
+  }
+  t->m0 = m * 2 * BM;
   return true;
 }
 
@@ -203,7 +215,7 @@ __device__ __forceinline__ void load_stage(const Maps& maps, const TcArgs& a, co
 // ------------------------------ epilogues ---------------------------------- //
 // A thread has 128 columns of one row, in registers; TMEM is free again.
 struct Epi {
-  uint32_t uses;  // completed waits on the warp's input barrier
+  uint32_t uses;  // completed waits on the box's input barrier
   bool pending;   // an input load is in flight
 };
 
@@ -216,9 +228,15 @@ __device__ __forceinline__ void mask_tail(float (&v)[HALF], int left) {
   }
 }
 
+// What an epilogue wants of a row, loaded while the MMAs run (rows up to Tp are there).
+struct RowData {
+  int label;
+  float g, lse;
+};
+
 // The row's maximum over the columns, and the sum of exp of the distances to it.
-__device__ __forceinline__ void logits_epilogue(const LossWork& w, int row, int col, float (&v)[HALF]) {
-  const int at = w.label[row] - col;  // rows up to Tp are there
+__device__ __forceinline__ void logits_epilogue(const LossWork& w, int row, int col, const RowData& rd, float (&v)[HALF]) {
+  const int at = rd.label - col;
   if (at >= 0 && at < HALF) {
     float z = 0.f;
 #pragma unroll
@@ -237,7 +255,9 @@ __device__ __forceinline__ void logits_epilogue(const LossWork& w, int row, int 
   w.partial[(int64_t)(col / HALF) * w.Tp + row] = make_float2(best, (s[0] + s[1]) + (s[2] + s[3]));
 }
 
-// The warp's one box may be written again.
+// The warp's box may be written again.  (Boxes of half the width, one filled while
+// the other leaves, and plain stores of whole lines from the box are both slower:
+// a tile of a float32 dW with one token's K 11 and 14 us, these 6.)
 __device__ __forceinline__ void wait_box(int lane) {
   if (lane == 0) bulk_wait_read0();
   __syncwarp();
@@ -253,24 +273,23 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t buf, 
 
 // dz of the row over the columns, 64 of them a box, a box a part
 __device__ __forceinline__ void dlogits_epilogue(const Maps& maps, const LossWork& w, int row, int col, int lane,
-                                                 uint32_t buf, float (&v)[HALF]) {
-  const int label = w.label[row], at = label - w.v0 - col;
-  const float g = w.grad[row], lse = w.lse[row];
+                                                 uint32_t box, const RowData& rd, float (&v)[HALF]) {
+  const int at = rd.label - w.v0 - col;
   mask_tail(v, w.V - w.v0 - col);
 #pragma unroll
-  for (int i = 0; i < HALF; ++i) v[i] = exp_from(v[i], lse);
-  if (label >= 0 && at >= 0 && at < HALF) {
+  for (int i = 0; i < HALF; ++i) v[i] = exp_from(v[i], rd.lse);
+  if (rd.label >= 0 && at >= 0 && at < HALF) {
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < HALF; ++i) {
       v[i] -= at == i ? 1.f : 0.f;
       z = at == i ? v[i] : z;
     }
-    z *= g;
+    z *= rd.g;
     w.off[row] = z - __bfloat162float(__float2bfloat16_rn(z));  // of the first part
   }
 #pragma unroll
-  for (int i = 0; i < HALF; ++i) v[i] = label >= 0 ? v[i] * g : 0.f;  // 0 on padding, whatever W holds
+  for (int i = 0; i < HALF; ++i) v[i] = rd.label >= 0 ? v[i] * rd.g : 0.f;  // 0 on padding, whatever W holds
 #pragma unroll
   for (int c = 0; c < HALF; c += 64) {
 #pragma unroll 1
@@ -282,23 +301,23 @@ __device__ __forceinline__ void dlogits_epilogue(const Maps& maps, const LossWor
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = v[c + 8 * q + i];
         const uint4 u = pack(x);
-        sts128(box_chunk(buf, lane, q), u);
+        sts128(box_chunk(box, lane, q), u);
         unpack(u, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[c + 8 * q + i] -= x[i];  // what the part leaves
       }
-      store_box(&maps.m[2], buf, col + c, p * w.Tp + row - lane, lane);
+      store_box(&maps.m[2], box, col + c, p * w.Tp + row - lane, lane);
     }
   }
 }
 
 // The old values of a box, on their way while the MMAs run or the box before leaves.
-__device__ __forceinline__ void fetch_box(const CUtensorMap* map, uint32_t buf, uint32_t bar, int c0, int c1, int lane,
+__device__ __forceinline__ void fetch_box(const CUtensorMap* map, uint32_t box, uint32_t bar, int c0, int c1, int lane,
                                           Epi& es) {
   if (lane == 0) {
     bulk_wait_read0();
     mbar_expect_tx(bar, BOX_BYTES);
-    tma_load_2d(buf, map, bar, c0, c1);
+    tma_load_2d(box, map, bar, c0, c1);
   }
   es.pending = true;
   __syncwarp();
@@ -306,14 +325,14 @@ __device__ __forceinline__ void fetch_box(const CUtensorMap* map, uint32_t buf, 
 // 128 columns of a row of acc or dW, stored or added to what is there, a box of 128 bytes a row at a time.
 template <bool BF16>
 __device__ __forceinline__ bool grads_epilogue(const CUtensorMap* map, int row0, int col, int d, bool add, int lane,
-                                               uint32_t buf, uint32_t bar, Epi& es, float (&v)[HALF], float scale,
+                                               uint32_t box, uint32_t bar, Epi& es, float (&v)[HALF], float scale,
                                                uint32_t* err, volatile int* abort_flag) {
   constexpr int W = BF16 ? 64 : 32;  // columns of a box
 #pragma unroll
   for (int c = 0; c < HALF; c += W) {
     if (col + c >= d) break;
     if (add) {
-      if (!es.pending) fetch_box(map, buf, bar, col + c, row0, lane, es);
+      if (!es.pending) fetch_box(map, box, bar, col + c, row0, lane, es);
       if (!mbar_wait(bar, es.uses & 1u, abort_flag, err, 962)) return false;
       ++es.uses;
       es.pending = false;
@@ -324,13 +343,13 @@ __device__ __forceinline__ bool grads_epilogue(const CUtensorMap* map, int row0,
     for (int j = 0; j < 8; ++j) {
       constexpr int N = BF16 ? 8 : 4;
       float x[N], o[N];
-      const uint32_t at = box_chunk(buf, lane, j);
+      const uint32_t at = box_chunk(box, lane, j);
       if (add) unpack(lds128(at), o);
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = add ? fmaf(v[c + N * j + i], scale, o[i]) : v[c + N * j + i] * scale;
       sts128(at, pack(x));
     }
-    store_box(map, buf, col + c, row0, lane);
+    store_box(map, box, col + c, row0, lane);
   }
   return true;
 }
@@ -394,6 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
   Deal deal{};
   if (n >= 0) deal = deal_of<KIND>(a, n, npairs);
   const bool any = deal.count[0] + deal.count[1] > 0;
+  const int stages = KIND == GRADS ? a.w.piece / (BK * KB) : 0;
   const uint32_t tmem_base = *tmem_slot, smem_base = smem_addr(smem);
 
   if (warp == 0) {
@@ -404,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
       uint32_t phase = 0;
       bool alive = true;
       Tile t;
-      for (int j = 0; alive && tile_of<KIND>(deal, pair, npairs, j, &t); ++j) {
+      for (int j = 0; alive && tile_of<KIND>(deal, pair, npairs, stages, j, &t); ++j) {
         const int nseg = a.seg[KIND == GRADS ? t.what : 0].n;
         for (int s = 0; s < nseg && alive; ++s)
           for (int b = 0; b < t.blocks; ++b) {
@@ -415,7 +435,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
             const uint32_t fb_local = smem_addr(&full_bar[stage]);
             if (rank == 0) mbar_expect_tx(fb_local, 2 * STAGE);
             const uint32_t fb = rank == 0 ? fb_local : mapa_shared(fb_local, 0);
-            load_stage<KIND>(maps, a, t, s, b, smem_base + stage * STAGE, fb, rank);
+            load_stage<KIND>(maps, a, t, s, t.b0 + b, smem_base + stage * STAGE, fb, rank);
             ++issued;
             if (++stage == NST) {
               stage = 0;
@@ -452,7 +472,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
       uint32_t phase = 0, uses = 0;
       bool alive = true;
       Tile t;
-      for (int j = 0; alive && tile_of<KIND>(deal, pair, npairs, j, &t); ++j) {
+      for (int j = 0; alive && tile_of<KIND>(deal, pair, npairs, stages, j, &t); ++j) {
         const bool a_mn = KIND == GRADS && t.what == 1, b_mn = KIND == GRADS;
         const uint32_t id = a_mn ? idesc(true, true) : b_mn ? idesc(false, true) : idesc(false, false);
         const int total = t.blocks * a.seg[KIND == GRADS ? t.what : 0].n;
@@ -506,17 +526,25 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
     Epi es{0u, false};
     uint32_t uses = 0;  // accumulators taken so far
     Tile t;
-    for (int j = 0; tile_of<KIND>(deal, pair, npairs, j, &t); ++j) {
+    for (int j = 0; tile_of<KIND>(deal, pair, npairs, stages, j, &t); ++j) {
       const int row0 = t.m0 + (int)rank * BM + q * 32, col = t.n0 + side;
       const CUtensorMap* map = &maps.m[4 + t.what];
-      const int orow = row0 + (KIND == GRADS && t.what == 1 ? a.w.v0 : 0);
+      const int orow = row0 + (KIND != GRADS ? 0 : t.what == 1 ? a.w.v0 : t.slice * a.w.Tp);
       const bool add = KIND == GRADS && (t.what == 0 ? a.add_acc : a.add_dw);
-      const bool wanted = KIND != GRADS || (orow < (t.what == 1 ? a.w.V : a.w.Tp) && col < a.w.d);
+      const bool wanted = KIND != GRADS || ((t.what == 0 || orow < a.w.V) && col < a.w.d);
       const int total = t.blocks * a.seg[KIND == GRADS ? t.what : 0].n;
       if (add && wanted && total > 0) fetch_box(map, buf, lbar, col, orow, lane, es);
+      RowData rd{};
+      if (KIND != GRADS) rd.label = a.w.label[row0 + lane];
+      if (KIND == DLOGITS) {
+        rd.g = a.w.grad[row0 + lane];
+        rd.lse = a.w.lse[row0 + lane];
+      }
       float v[HALF];
+      if (total == 0) {
 #pragma unroll
-      for (int i = 0; i < HALF; ++i) v[i] = 0.f;
+        for (int i = 0; i < HALF; ++i) v[i] = 0.f;
+      }
       bool ok = true;
       for (int b = 0; b < total; b += CHAIN) {
         const uint32_t acc = uses & 1u;
@@ -533,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
           tmem_ld32(tacc + c, r);
           tmem_ld_wait(r);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[c + i] += __uint_as_float(r[i]);
+          for (int i = 0; i < 32; ++i) v[c + i] = b == 0 ? __uint_as_float(r[i]) : v[c + i] + __uint_as_float(r[i]);
         }
         tc_fence_before();
         __syncwarp();
@@ -545,9 +573,9 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
       }
       if (!ok) break;
       if (KIND == LOGITS) {
-        logits_epilogue(a.w, row0 + lane, col, v);
+        logits_epilogue(a.w, row0 + lane, col, rd, v);
       } else if (KIND == DLOGITS) {
-        dlogits_epilogue(maps, a.w, row0 + lane, col, lane, buf, v);
+        dlogits_epilogue(maps, a.w, row0 + lane, col, lane, buf, rd, v);
       } else if (wanted && (total > 0 || !add)) {  // no labelled tokens: dW is 0, or as it was
         const float scale = t.what == 1 && a.w.mean && n > 0 ? 1.f / (float)n : 1.f;
         if (t.what == 1 && a.dw_bf16)
@@ -691,11 +719,11 @@ cudaError_t tc_loss_grads(const LossWork& w, bool dx, void* dW, bool dw_bf16, bo
   bool ok = make_map(&maps.m[0], w.dz, planes, w.piece, BK, BM) && make_map(&maps.m[2], w.dz, planes, w.piece, 64, KB * BK) &&
             make_map(&maps.m[1], w.wp, w.V, (uint64_t)w.parts * w.ldw, 64, KB * BK) &&
             make_map(&maps.m[3], w.xp, w.Tp, (uint64_t)w.parts * w.ldx, 64, KB * BK);
-  if (dx) ok = ok && make_map(&maps.m[4], w.acc, w.Tp, w.d, 32, 32, true);
+  if (dx) ok = ok && make_map(&maps.m[4], w.acc, (uint64_t)w.slices * w.Tp, w.d, 32, 32, true);
   if (dW) ok = ok && make_map(&maps.m[5], dW, w.V, w.d, dw_bf16 ? 64 : 32, 32, !dw_bf16);
   if (!ok) return cudaErrorInvalidValue;
   const int64_t cols = (w.d + BN - 1) / BN;
-  const int64_t tiles = ((dx ? w.Tp / (2 * BM) : 0) + (dW ? w.piece / BN : 0)) * cols;
+  const int64_t tiles = ((dx ? (int64_t)w.Tp / (2 * BM) * w.slices : 0) + (dW ? w.piece / BN : 0)) * cols;
   return launch<GRADS>(maps, a, tiles, KK_LOSS_GRADS, st);
 }
 
