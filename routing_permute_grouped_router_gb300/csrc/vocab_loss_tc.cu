@@ -43,20 +43,27 @@ constexpr int KB = 2;                       // k-blocks of a stage
 constexpr int BLOCK_BYTES = BM * BK * 2;    // a loaded box
 constexpr int A_BYTES = KB * BLOCK_BYTES, STAGE = 2 * A_BYTES;
 static_assert(BM == BNH && KB == 2, "boxes of A and B are alike");
-constexpr int NST = 3;
 constexpr int CHAIN = 8;                    // stages added up in TMEM
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int HALF = BN / 2;                // columns of a row that an epilogue thread holds
 constexpr int BOX_BYTES = 4096;             // a warp's staged output box: 32 rows x 128 bytes
-constexpr int EPI_OFF = NST * STAGE;
-constexpr int CTRL_OFF = EPI_OFF + EPI_WARPS * BOX_BYTES;
 static_assert(HALF == LOSS_PART, "columns of a partial sum");
-constexpr int SMEM = CTRL_OFF + 512 + 1024;  // control block, alignment
-static_assert(SMEM <= 232448, "shared memory budget");
+// A tile of long K wants three stages, which leaves a box a warp; one of short K
+// waits for its epilogue, and has two boxes a warp and two stages.  (4096 x 512 x
+// 32000 dz: 169 us with two boxes, 194 with three stages; at d 1024 248 and 221.
+// A float32 dW of 64 and of 300 tokens, 4096 x 128000: 895 and 980, 1217 and 993.)
+template <bool SHORT>
+struct Shape {
+  static constexpr int NST = SHORT ? 2 : 3, BOXES = SHORT ? 2 : 1;
+  static constexpr int EPI_OFF = NST * STAGE, CTRL_OFF = EPI_OFF + EPI_WARPS * BOXES * BOX_BYTES;
+  static constexpr int SMEM = CTRL_OFF + 512 + 1024;  // control block, alignment
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
 constexpr uint32_t TMEM_COLS = 512;         // two accumulators of 256 columns
 constexpr int MAX_SEG = 6;
 constexpr int GROUP_M = 16;                 // row tiles that share the columns' panels through L2
+constexpr int SHORT_K = 4;                  // stages: K of 512
 constexpr float LOG2E = 1.44269504088896340736f;
 
 enum Kind { LOGITS = 0, DLOGITS = 1, GRADS = 2 };
@@ -214,9 +221,14 @@ __device__ __forceinline__ void load_stage(const Maps& maps, const TcArgs& a, co
 
 // ------------------------------ epilogues ---------------------------------- //
 // A thread has 128 columns of one row, in registers; TMEM is free again.
+template <int BOXES>
 struct Epi {
-  uint32_t uses;  // completed waits on the box's input barrier
-  bool pending;   // an input load is in flight
+  uint32_t box;          // the one that is filled next
+  uint32_t uses[BOXES];  // completed waits on the boxes' input barriers
+  bool pending[BOXES];   // an input load is in flight
+  __device__ __forceinline__ void next() {
+    if (BOXES == 2) box ^= 1u;
+  }
 };
 
 // Columns past the vocabulary are left out; `left` is how many of the thread's are not.
@@ -255,11 +267,15 @@ __device__ __forceinline__ void logits_epilogue(const LossWork& w, int row, int 
   w.partial[(int64_t)(col / HALF) * w.Tp + row] = make_float2(best, (s[0] + s[1]) + (s[2] + s[3]));
 }
 
-// The warp's box may be written again.  (Boxes of half the width, one filled while
-// the other leaves, and plain stores of whole lines from the box are both slower:
-// a tile of a float32 dW with one token's K 11 and 14 us, these 6.)
+// The warp's next box may be written again.  (Boxes of half the width, one filled
+// while the other leaves, and plain stores of whole lines from the box are both
+// slower: a tile of a float32 dW with one token's K 11 and 14 us, these 6.)
+template <int BOXES>
 __device__ __forceinline__ void wait_box(int lane) {
-  if (lane == 0) bulk_wait_read0();
+  if (lane == 0) {
+    if (BOXES == 2) bulk_wait_read1();
+    else bulk_wait_read0();
+  }
   __syncwarp();
 }
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t buf, int c0, int c1, int lane) {
@@ -272,8 +288,9 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t buf, 
 }
 
 // dz of the row over the columns, 64 of them a box, a box a part
+template <int BOXES>
 __device__ __forceinline__ void dlogits_epilogue(const Maps& maps, const LossWork& w, int row, int col, int lane,
-                                                 uint32_t box, const RowData& rd, float (&v)[HALF]) {
+                                                 uint32_t buf, Epi<BOXES>& es, const RowData& rd, float (&v)[HALF]) {
   const int at = rd.label - w.v0 - col;
   mask_tail(v, w.V - w.v0 - col);
 #pragma unroll
@@ -294,7 +311,8 @@ __device__ __forceinline__ void dlogits_epilogue(const Maps& maps, const LossWor
   for (int c = 0; c < HALF; c += 64) {
 #pragma unroll 1
     for (int p = 0; p < w.dzp; ++p) {
-      wait_box(lane);
+      const uint32_t box = buf + es.box * BOX_BYTES;
+      wait_box<BOXES>(lane);
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
         float x[8];
@@ -307,37 +325,43 @@ __device__ __forceinline__ void dlogits_epilogue(const Maps& maps, const LossWor
         for (int i = 0; i < 8; ++i) v[c + 8 * q + i] -= x[i];  // what the part leaves
       }
       store_box(&maps.m[2], box, col + c, p * w.Tp + row - lane, lane);
+      es.next();
     }
   }
 }
 
-// The old values of a box, on their way while the MMAs run or the box before leaves.
-__device__ __forceinline__ void fetch_box(const CUtensorMap* map, uint32_t box, uint32_t bar, int c0, int c1, int lane,
-                                          Epi& es) {
+// The old values of the box that is filled `ahead` from now, on their way while
+// the MMAs run or the box before leaves.
+template <int BOXES>
+__device__ __forceinline__ void fetch_box(const CUtensorMap* map, uint32_t buf, uint32_t bar, int c0, int c1, int lane,
+                                          uint32_t ahead, Epi<BOXES>& es) {
+  const uint32_t h = BOXES == 2 ? es.box ^ ahead : 0;
   if (lane == 0) {
     bulk_wait_read0();
-    mbar_expect_tx(bar, BOX_BYTES);
-    tma_load_2d(box, map, bar, c0, c1);
+    mbar_expect_tx(bar + 8 * h, BOX_BYTES);
+    tma_load_2d(buf + h * BOX_BYTES, map, bar + 8 * h, c0, c1);
   }
-  es.pending = true;
+  es.pending[h] = true;
   __syncwarp();
 }
 // 128 columns of a row of acc or dW, stored or added to what is there, a box of 128 bytes a row at a time.
-template <bool BF16>
+template <bool BF16, int BOXES>
 __device__ __forceinline__ bool grads_epilogue(const CUtensorMap* map, int row0, int col, int d, bool add, int lane,
-                                               uint32_t box, uint32_t bar, Epi& es, float (&v)[HALF], float scale,
+                                               uint32_t buf, uint32_t bar, Epi<BOXES>& es, float (&v)[HALF], float scale,
                                                uint32_t* err, volatile int* abort_flag) {
   constexpr int W = BF16 ? 64 : 32;  // columns of a box
 #pragma unroll
   for (int c = 0; c < HALF; c += W) {
     if (col + c >= d) break;
+    const uint32_t h = es.box, box = buf + h * BOX_BYTES;
     if (add) {
-      if (!es.pending) fetch_box(map, box, bar, col + c, row0, lane, es);
-      if (!mbar_wait(bar, es.uses & 1u, abort_flag, err, 962)) return false;
-      ++es.uses;
-      es.pending = false;
+      if (!es.pending[h]) fetch_box<BOXES>(map, buf, bar, col + c, row0, lane, 0, es);
+      if (BOXES == 2 && c + W < HALF && col + c + W < d) fetch_box<BOXES>(map, buf, bar, col + c + W, row0, lane, 1, es);
+      if (!mbar_wait(bar + 8 * h, es.uses[h] & 1u, abort_flag, err, 962)) return false;
+      ++es.uses[h];
+      es.pending[h] = false;
     } else {
-      wait_box(lane);
+      wait_box<BOXES>(lane);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -350,24 +374,26 @@ __device__ __forceinline__ bool grads_epilogue(const CUtensorMap* map, int row0,
       sts128(at, pack(x));
     }
     store_box(map, box, col + c, row0, lane);
+    es.next();
   }
   return true;
 }
 
 // ------------------------------ the kernel --------------------------------- //
-template <int KIND>
+template <int KIND, bool SHORT>
 __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_constant__ Maps maps,
                                                              const __grid_constant__ TcArgs a) {
+  constexpr int NST = Shape<SHORT>::NST, BOXES = Shape<SHORT>::BOXES;
   extern __shared__ uint8_t smem_raw[];
   // the same offsets in both CTAs of the pair: the MMA reads both at these addresses
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + CTRL_OFF);  // [NST] (used in the first CTA)
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + Shape<SHORT>::CTRL_OFF);  // [NST] (used in the first CTA)
   uint64_t* empty_bar = full_bar + NST;                               // [NST]
   uint64_t* tfull_bar = empty_bar + NST;                              // [2]
   uint64_t* tempty_bar = tfull_bar + 2;                               // [2] (used in the first CTA)
   uint64_t* drain_bar = tempty_bar + 2;
-  uint64_t* load_bar = drain_bar + 1;                                 // [EPI_WARPS]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(load_bar + EPI_WARPS);
+  uint64_t* load_bar = drain_bar + 1;                                 // [EPI_WARPS][BOXES]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(load_bar + BOXES * EPI_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_ok = reinterpret_cast<int*>(tmem_slot + 2);
 
@@ -385,7 +411,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
       mbar_init(smem_addr(&tempty_bar[i]), 2 * EPI_WARPS);
     }
     mbar_init(smem_addr(drain_bar), 1);
-    for (int i = 0; i < EPI_WARPS; ++i) mbar_init(smem_addr(&load_bar[i]), 1);
+    for (int i = 0; i < BOXES * EPI_WARPS; ++i) mbar_init(smem_addr(&load_bar[i]), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -521,9 +547,9 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
     const int side = (warp - 2) / 4 * HALF;   // and its columns
     const int ew = warp - 2;
-    const uint32_t buf = smem_base + EPI_OFF + ew * BOX_BYTES;
-    const uint32_t lbar = smem_addr(&load_bar[ew]);
-    Epi es{0u, false};
+    const uint32_t buf = smem_base + Shape<SHORT>::EPI_OFF + ew * BOXES * BOX_BYTES;
+    const uint32_t lbar = smem_addr(&load_bar[BOXES * ew]);
+    Epi<BOXES> es{};
     uint32_t uses = 0;  // accumulators taken so far
     Tile t;
     for (int j = 0; tile_of<KIND>(deal, pair, npairs, stages, j, &t); ++j) {
@@ -533,7 +559,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
       const bool add = KIND == GRADS && (t.what == 0 ? a.add_acc : a.add_dw);
       const bool wanted = KIND != GRADS || ((t.what == 0 || orow < a.w.V) && col < a.w.d);
       const int total = t.blocks * a.seg[KIND == GRADS ? t.what : 0].n;
-      if (add && wanted && total > 0) fetch_box(map, buf, lbar, col, orow, lane, es);
+      if (add && wanted && total > 0) fetch_box<BOXES>(map, buf, lbar, col, orow, lane, 0, es);
       RowData rd{};
       if (KIND != GRADS) rd.label = a.w.label[row0 + lane];
       if (KIND == DLOGITS) {
@@ -575,21 +601,22 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
       if (KIND == LOGITS) {
         logits_epilogue(a.w, row0 + lane, col, rd, v);
       } else if (KIND == DLOGITS) {
-        dlogits_epilogue(maps, a.w, row0 + lane, col, lane, buf, rd, v);
+        dlogits_epilogue<BOXES>(maps, a.w, row0 + lane, col, lane, buf, es, rd, v);
       } else if (wanted && (total > 0 || !add)) {  // no labelled tokens: dW is 0, or as it was
         const float scale = t.what == 1 && a.w.mean && n > 0 ? 1.f / (float)n : 1.f;
         if (t.what == 1 && a.dw_bf16)
-          ok = grads_epilogue<true>(map, orow, col, a.w.d, add, lane, buf, lbar, es, v, scale, a.w.err,
+          ok = grads_epilogue<true, BOXES>(map, orow, col, a.w.d, add, lane, buf, lbar, es, v, scale, a.w.err,
                                     abort_flag);
         else
-          ok = grads_epilogue<false>(map, orow, col, a.w.d, add, lane, buf, lbar, es, v, scale, a.w.err, abort_flag);
+          ok = grads_epilogue<false, BOXES>(map, orow, col, a.w.d, add, lane, buf, lbar, es, v, scale, a.w.err, abort_flag);
         if (!ok) break;
       }
     }
-    // an input load still in flight (only after an abort), then every store
-    if (es.pending)
-      for (uint32_t it = 0; it < (1u << 24) && !mbar_try_wait(lbar, es.uses & 1u); ++it) {
-      }
+    // input loads still in flight (only after an abort), then every store
+    for (int h = 0; h < BOXES; ++h)
+      if (es.pending[h])
+        for (uint32_t it = 0; it < (1u << 24) && !mbar_try_wait(lbar + 8 * h, es.uses[h] & 1u); ++it) {
+        }
     if (lane == 0) bulk_wait_all();
   }
   __syncwarp();
@@ -640,7 +667,7 @@ Segs segs(int pa, int pb, int la, int lb) {
   return s;
 }
 
-template <int KIND>
+template <int KIND, bool SHORT>
 cudaError_t launch(const Maps& maps, const TcArgs& args, int64_t tiles, int kind, cudaStream_t st) {
   struct PerDevice {
     bool ready;
@@ -659,16 +686,17 @@ cudaError_t launch(const Maps& maps, const TcArgs& args, int64_t tiles, int kind
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
+  cfg.dynamicSmemBytes = Shape<SHORT>::SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(2);
   if (!per[dev].ready) {
-    const cudaError_t e = cudaFuncSetAttribute(loss_tc_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(loss_tc_kernel<KIND, SHORT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Shape<SHORT>::SMEM);
     if (e != cudaSuccess) return e;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, loss_tc_kernel<KIND>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, loss_tc_kernel<KIND, SHORT>, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
       n = sm_count() / 2;
     }
@@ -679,7 +707,7 @@ cudaError_t launch(const Maps& maps, const TcArgs& args, int64_t tiles, int kind
   cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, per[dev].pairs)));
   cfg.numAttrs = 2;
   LaunchScope ls(kind, st);
-  return cudaLaunchKernelEx(&cfg, loss_tc_kernel<KIND>, maps, args);
+  return cudaLaunchKernelEx(&cfg, loss_tc_kernel<KIND, SHORT>, maps, args);
 }
 
 template <int KIND>
@@ -694,7 +722,10 @@ cudaError_t logits(const LossWork& w, cudaStream_t st) {
   if (KIND == DLOGITS) ok = ok && make_map(&maps.m[2], w.dz, (uint64_t)w.dzp * w.Tp, w.piece, 64, 32);
   if (!ok) return cudaErrorInvalidValue;
   const int64_t cols = KIND == LOGITS ? (w.V + BN - 1) / BN : w.piece / BN;
-  return launch<KIND>(maps, a, (int64_t)(w.Tp / (2 * BM)) * cols, KIND == LOGITS ? KK_LOSS_LOGITS : KK_LOSS_DLOGITS, st);
+  const int64_t tiles = (int64_t)(w.Tp / (2 * BM)) * cols;
+  if (KIND == LOGITS) return launch<KIND, false>(maps, a, tiles, KK_LOSS_LOGITS, st);
+  return (w.d + 127) / 128 * a.seg[0].n <= SHORT_K ? launch<KIND, true>(maps, a, tiles, KK_LOSS_DLOGITS, st)
+                                                  : launch<KIND, false>(maps, a, tiles, KK_LOSS_DLOGITS, st);
 }
 
 }  // namespace
@@ -724,7 +755,8 @@ cudaError_t tc_loss_grads(const LossWork& w, bool dx, void* dW, bool dw_bf16, bo
   if (!ok) return cudaErrorInvalidValue;
   const int64_t cols = (w.d + BN - 1) / BN;
   const int64_t tiles = ((dx ? (int64_t)w.Tp / (2 * BM) * w.slices : 0) + (dW ? w.piece / BN : 0)) * cols;
-  return launch<GRADS>(maps, a, tiles, KK_LOSS_GRADS, st);
+  return dW && w.Tp / 128 * a.seg[1].n <= SHORT_K ? launch<GRADS, true>(maps, a, tiles, KK_LOSS_GRADS, st)
+                                                 : launch<GRADS, false>(maps, a, tiles, KK_LOSS_GRADS, st);
 }
 
 }  // namespace moe
