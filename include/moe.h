@@ -376,7 +376,8 @@ moe_status moe_dropout_bwd(int64_t n, int32_t dtype, const void* dout, void* dy,
  * the loss at the end of the stack, and the clipping of the accumulated
  * gradients.  (The pages have no counterpart.)  Conventions as above: dense
  * rows, tensors of `dtype` 16-byte aligned unless a parameter says otherwise,
- * float32 vectors 4-byte aligned. */
+ * float32 vectors 4-byte aligned.  A workspace's contents are of one call alone;
+ * calls that may overlap want one each. */
 
 /* The residual path between two blocks, per row t and channel c:
  *   u   = y * ry * gamma_post,  ry = 1 / sqrt(sum(y^2) / d + eps)     (gamma_post NULL: u = y)

@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gb300.so")
 SOURCES = ["moe_api.cu", "routing.cu", "rows.cu", "gemm_simt.cu", "gemm_tc.cu", "noalloc.cu", "router_tc.cu", "selftest.cu", "dwr_tc.cu", "aux_loss.cu",
            "block_api.cu", "norm.cu", "dropout.cu", "decode.cu", "decode_tc.cu",
-           "step_api.cu", "residual_norm.cu", "clip.cu", "vocab_loss.cu", "vocab_loss_tc.cu"]
+           "step_api.cu", "residual_norm.cu", "clip.cu", "vocab_loss.cu", "vocab_loss_tc.cu", "vocab_loss_few.cu"]
 HEADERS = ["internal.h", "block.h", "step.h", "vocab_loss.h", "decode.cuh", "row_ring.cuh", "common.cuh", "tc_ptx.cuh", os.path.join("..", "..", "include", "moe.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -18,6 +18,7 @@
 // loop, again from cache for each pass.  There the columns' sums are taken in a
 // pass of their own before anything is written (dx and dy may be dh or dout).
 #include <algorithm>
+#include <atomic>
 
 #include "row_ring.cuh"
 #include "step.h"
@@ -847,7 +848,7 @@ Grid grid_of(int64_t rows, int d, int es, int bufs, bool bwd) {
 }
 
 template <typename K>
-cudaError_t launch_ring(K kernel, const Grid& g, JoinK& a, bool* attr_done, cudaStream_t st) {
+cudaError_t launch_ring(K kernel, const Grid& g, JoinK& a, std::atomic<bool>* attr_done, cudaStream_t st) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
@@ -864,12 +865,12 @@ cudaError_t launch_ring(K kernel, const Grid& g, JoinK& a, bool* attr_done, cuda
 }
 template <typename T, bool WHOLE, bool BRANCH, bool FOLLOWING>
 cudaError_t fwd_ring(const Grid& g, JoinK& a, cudaStream_t st) {
-  static bool done[64] = {false};
+  static std::atomic<bool> done[64];
   return launch_ring(join_fwd_kernel<T, WHOLE, BRANCH, FOLLOWING>, g, a, done, st);
 }
 template <typename T, bool WHOLE, bool BRANCH, bool FOLLOWING, bool DOUT>
 cudaError_t bwd_ring(const Grid& g, JoinK& a, cudaStream_t st) {
-  static bool done[64] = {false};
+  static std::atomic<bool> done[64];
   return launch_ring(join_bwd_kernel<T, WHOLE, BRANCH, FOLLOWING, DOUT>, g, a, done, st);
 }
 template <typename T, bool WHOLE>

@@ -1,6 +1,6 @@
-// What the two halves of the vocabulary loss share: the token lists and
-// epilogue data that vocab_loss.cu prepares, and the products of
-// vocab_loss_tc.cu.
+// What the parts of the vocabulary loss share: the token lists and epilogue data
+// that vocab_loss.cu prepares, the products of vocab_loss_tc.cu, and the form
+// for few tokens.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -13,6 +13,12 @@ constexpr int LOSS_TILE = 256;   // rows and columns of a product's tile
 constexpr int LOSS_PART = 128;   // columns of a partial sum of the forward
 constexpr int MAX_PARTS = 3;     // bf16 parts of a float32 value
 
+// ---- vocab_loss_few.cu: the forward of at most LOSS_FEW bf16 tokens, in the workspace's first bytes ----
+constexpr int LOSS_FEW = 64;
+size_t loss_few_bytes();
+cudaError_t launch_loss_few(const LossArgs& a, uint32_t* err, cudaStream_t st);
+
+// ---- vocab_loss_tc.cu ----
 // Labelled tokens only, in token order, padded with zero rows to a whole tile.
 struct LossWork {
   int32_t* list;    // [T]: the labelled tokens

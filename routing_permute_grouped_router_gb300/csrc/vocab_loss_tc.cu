@@ -29,6 +29,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -669,11 +670,7 @@ Segs segs(int pa, int pb, int la, int lb) {
 
 template <int KIND, bool SHORT>
 cudaError_t launch(const Maps& maps, const TcArgs& args, int64_t tiles, int kind, cudaStream_t st) {
-  struct PerDevice {
-    bool ready;
-    int pairs;
-  };
-  static PerDevice per[64] = {};
+  static std::atomic<int> pairs_of[64];  // pairs that are resident at once, 0 where it has not been asked
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
@@ -691,20 +688,19 @@ cudaError_t launch(const Maps& maps, const TcArgs& args, int64_t tiles, int kind
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(2);
-  if (!per[dev].ready) {
+  int pairs = pairs_of[dev].load(std::memory_order_acquire);
+  if (pairs == 0) {
     const cudaError_t e = cudaFuncSetAttribute(loss_tc_kernel<KIND, SHORT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Shape<SHORT>::SMEM);
     if (e != cudaSuccess) return e;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, loss_tc_kernel<KIND, SHORT>, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&pairs, loss_tc_kernel<KIND, SHORT>, &cfg) != cudaSuccess || pairs <= 0) {
       cudaGetLastError();
-      n = sm_count() / 2;
+      pairs = sm_count() / 2;
     }
-    per[dev].pairs = n;
-    per[dev].ready = true;
+    pairs_of[dev].store(pairs, std::memory_order_release);
   }
   if (tiles <= 0) return cudaSuccess;
-  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, per[dev].pairs)));
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, pairs)));
   cfg.numAttrs = 2;
   LaunchScope ls(kind, st);
   return cudaLaunchKernelEx(&cfg, loss_tc_kernel<KIND, SHORT>, maps, args);
