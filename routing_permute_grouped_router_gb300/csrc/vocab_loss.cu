@@ -131,22 +131,25 @@ __global__ void __launch_bounds__(ROW_NT) loss_pack_kernel(const LossWork w, con
       if (w.pos[t] < 0) a.loss[t] = a.lse_out[t] = 0.f;
 }
 
-// The parts of a float32 W, zeros up to ldw.  Infinities count as the largest
-// bf16: as one part they would meet the zeros of the other operand's parts.
+// The parts of a float32 W, zeros up to ldw, a warp a row.  Infinities count as
+// the largest bf16: as one part they would meet the zeros of the other operand's
+// parts.
 __global__ void __launch_bounds__(ROW_NT) loss_split_kernel(const LossWork w, const float* W, __nv_bfloat16* out) {
   pdl_enter();
-  const int64_t vecs = w.ldw / 4, all = vecs * w.V;
-  for (int64_t i = (int64_t)blockIdx.x * ROW_NT + threadIdx.x; i < all; i += (int64_t)gridDim.x * ROW_NT) {
-    const int64_t row = i / vecs;
-    const int c = (int)(i - row * vecs) * 4;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (c < w.d) u = ldg16(W + row * w.d + c);
-    float v[4];
-    unpack(u, v);
+  for (int row = blockIdx.x * (ROW_NT / 32) + threadIdx.x / 32; row < w.V; row += gridDim.x * (ROW_NT / 32)) {
+    const float* src = W + (int64_t)row * w.d;
+    __nv_bfloat16* dst = out + (int64_t)row * MAX_PARTS * w.ldw;
+#pragma unroll 4
+    for (int c = threadIdx.x % 32 * 4; c < w.ldw; c += 128) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (c < w.d) u = ldg16(src + c);
+      float v[4];
+      unpack(u, v);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (isinf(v[j])) v[j] = copysignf(0x1.fep127f, v[j]);
-    put_parts(out + row * MAX_PARTS * w.ldw + c, w.ldw, v);
+      for (int j = 0; j < 4; ++j)
+        if (isinf(v[j])) v[j] = copysignf(0x1.fep127f, v[j]);
+      put_parts(dst + c, w.ldw, v);
+    }
   }
 }
 
@@ -334,7 +337,7 @@ cudaError_t prepare(LossWork* w, const LossArgs& a, const PackArgs& p, cudaStrea
     w->wp = static_cast<const __nv_bfloat16*>(a.W);
     return cudaSuccess;
   }
-  LAUNCH(KK_LOSS_ROWS, loss_split_kernel, dim3(few((int64_t)w->V * (w->ldw / 4) / ROW_NT + 1, 16)), dim3(ROW_NT), 0, st,
+  LAUNCH(KK_LOSS_ROWS, loss_split_kernel, dim3(few((w->V + ROW_NT / 32 - 1) / (ROW_NT / 32), 16)), dim3(ROW_NT), 0, st,
          *w, static_cast<const float*>(a.W), const_cast<__nv_bfloat16*>(w->wp));
   return cudaSuccess;
 }
