@@ -151,10 +151,11 @@ class MoEStack:
         if n == 0 or len(gammas) != n + 1 or any(v is not None and len(v) != n for v in (posts, gates)):
             raise ValueError("a stack of n layers has n + 1 norms, and n norms and n gates behind the layers or none")
         first = self.layers[0]
-        shape = [f for f, _ in MoeConfig._fields_ if f in ("T", "d_model", "dtype")]
-        if any(getattr(l.cfg, f) != getattr(first.cfg, f) for l in self.layers for f in shape) or any(
-                l.training != first.training for l in self.layers):
+        alike = lambda l: (l.cfg.T, l.cfg.d_model, l.cfg.dtype, l.training)  # noqa: E731
+        if any(alike(l) != alike(first) for l in self.layers):
             raise ValueError("the layers of a stack have the same tokens, width, type and training flag")
+        if len({id(l) for l in self.layers}) != n:  # each keeps its own output and state for the backward
+            raise ValueError("a layer is in the stack twice: build two on the same weights")
         self.gammas = [g.contiguous() for g in gammas]
         self.posts = [None] * n if posts is None else [p.contiguous() for p in posts]
         self.gates = [None] * n if gates is None else [g.contiguous() for g in gates]
@@ -173,7 +174,7 @@ class MoEStack:
         if self.head is not None:
             self.loss, self.lse, self.total = torch.empty(T, **f32), torch.empty(T, **f32), torch.empty(2, **f32)
             self.loss_ws = vocab_loss_workspace(T, d, self.head.shape[0], first.act_dtype, self.training, dev)
-        self._decode = {}  # (stream, tokens) -> config, s, h, y and workspace
+        self._decode = {}  # (stream, tokens) -> configs, s, h, y, out and workspace
         self._decode_ws = {}  # stream -> workspace, large enough for any number of tokens and layer
         if not self.training:
             return
@@ -247,15 +248,16 @@ class MoEStack:
         if key not in self._decode:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
                 self._decode[key] = self._decode_buffers(*key)
-        cfgs, s, h, y, ws = self._decode[key]
+        cfgs, s, h, y, out, ws = self._decode[key]
         moe_residual_norm_fwd(x, None, None, h, None, self.gammas[0], eps=self.eps, stream=stream)
-        before = x
+        before, last = x, len(self.layers) - 1
         for i, layer in enumerate(self.layers):
             moe_layer_decode(cfgs[i], layer.weights, h, None, y, None, None, ws, stream)
-            moe_residual_norm_fwd(before, y, s, h, self.posts[i], self.gammas[i + 1], self.gates[i], None,
-                                  self.residual_scale, self.branch_scale, self.eps, stream=stream)
+            # x may be the last call's result: nothing but the last path writes there
+            moe_residual_norm_fwd(before, y, s, out if i == last else h, self.posts[i], self.gammas[i + 1], self.gates[i],
+                                  None, self.residual_scale, self.branch_scale, self.eps, stream=stream)
             before = s
-        return h if h.shape == x.shape else h.view(x.shape)
+        return out if out.shape == x.shape else out.view(x.shape)
 
     def _decode_buffers(self, raw_stream: int, T: int):
         cfgs = [_tokens(l.cfg, T) for l in self.layers]
@@ -266,8 +268,8 @@ class MoEStack:
         if ws is None:
             size = max(moe_decode_workspace_size(_tokens(l.cfg, t)) for l in self.layers for t in range(1, MOE_DECODE_MAX_T + 1))
             ws = self._decode_ws[raw_stream] = torch.empty(size, dtype=torch.uint8, device=first.device)
-        s, h, y = (torch.empty(T, first.cfg.d_model, dtype=first.act_dtype, device=first.device) for _ in range(3))
-        return cfgs, s, h, y, ws
+        rows = [torch.empty(T, first.cfg.d_model, dtype=first.act_dtype, device=first.device) for _ in range(4)]
+        return (cfgs, *rows, ws)
 
 
 def _tokens(c: MoeConfig, T: int) -> MoeConfig:

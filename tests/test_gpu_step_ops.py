@@ -107,7 +107,8 @@ def check_bwd(r, e, add=None):
 
 
 SHAPES = [(1, 1), (1, 4096), (3, 7), (5, 8), (16, 4096), (33, 512), (129, 1000), (333, 2048), (7, 8192), (64, 520),
-          (2, 8200), (3, 16384), (5, 9001), (1, 65536), (1030, 96), (4099, 1021)]
+          (2, 8200), (3, 16384), (5, 9001), (1, 65536), (1030, 96), (4099, 1021), (9, 7001), (310, 6888), (700, 1007), (155, 8191),
+          (17, 33), (1200, 31), (400, 2047)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -181,6 +182,24 @@ def test_join_rows_of_zeros_and_non_finite_rows():
                 near(n, r[n][ok], v[ok], rel=2 * STAT, big=8 * U)
             assert (r["h"][2] == 0).all() and r["h"][4].isnan().all()
             torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("d", [520, 1021, 1023, 4090, 9000])
+def test_join_neighbours_of_a_row_do_not_reach_it(d):
+    """Rows of NaN between the others: what copies bring of them beside a row is left out, and sums go by row."""
+    for t in TYPES.values():
+        i = join_inputs(641, d, t, seed=61, row=True)
+        clean = {n: None if v is None else v.clone() for n, v in i.items()}
+        i["x"][1::2], i["y"][1::2] = float("nan"), float("inf")
+        r, e = run_fwd(i, 0.8, 0.5), run_fwd(clean, 0.8, 0.5)
+        assert all(torch.equal(r[n][::2], e[n][::2]) for n in r)
+        dh, dout = rand(641, d, seed=8, dtype=t), rand(641, d, seed=9, dtype=t)
+        a = run_bwd(clean, e, dh, dout, 0.8, 0.5)
+        dh[1::2], dout[1::2] = float("nan"), float("nan")
+        b = run_bwd(i, r, dh, dout, 0.8, 0.5)
+        for n in ("dx", "dy", "drow_gate"):
+            assert torch.equal(a[n][::2], b[n][::2]), n
+    torch.cuda.synchronize()
 
 
 def test_join_no_rows():

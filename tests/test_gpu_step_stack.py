@@ -159,6 +159,25 @@ def test_stack_decode(kind):
     check_no_device_error()
 
 
+@pytest.mark.parametrize("n", [1, 2])
+def test_stack_decode_of_its_own_result(n):
+    """The buffer that a call returns is the next call's input; and calls on two streams keep apart."""
+    stack, x, _ = make("f32", n=n, training=False)
+    first = stack.decode(x[:8].contiguous()).clone()
+    again = stack.decode(first.clone()).clone()
+    out = stack.decode(x[:8].contiguous())
+    assert torch.equal(stack.decode(out), again)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = stack.decode(x[:8].contiguous(), s)
+    here = stack.decode(first)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(other, first) and torch.equal(here, again) and other.data_ptr() != here.data_ptr()
+    assert stack.decode(x[:0]).shape == (0, 64)
+    check_no_device_error()
+
+
 def test_stack_of_no_tokens():
     stack, x, labels = make("f32", T=0)
     assert stack.forward_loss(x, labels).tolist() == [0.0, 0.0]
@@ -177,6 +196,11 @@ def test_stack_refuses():
         L.MoEStack(stack.layers, stack.gammas[:2])
     with pytest.raises(ValueError, match="same tokens"):
         L.MoEStack([stack.layers[0], make("f32", T=5)[0].layers[0]], stack.gammas)
+    with pytest.raises(ValueError, match="twice"):
+        L.MoEStack([stack.layers[0], stack.layers[0]], stack.gammas)
+    for bad, err in ((x.half(), TypeError), (x[:65].repeat(3, 1), pkg.MoeError)):
+        with pytest.raises(err):
+            stack.decode(bad)
     bare = L.MoEStack(stack.layers, stack.gammas)
     with pytest.raises(RuntimeError, match="without a head"):
         bare.forward_loss(x, labels)
