@@ -26,7 +26,10 @@
 namespace moe {
 namespace {
 
-constexpr int FWD_REGS = 80;   // a thread's in the forward: three CTAs of 256 fit an SM
+// A thread's registers in the forward: three CTAs of 256 fit an SM with 80, two
+// with 96.  (32768 x 4096 bf16 178 us with 80, 169 with 96; 16384 x 8192 197 and
+// 170; 32768 x 2048 97 and 101; 16384 x 4096 float32 175 and 184.)
+constexpr int fwd_regs(int es) { return es == 2 ? 96 : 80; }
 constexpr int BWD_NT = 512;    // most threads of the backward's CTAs, one an SM
 constexpr int MAX_GROUPS = BWD_NT / 32;
 constexpr int BWD_SMEM = 230400;  // a CTA's dynamic shared memory there: 227 KB less its static part
@@ -266,7 +269,7 @@ __device__ __forceinline__ void begin(JoinRows<T, WHOLE>& R, const JoinK& a, uin
 // BRANCH: there is a y; FOLLOWING: there is an h.  (As run-time flags they cost
 // branches in every chunk of a row: the backward 371 us at 32768 x 4096 bf16, not 347.)
 template <typename T, bool WHOLE, bool BRANCH, bool FOLLOWING>
-__global__ void __maxnreg__(FWD_REGS) join_fwd_kernel(const JoinK a) {
+__global__ void __maxnreg__(fwd_regs(sizeof(T))) join_fwd_kernel(const JoinK a) {
   constexpr int CN = Mine<T, WHOLE>::CN;
   __shared__ float scratch[2][2][16];
   __shared__ uint64_t bars[MAX_GROUPS * RING];
@@ -831,7 +834,7 @@ Grid grid_of(int64_t rows, int d, int es, int bufs, bool bwd) {
   g.tpr = threads_per_row(most_units * 16 / es);
   g.slot = whole ? most_units * 16 : (most_units * 16 + 112 + 127) / 128 * 128;
   const size_t place = (size_t)bufs * g.slot, weights = bwd ? 2 * EPT * g.tpr * 4 : 0;
-  int groups = bwd ? BWD_NT / g.tpr : (g.tpr == 32 ? 4 : 1), per = bwd ? 1 : 65536 / (g.tpr * groups * FWD_REGS);
+  int groups = bwd ? BWD_NT / g.tpr : (g.tpr == 32 ? 4 : 1), per = bwd ? 1 : 65536 / (g.tpr * groups * fwd_regs(es));
   const size_t room = bwd ? BWD_SMEM - weights : SMEM_SM;
   if (bwd) groups = std::max(1, std::min(groups, (int)(room / (2 * place))));
   while (per > 1 && per * 2 * (groups * place + 1024) > room) --per;
