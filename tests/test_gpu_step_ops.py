@@ -650,6 +650,32 @@ def test_loss_past_32_bits_of_elements():
     check_no_device_error()
 
 
+@pytest.mark.parametrize("T", [40, 70])
+def test_loss_weights_past_32_bits_of_elements(T):
+    d, V = 4096, 560000
+    W = torch.empty(V, d, dtype=torch.bfloat16, device="cuda")
+    for i, part in enumerate(W.split(70000)):
+        part.copy_(rand(part.shape[0], d, seed=100 + i, scale=d ** -0.5))
+    x = rand(T, d, seed=99, dtype=torch.bfloat16)
+    labels = torch.randint(V - 1000, V, (T,), device="cuda", dtype=torch.int32)
+    loss, lse, _ = run_loss(x, W, labels)
+    z = torch.cat([x.double() @ part.double().t() for part in W.split(70000)], 1)
+    e_lse = torch.logsumexp(z, 1)
+    tol = 2 * float(logit_error(x, W[:4096]).max()) * 1.5 + 64 * U
+    near("lse", lse, e_lse, rel=4 * U, tol=tol)
+    near("loss", loss, e_lse - z.gather(1, labels.long()[:, None])[:, 0], rel=4 * U, tol=tol)
+    dz = torch.exp(z - lse.double()[:, None])
+    dz[torch.arange(T, device="cuda"), labels.long()] -= 1
+    dz /= T
+    gx, gW = run_loss_bwd(x, W, labels, lse, None, torch.bfloat16)
+    for at in (0, V - 3000):
+        e = dz[:, at:at + 3000].t() @ x.double()
+        assert float((gW[at:at + 3000].double() - e).norm()) <= (2.0 ** -7 + tol) * float(e.norm())
+    e = sum(a @ b.double() for a, b in zip(dz.split(70000, 1), W.split(70000)))
+    assert float((gx.double() - e).norm()) <= (2.0 ** -7 + tol) * float(e.norm())
+    check_no_device_error()
+
+
 @pytest.mark.parametrize("T", [8, 300])
 def test_loss_captured_and_on_another_stream(T):
     x, W, labels = loss_inputs(T, 512, 2000, torch.bfloat16, 0.2, seed=15)
