@@ -700,3 +700,75 @@ def test_loss_captured_and_on_another_stream(T):
         g.replay()
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(o, (loss, lse, tot, gx, gW)))
+
+
+# ----------------------------- all of them -------------------------------- #
+def test_step_ops_from_new_threads():
+    """Several host threads whose first CUDA calls these are, each on a stream of its own."""
+    import threading
+
+    i = join_inputs(300, 520, torch.bfloat16, seed=71)
+    x, W, labels = loss_inputs(300, 520, 1000, torch.bfloat16, 0.1, seed=72)
+    src = [rand(5000, seed=73)]
+    torch.cuda.synchronize()
+    got, failed = {}, []
+
+    def work(k):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                a = run_fwd(i)
+                b = run_bwd(i, a, i["x"], i["y"], 1.0, 1.0)
+                loss, lse, _ = run_loss(x, W, labels)
+                few, _, _ = run_loss(x[:20].contiguous(), W, labels[:20].contiguous())
+                g = run_loss_bwd(x, W, labels, lse, None, torch.float32)
+                out = [torch.empty_like(src[0])]
+                norm = torch.zeros(1, device="cuda")
+                pkg.moe_clip_grads(pkg.grad_list(src, out), 1.0, norm, pkg.clip_workspace(1))
+            s.synchronize()
+            got[k] = [a["out"], a["h"], b["dx"], b["dy"], b["dgate"], loss, lse, few, *g, norm, *out]
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for k in range(1, 4):
+        assert all(torch.equal(a, b) for a, b in zip(got[0], got[k]))
+    check_no_device_error()
+
+
+def test_step_ops_refuse_views_types_and_places():
+    x = rand(8, 64, seed=1, dtype=torch.bfloat16)
+    g, f, i32 = rand(64, seed=2), rand(8, seed=3), torch.zeros(8, dtype=torch.int32, device="cuda")
+    wide = rand(8, 128, seed=4, dtype=torch.bfloat16)
+    W, ws = rand(100, 64, seed=5, dtype=torch.bfloat16), pkg.vocab_loss_workspace(8, 64, 100, torch.bfloat16, True)
+    with pytest.raises(ValueError, match="contiguous"):
+        pkg.moe_residual_norm_fwd(x, wide[:, ::2], x.clone(), None)
+    with pytest.raises(TypeError, match="y has type"):
+        pkg.moe_residual_norm_fwd(x, x.float(), x.clone(), None)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkg.moe_residual_norm_fwd(x, x.cpu(), x.clone(), None)
+    with pytest.raises(ValueError, match="gate has"):
+        pkg.moe_residual_norm_fwd(x, x.clone(), x.clone(), None, gate=f)
+    flat = rand(8 * 64 + 8, seed=6, dtype=torch.bfloat16)
+    with pytest.raises(pkg.MoeError, match="ALIGNMENT"):
+        pkg.moe_residual_norm_fwd(flat[1:513].view(8, 64), x, x.clone(), None)
+    with pytest.raises(TypeError, match="labels has type"):
+        pkg.moe_vocab_loss_fwd(x, W, i32.long(), f, f.clone(), ws)
+    with pytest.raises(ValueError, match="labels has"):
+        pkg.moe_vocab_loss_fwd(x, W, i32[:7], f, f.clone(), ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        pkg.moe_vocab_loss_fwd(x, rand(64, 100, seed=7, dtype=torch.bfloat16).t(), i32, f, f.clone(), ws)
+    with pytest.raises(pkg.MoeError, match="WORKSPACE"):
+        pkg.moe_vocab_loss_bwd(x, W, i32, f, None, x.clone(), None, False, ws[:1000])
+    with pytest.raises(TypeError, match="dW has type"):
+        pkg.moe_vocab_loss_bwd(x, W, i32, f, None, None, W.half(), False, ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        pkg.grad_list([wide[:, :3]])
+    with pytest.raises(pkg.MoeError, match="INVALID_ARG"):
+        pkg.moe_clip_grads(pkg.grad_list([g, g], [g, g]), 1.0, f[:1].clone(), pkg.clip_workspace(2))
+    check_no_device_error()
