@@ -347,7 +347,7 @@ cudaError_t prepare(LossWork* w, const LossArgs& a, const PackArgs& p, cudaStrea
 size_t loss_ws_bytes(int T, int d, int V, bool bf16, bool training) {
   if (T == 0) return 0;
   LossWork w{};
-  const size_t fwd = bf16 && T <= LOSS_FEW ? loss_few_bytes() : lay_out(&w, nullptr, T, d, V, bf16, false, 0);
+  const size_t fwd = loss_is_few(T, d, bf16) ? loss_few_bytes() : lay_out(&w, nullptr, T, d, V, bf16, false, 0);
   if (!training) return fwd;
   size_t most = fwd;
   for (int dzp = bf16 ? 1 : MAX_PARTS; dzp <= (bf16 ? 2 : MAX_PARTS); ++dzp)
@@ -356,7 +356,7 @@ size_t loss_ws_bytes(int T, int d, int V, bool bf16, bool training) {
 }
 
 cudaError_t launch_loss_fwd(const LossArgs& a, uint32_t* err, cudaStream_t st) {
-  if (a.bf16 && a.T <= LOSS_FEW) return launch_loss_few(a, err, st);
+  if (loss_is_few(a.T, a.d, a.bf16)) return launch_loss_few(a, err, st);
   LossWork w{};
   w.err = err;
   lay_out(&w, static_cast<char*>(a.ws), a.T, a.d, a.V, a.bf16, false, 0);

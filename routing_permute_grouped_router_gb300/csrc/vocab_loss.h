@@ -13,8 +13,9 @@ constexpr int LOSS_TILE = 256;   // rows and columns of a product's tile
 constexpr int LOSS_PART = 128;   // columns of a partial sum of the forward
 constexpr int MAX_PARTS = 3;     // bf16 parts of a float32 value
 
-// ---- vocab_loss_few.cu: the forward of at most LOSS_FEW bf16 tokens, in the workspace's first bytes ----
+// ---- vocab_loss_few.cu: the forward of at most LOSS_FEW tokens, in the workspace's first bytes ----
 constexpr int LOSS_FEW = 64;
+bool loss_is_few(int T, int d, bool bf16);  // float32: fewer
 size_t loss_few_bytes();
 cudaError_t launch_loss_few(const LossArgs& a, uint32_t* err, cudaStream_t st);
 

@@ -1,4 +1,4 @@
-// The vocabulary loss of at most 64 bf16 tokens, as a serving step scores them.
+// The vocabulary loss of at most 64 bf16 or 48 float32 tokens, as a serving step scores them.
 //
 // The weights are read once and bound it.  They are the M side of the MMAs (128
 // words), the tokens the 16, 32 or 64 columns, so few tokens cost few MMA cycles:
@@ -11,6 +11,18 @@
 //
 // Sums over K of 1024 at a time are added up in TMEM and then, rounded, in
 // registers, as in the products of many tokens.
+//
+// Few float32 tokens take no tensor core: W's parts would have to be written and
+// read again, 12 bytes for each 4.  Groups of 8 tokens, or of fewer
+// where more do not fit in shared memory, have an equal share of the CTAs each; a
+// warp brings four words' weights from memory to its registers once and
+// multiplies them with each token's elements from shared memory.  The CTAs of
+// the groups that have the same words run side by side, so that the weights come
+// from HBM once and otherwise from L2.  128000 x 4096 at 1 and 8 tokens 293 and
+// 325 us (7.2 and 6.5 TB/s), at 16, 32 and 48 513, 957 and 1421: multiplications,
+// reads of shared memory and reads of L2 all count there.  The form for many takes 1837
+// for any of them, and 64 tokens would be 1860 here: six groups are the most.
+// 16 tokens in one group, with 64 sums a lane, are slower (2048 x 50257: 140 us, 115).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -59,6 +71,12 @@ __device__ __forceinline__ void add_logit(float& top, float& sum, float z) {
   const float e = exp_of(fminf(top, z) - best);  // 0 for a first one; NaN stays
   sum = z > top ? fmaf(sum, e, 1.f) : sum + (z == z ? e : z);
   top = best;
+}
+
+__device__ __forceinline__ uint4 ldg16_once(const float* p) {  // not to be read again
+  uint4 u;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+  return u;
 }
 
 template <int N>
@@ -257,6 +275,118 @@ __global__ void __launch_bounds__(THREADS, 1) loss_few_kernel(const __grid_const
   if (warp == 1) tmem_dealloc(tmem_base, COLS);
 }
 
+// ---- float32 ----
+constexpr int F32_NT = 512, F32_WARPS = F32_NT / 32, R = 4;  // words of a warp
+constexpr int F32_SMEM = 208 * 1024;                         // of the tokens' rows
+constexpr int F32_GROUPS = 6, F32_GROUPS_LONG = 12;          // of 8 tokens, of fewer
+
+// acc[n * R + r] = the lane's part of token n with word r; rows past the last word read it again.
+// CAP: infinities count as the largest bf16, as in the products of parts.
+template <int N, int U, bool CAP>
+__device__ __forceinline__ void dot_words(float (&acc)[N * R], const float* W, const float* xs, int d, int word, int V, int lane) {
+#pragma unroll
+  for (int i = 0; i < N * R; ++i) acc[i] = 0.f;
+  const float* src[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) src[r] = W + (int64_t)min(word + r, V - 1) * d;
+  for (int c0 = lane * 4; c0 < d; c0 += U * 128) {
+    uint4 u[U][R];
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+#pragma unroll
+      for (int r = 0; r < R; ++r) u[j][r] = c0 + j * 128 < d ? ldg16_once(src[r] + c0 + j * 128) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (c0 + j * 128 >= d) break;
+      float w[R][4];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        unpack(u[j][r], w[r]);
+        if constexpr (CAP) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (isinf(w[r][i])) w[r][i] = copysignf(0x1.fep127f, w[r][i]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const float4 x = *reinterpret_cast<const float4*>(xs + n * d + c0 + j * 128);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          acc[n * R + r] = fmaf(x.w, w[r][3], fmaf(x.z, w[r][2], fmaf(x.y, w[r][1], fmaf(x.x, w[r][0], acc[n * R + r]))));
+      }
+    }
+  }
+}
+// Sums over the lanes, halving what a lane has: it ends with those from lane * C / 32 on.
+template <int C, int O>
+__device__ __forceinline__ void add_lanes(float* v, int lane) {
+  if constexpr (O > 0) {
+    if constexpr (C > 1) {
+      const bool upper = lane & O;
+#pragma unroll
+      for (int i = 0; i < C / 2; ++i) {
+        const float keep = upper ? v[i + C / 2] : v[i], give = upper ? v[i] : v[i + C / 2];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, O);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], O);
+    }
+    add_lanes<(C > 1 ? C / 2 : 1), O / 2>(v, lane);
+  }
+}
+
+template <int N, int U>
+__global__ void __launch_bounds__(F32_NT, 1) loss_few_f32_kernel(const FewArgs a, const float* x, const float* W, int groups) {
+  extern __shared__ uint8_t smem_raw[];
+  float* xs = reinterpret_cast<float*>(smem_raw);  // [N][d], 0 for tokens that are ignored
+  __shared__ float2 s_sum[F32_WARPS][N];
+  pdl_enter();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, vecs = a.d / 4;
+  const int t0 = blockIdx.x % groups * N, place = blockIdx.x / groups, places = gridDim.x / groups;
+  for (int n = 0; n < N; ++n) {
+    const int label = t0 + n < a.T ? a.labels[t0 + n] : -1;
+    const bool valid = label >= 0 && label < a.V;
+    for (int i = threadIdx.x; i < vecs; i += F32_NT)
+      *reinterpret_cast<uint4*>(xs + n * a.d + i * 4) = valid ? ldg16(x + (int64_t)(t0 + n) * a.d + i * 4) : make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+  constexpr int C = N * R, COPIES = 32 / C;  // lanes of a sum
+  const int n = lane / (32 / N), at = lane / COPIES % R;
+  const int label = t0 + n < a.T ? a.labels[t0 + n] : -1;
+  float top = -INFINITY, sum = 0.f;
+  for (int word = (place * F32_WARPS + warp) * R; word < a.V; word += places * F32_WARPS * R) {
+    float acc[C];
+    dot_words<N, U, false>(acc, W, xs, a.d, word, a.V, lane);
+    add_lanes<C, 16>(acc, lane);
+    if (!__all_sync(0xffffffffu, isfinite(acc[0]))) {
+      dot_words<N, 1, true>(acc, W, xs, a.d, word, a.V, lane);
+      add_lanes<C, 16>(acc, lane);
+    }
+    const int v = word + at;
+    if (lane % COPIES == 0 && v < a.V) {
+      add_logit(top, sum, acc[0]);
+      if (v == label) a.picked[t0 + n] = acc[0];
+    }
+  }
+  auto join = [](float& t, float& s, float t2, float s2) {
+    const float best = fmaxf(t, t2), from = best == -INFINITY ? 0.f : best;
+    s = s * exp_of(t - from) + s2 * exp_of(t2 - from);
+    t = best;
+  };
+#pragma unroll
+  for (int o = 16 / N; o > 0; o /= 2) {
+    const float t2 = __shfl_xor_sync(0xffffffffu, top, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
+    join(top, sum, t2, s2);
+  }
+  if (lane % (32 / N) == 0) s_sum[warp][n] = make_float2(top, sum);
+  __syncthreads();
+  if (threadIdx.x >= N || t0 + threadIdx.x >= a.T) return;
+  float2 p = s_sum[0][threadIdx.x];
+  for (int k = 1; k < F32_WARPS; ++k) join(p.x, p.y, s_sum[k][threadIdx.x].x, s_sum[k][threadIdx.x].y);
+  a.partial[(t0 + threadIdx.x) * places + place] = p;
+}
+
 // A warp a token: the CTAs' sums, the loss; then the sum of the losses in token order.
 __global__ void __launch_bounds__(1024) loss_few_join_kernel(const FewArgs a, int ctas, float* loss, float* lse, float* total) {
   pdl_enter();
@@ -340,20 +470,59 @@ cudaError_t launch(const FewMaps& maps, const FewArgs& a, int ctas, cudaStream_t
   return launch_pdl(loss_few_kernel<N>, dim3(ctas), dim3(THREADS), SMEM, st, maps, a);
 }
 
+// float32 tokens of a group: 8, or fewer where they are few or long.
+int f32_tokens(int T, int d) {
+  int n = 1;
+  while (n < 8 && n < T && (int64_t)2 * n * d * 4 <= F32_SMEM) n *= 2;
+  return n;
+}
+
+template <int N, int U>
+cudaError_t launch_f32(const LossArgs& l, const FewArgs& a, int groups, int places, cudaStream_t st) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) dev = 0;
+  if (!done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(loss_few_f32_kernel<N, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, F32_SMEM);
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  LaunchScope ls(KK_LOSS_LOGITS, st);
+  return launch_pdl(loss_few_f32_kernel<N, U>, dim3(groups * places), dim3(F32_NT), (size_t)N * l.d * 4, st, a,
+                    static_cast<const float*>(l.x), static_cast<const float*>(l.W), groups);
+}
+
 }  // namespace
+
+bool loss_is_few(int T, int d, bool bf16) {
+  if (bf16) return T <= LOSS_FEW;
+  const int n = f32_tokens(T, d);
+  return (int64_t)n * d * 4 <= F32_SMEM && T <= n * (n == 8 ? F32_GROUPS : F32_GROUPS_LONG);
+}
 
 size_t loss_few_bytes() { return ((size_t)sm_count() * sizeof(float2) + sizeof(float)) * LOSS_FEW; }
 
 cudaError_t launch_loss_few(const LossArgs& l, uint32_t* err, cudaStream_t st) {
-  if (encoder() == nullptr) return cudaErrorNotSupported;
-  const int n = l.T <= 16 ? 16 : l.T <= 32 ? 32 : 64;
   FewArgs a{l.labels, static_cast<float2*>(l.ws), nullptr, l.T, l.d, l.V, words_of(l.V), err};
   a.picked = reinterpret_cast<float*>(a.partial + (size_t)sm_count() * LOSS_FEW);
-  FewMaps maps{};
-  if (!make_map(&maps.w, l.W, l.V, l.d, MW) || !make_map(&maps.tail, l.W, l.V, l.d, TAIL) || !make_map(&maps.x, l.x, l.T, l.d, n))
-    return cudaErrorInvalidValue;
-  const int ctas = (l.V + a.words - 1) / a.words;
-  const cudaError_t e = n == 16 ? launch<16>(maps, a, ctas, st) : n == 32 ? launch<32>(maps, a, ctas, st) : launch<64>(maps, a, ctas, st);
+  int ctas = (l.V + a.words - 1) / a.words;
+  cudaError_t e;
+  if (l.bf16) {
+    if (encoder() == nullptr) return cudaErrorNotSupported;
+    const int n = l.T <= 16 ? 16 : l.T <= 32 ? 32 : 64;
+    FewMaps maps{};
+    if (!make_map(&maps.w, l.W, l.V, l.d, MW) || !make_map(&maps.tail, l.W, l.V, l.d, TAIL) || !make_map(&maps.x, l.x, l.T, l.d, n))
+      return cudaErrorInvalidValue;
+    e = n == 16 ? launch<16>(maps, a, ctas, st) : n == 32 ? launch<32>(maps, a, ctas, st) : launch<64>(maps, a, ctas, st);
+  } else {
+    const int n = f32_tokens(l.T, l.d), groups = (l.T + n - 1) / n;
+    ctas = std::min(sm_count() / groups, (l.V + F32_WARPS * R - 1) / (F32_WARPS * R));
+    e = n == 1   ? launch_f32<1, 4>(l, a, groups, ctas, st)
+        : n == 2 ? launch_f32<2, 4>(l, a, groups, ctas, st)
+        : n == 4 ? launch_f32<4, 4>(l, a, groups, ctas, st)
+                 : launch_f32<8, 2>(l, a, groups, ctas, st);
+  }
   if (e != cudaSuccess) return e;
   LaunchScope ls(KK_LOSS_COMBINE, st);
   return launch_pdl(loss_few_join_kernel, dim3(1), dim3(1024), 0, st, a, ctas, l.loss, l.lse, l.total);

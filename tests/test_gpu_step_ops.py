@@ -609,6 +609,35 @@ def test_loss_non_finite_rows_stay_to_themselves():
             assert loss[3].isnan() and torch.equal(loss[ok], clean[0][ok]) and torch.equal(lse[ok], clean[1][ok])
 
 
+# the float32 form of few tokens: groups of 8, 4, 2 and 1, the most of them and one token more, the longest rows and past them
+@pytest.mark.parametrize("T,d,V", [(3, 4, 5), (8, 6656, 70), (9, 6660, 131), (24, 13312, 37), (25, 6660, 65), (13, 13316, 33), (24, 26624, 29),
+                                   (25, 26624, 29), (48, 13312, 700), (49, 13312, 700), (5, 26628, 40), (12, 53248, 19), (13, 53248, 19), (2, 53252, 17), (1, 65536, 23), (41, 100, 9729), (48, 132, 4000), (49, 132, 4000)])
+def test_loss_few_float32_tokens(T, d, V):
+    x, W, labels = loss_inputs(T, d, V, torch.float32, 0.2, seed=T + d)
+    labels[-1] = V - 1
+    loss, lse = check_loss(x, W, labels)
+    # an infinity counts as the largest bf16 here as with many tokens, and where it meets a zero adds nothing
+    x[:, 1] = 0
+    W[:, 1] = float("inf")
+    W[V // 2, 0] = float("-inf")
+    x[:, 0] = x[:, 0].abs() + 0.01
+    labels[labels == V // 2] = 0
+    loss, lse, _ = run_loss(x, W, labels)
+    W[:, 1] = 0
+    rest = [v for v in range(V) if v != V // 2]
+    e_loss, e_lse, _ = ref.loss_fwd(x, W[rest], torch.where(labels > V // 2, labels - 1, labels))
+    ze = float(logit_error(x, W[rest]).max())
+    near("lse", lse, e_lse, rel=4 * U, tol=2 * ze + 64 * U)
+    near("loss", loss, e_loss, rel=4 * U, tol=3 * ze + 64 * U)
+    x[0] = float("nan")
+    bad, bad_lse, _ = run_loss(x, W, labels)
+    W[:, 1] = float("inf")
+    again = run_loss(x, W, labels)
+    assert torch.equal(bad_lse[1:], again[1][1:]) and torch.equal(bad[1:], again[0][1:])
+    assert bad[0].isnan() if labels[0] >= 0 else bad[0] == 0
+    check_no_device_error()
+
+
 @pytest.mark.parametrize("dtype,T,d,V", [("bf16", 1024, 64, 300001), ("f32", 600, 64, 130003), ("bf16", 3000, 520, 50257)])
 def test_loss_in_several_pieces(dtype, T, d, V):
     x, W, labels = loss_inputs(T, d, V, TYPES[dtype], 0.1, seed=13)
