@@ -13,16 +13,19 @@
 // registers, as in the products of many tokens.
 //
 // Few float32 tokens take no tensor core: W's parts would have to be written and
-// read again, 12 bytes for each 4.  Groups of 8 tokens, or of fewer
-// where more do not fit in shared memory, have an equal share of the CTAs each; a
-// warp brings four words' weights from memory to its registers once and
-// multiplies them with each token's elements from shared memory.  The CTAs of
-// the groups that have the same words run side by side, so that the weights come
-// from HBM once and otherwise from L2.  128000 x 4096 at 1 and 8 tokens 293 and
-// 325 us (7.2 and 6.5 TB/s), at 16, 32 and 48 513, 957 and 1421: multiplications,
-// reads of shared memory and reads of L2 all count there.  The form for many takes 1837
-// for any of them, and 64 tokens would be 1860 here: six groups are the most.
-// 16 tokens in one group, with 64 sums a lane, are slower (2048 x 50257: 140 us, 115).
+// read again, 12 bytes for each 4.  Groups of 8 tokens, or of fewer where more do
+// not fit in shared memory, have an equal share of the CTAs each; a warp brings
+// four words' weights from memory to its registers once and multiplies them with
+// each token's elements from shared memory.  CTAs of different groups that have
+// the same words run side by side, so that the weights come from HBM once and
+// otherwise from L2.  128000 x 4096 at 1 and 8 tokens 295 and 326 us (7.1 and 6.4
+// TB/s), at 16, 32 and 48 464, 864 and 1290: there the multiplications, the reads
+// of shared memory and those of L2 add up.  The form for many takes 1837 for any
+// of them (256 columns: 45, and 44 here at 48 tokens), so six groups of 8 are the
+// most; of fewer, longer ones, twelve (12 of 32768 x 16384 1482, 13 of the other
+// form 1983).  Two multiplications an instruction and 12 warps with the next
+// columns on their way instead of 16 without: 16 tokens 513 to 464.  16 tokens a
+// group, 64 sums a lane, is slower (2048 x 50257: 140 us, not 105).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -276,25 +279,34 @@ __global__ void __launch_bounds__(THREADS, 1) loss_few_kernel(const __grid_const
 }
 
 // ---- float32 ----
-constexpr int F32_NT = 512, F32_WARPS = F32_NT / 32, R = 4;  // words of a warp
+constexpr int F32_NT = 384, F32_WARPS = F32_NT / 32, R = 4;  // words of a warp
 constexpr int F32_SMEM = 208 * 1024;                         // of the tokens' rows
 constexpr int F32_GROUPS = 6, F32_GROUPS_LONG = 12;          // of 8 tokens, of fewer
 
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t x, float lo, float hi) {
+  uint64_t w;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(w) : "f"(lo), "f"(hi));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(x), "l"(w));
+}
 // acc[n * R + r] = the lane's part of token n with word r; rows past the last word read it again.
-// CAP: infinities count as the largest bf16, as in the products of parts.
-template <int N, int U, bool CAP>
+// U * 128 columns at a time, with AHEAD those behind them on their way; a sum is
+// that of the even and that of the odd columns, two multiplications an
+// instruction.  CAP: infinities count as the largest bf16, as in the products of parts.
+template <int N, int U, bool AHEAD, bool CAP>
 __device__ __forceinline__ void dot_words(float (&acc)[N * R], const float* W, const float* xs, int d, int word, int V, int lane) {
+  uint64_t two_sums[N * R];
 #pragma unroll
-  for (int i = 0; i < N * R; ++i) acc[i] = 0.f;
+  for (int i = 0; i < N * R; ++i) two_sums[i] = 0;
   const float* src[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) src[r] = W + (int64_t)min(word + r, V - 1) * d;
-  for (int c0 = lane * 4; c0 < d; c0 += U * 128) {
-    uint4 u[U][R];
+  auto load = [&](uint4 (&u)[U][R], int c0) {
 #pragma unroll
     for (int j = 0; j < U; ++j)
 #pragma unroll
       for (int r = 0; r < R; ++r) u[j][r] = c0 + j * 128 < d ? ldg16_once(src[r] + c0 + j * 128) : make_uint4(0, 0, 0, 0);
+  };
+  auto multiply = [&](const uint4 (&u)[U][R], int c0) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       if (c0 + j * 128 >= d) break;
@@ -310,13 +322,35 @@ __device__ __forceinline__ void dot_words(float (&acc)[N * R], const float* W, c
       }
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const float4 x = *reinterpret_cast<const float4*>(xs + n * d + c0 + j * 128);
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(xs + n * d + c0 + j * 128);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-          acc[n * R + r] = fmaf(x.w, w[r][3], fmaf(x.z, w[r][2], fmaf(x.y, w[r][1], fmaf(x.x, w[r][0], acc[n * R + r]))));
+        for (int r = 0; r < R; ++r) {
+          fma2(two_sums[n * R + r], x.x, w[r][0], w[r][1]);
+          fma2(two_sums[n * R + r], x.y, w[r][2], w[r][3]);
+        }
       }
     }
+  };
+  uint4 one[U][R];
+  if constexpr (AHEAD) {
+    uint4 two[U][R];
+    load(one, lane * 4);
+    for (int c0 = lane * 4; c0 < d; c0 += U * 256) {
+      load(two, c0 + U * 128);
+      multiply(one, c0);
+      if (c0 + U * 128 >= d) break;
+      load(one, c0 + U * 256);
+      multiply(two, c0 + U * 128);
+    }
+  } else {
+    for (int c0 = lane * 4; c0 < d; c0 += U * 128) {
+      load(one, c0);
+      multiply(one, c0);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < N * R; ++i)
+    acc[i] = __uint_as_float((uint32_t)two_sums[i]) + __uint_as_float((uint32_t)(two_sums[i] >> 32));
 }
 // Sums over the lanes, halving what a lane has: it ends with those from lane * C / 32 on.
 template <int C, int O>
@@ -336,7 +370,7 @@ __device__ __forceinline__ void add_lanes(float* v, int lane) {
   }
 }
 
-template <int N, int U>
+template <int N, int U, bool AHEAD>
 __global__ void __launch_bounds__(F32_NT, 1) loss_few_f32_kernel(const FewArgs a, const float* x, const float* W, int groups) {
   extern __shared__ uint8_t smem_raw[];
   float* xs = reinterpret_cast<float*>(smem_raw);  // [N][d], 0 for tokens that are ignored
@@ -357,10 +391,10 @@ __global__ void __launch_bounds__(F32_NT, 1) loss_few_f32_kernel(const FewArgs a
   float top = -INFINITY, sum = 0.f;
   for (int word = (place * F32_WARPS + warp) * R; word < a.V; word += places * F32_WARPS * R) {
     float acc[C];
-    dot_words<N, U, false>(acc, W, xs, a.d, word, a.V, lane);
+    dot_words<N, U, AHEAD, false>(acc, W, xs, a.d, word, a.V, lane);
     add_lanes<C, 16>(acc, lane);
     if (!__all_sync(0xffffffffu, isfinite(acc[0]))) {
-      dot_words<N, 1, true>(acc, W, xs, a.d, word, a.V, lane);
+      dot_words<N, 1, false, true>(acc, W, xs, a.d, word, a.V, lane);
       add_lanes<C, 16>(acc, lane);
     }
     const int v = word + at;
@@ -477,19 +511,19 @@ int f32_tokens(int T, int d) {
   return n;
 }
 
-template <int N, int U>
+template <int N, int U, bool AHEAD>
 cudaError_t launch_f32(const LossArgs& l, const FewArgs& a, int groups, int places, cudaStream_t st) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) dev = 0;
   if (!done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(loss_few_f32_kernel<N, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, F32_SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(loss_few_f32_kernel<N, U, AHEAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, F32_SMEM);
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
   LaunchScope ls(KK_LOSS_LOGITS, st);
-  return launch_pdl(loss_few_f32_kernel<N, U>, dim3(groups * places), dim3(F32_NT), (size_t)N * l.d * 4, st, a,
+  return launch_pdl(loss_few_f32_kernel<N, U, AHEAD>, dim3(groups * places), dim3(F32_NT), (size_t)N * l.d * 4, st, a,
                     static_cast<const float*>(l.x), static_cast<const float*>(l.W), groups);
 }
 
@@ -518,10 +552,11 @@ cudaError_t launch_loss_few(const LossArgs& l, uint32_t* err, cudaStream_t st) {
   } else {
     const int n = f32_tokens(l.T, l.d), groups = (l.T + n - 1) / n;
     ctas = std::min(sm_count() / groups, (l.V + F32_WARPS * R - 1) / (F32_WARPS * R));
-    e = n == 1   ? launch_f32<1, 4>(l, a, groups, ctas, st)
-        : n == 2 ? launch_f32<2, 4>(l, a, groups, ctas, st)
-        : n == 4 ? launch_f32<4, 4>(l, a, groups, ctas, st)
-                 : launch_f32<8, 2>(l, a, groups, ctas, st);
+    e = n == 1       ? launch_f32<1, 4, false>(l, a, groups, ctas, st)
+        : n == 2     ? launch_f32<2, 4, false>(l, a, groups, ctas, st)
+        : n == 4     ? launch_f32<4, 4, false>(l, a, groups, ctas, st)
+        : l.d <= 512 ? launch_f32<8, 2, false>(l, a, groups, ctas, st)  // 48 x 32000 x 256: 44 us, 50 ahead
+                     : launch_f32<8, 2, true>(l, a, groups, ctas, st);
   }
   if (e != cudaSuccess) return e;
   LaunchScope ls(KK_LOSS_COMBINE, st);
