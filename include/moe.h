@@ -481,7 +481,8 @@ moe_status moe_vocab_loss_fwd(int32_t T, int32_t d, int32_t V, int32_t dtype, co
                               moe_stream_t stream);
 
 /* Bytes of workspace of moe_vocab_loss_fwd (training = 0) or of both calls
- * (training = 1).  Host only; device as above. */
+ * (training = 1).  As many bytes do for any fewer tokens too, with the same d, V
+ * and dtype.  Host only; device as above. */
 moe_status moe_vocab_loss_workspace_size(int32_t T, int32_t d, int32_t V, int32_t dtype, int training, size_t* bytes);
 
 /* Its gradient, the logits formed again:

@@ -677,7 +677,7 @@ def clip_workspace(count: int, device="cuda"):
 
 def vocab_loss_workspace(T: int, d: int, V: int, dtype, training: bool, device="cuda"):
     """Workspace of ``moe_vocab_loss_fwd``, and with ``training`` of ``moe_vocab_loss_bwd`` too, for x of torch type
-    ``dtype``; kept from call to call."""
+    ``dtype``; kept from call to call, of T tokens or of fewer."""
     import torch
 
     code = _torch_types()[2].get(dtype)

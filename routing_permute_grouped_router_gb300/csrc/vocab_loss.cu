@@ -279,6 +279,26 @@ int slices_of(const LossWork& w) {
   return (int)std::max<int64_t>(1, std::min(s, most));
 }
 
+// What dz and acc are given in the workspace: enough for as many tokens and for any
+// fewer.  Equal pieces and slices of whole tiles take less of some larger batches
+// than of smaller ones (bf16, 4096 x 128000: 617 MB for 2304 tokens, 1048 for 2048),
+// and a buffer for the largest batch has to do for the last, shorter one.
+//
+// A piece has at most PIECE_VALUES values of a part, or a tile's columns of each row.
+int64_t dz_values(int64_t Tp, int64_t V) {
+  return std::max(std::min(Tp * (int64_t)up(V, LOSS_TILE), PIECE_VALUES), Tp * LOSS_TILE);
+}
+// Rows of acc.  slices_of is the ceiling of n / m for m tiles of tokens, n a ratio
+// of the sizes that has neither tokens nor the piece in it, so slices * m < n + m
+// below n tiles, and m from there on; and no more than its caps give.
+int64_t acc_rows(const LossWork& w) {
+  const int64_t seg = w.parts == 1 ? 1 : 6, cols = (w.d + 255) / 256, m = w.Tp / LOSS_TILE;
+  const int64_t both = cols * (seg + (w.parts == 1 ? w.dzp : 6)), n = (2 * seg * (sm_count() / 2) + both - 1) / both;
+  const int64_t most = std::min<int64_t>(MAX_SLICES, (int64_t)up(w.V, LOSS_TILE) / 128) * m;
+  const int64_t tiles = std::min({n + std::min(m, n) - 1, most, ((int64_t)1 << 28) / ((int64_t)LOSS_TILE * w.d)});
+  return std::max(m, tiles) * LOSS_TILE;
+}
+
 // What a call keeps in the workspace, from `base` on (null: its size alone); returns its end.
 size_t lay_out(LossWork* w, char* base, int T, int d, int V, bool bf16, bool backward, int dzp) {
   size_t end = 0;
@@ -309,9 +329,9 @@ size_t lay_out(LossWork* w, char* base, int T, int d, int V, bool bf16, bool bac
     w->lse = reinterpret_cast<float*>(take(Tp * 4));
     w->grad = reinterpret_cast<float*>(take(Tp * 4));
     w->off = reinterpret_cast<float*>(take(Tp * 4));
-    w->dz = reinterpret_cast<__nv_bfloat16*>(take((size_t)dzp * Tp * w->piece * 2));
+    w->dz = reinterpret_cast<__nv_bfloat16*>(take((size_t)dzp * dz_values(Tp, V) * 2));
     w->slices = slices_of(*w);
-    w->acc = reinterpret_cast<float*>(take(w->slices * Tp * d * 4));
+    w->acc = reinterpret_cast<float*>(take((size_t)acc_rows(*w) * d * 4));
   }
   return end;
 }
@@ -347,7 +367,8 @@ cudaError_t prepare(LossWork* w, const LossArgs& a, const PackArgs& p, cudaStrea
 size_t loss_ws_bytes(int T, int d, int V, bool bf16, bool training) {
   if (T == 0) return 0;
   LossWork w{};
-  const size_t fwd = loss_is_few(T, d, bf16) ? loss_few_bytes() : lay_out(&w, nullptr, T, d, V, bf16, false, 0);
+  size_t fwd = loss_few_bytes();  // that of more tokens may be less, of a small vocabulary
+  if (!loss_is_few(T, d, bf16)) fwd = std::max(fwd, lay_out(&w, nullptr, T, d, V, bf16, false, 0));
   if (!training) return fwd;
   size_t most = fwd;
   for (int dzp = bf16 ? 1 : MAX_PARTS; dzp <= (bf16 ? 2 : MAX_PARTS); ++dzp)
