@@ -13,9 +13,10 @@
 // registers over all rows of the CTA; a second kernel adds the CTAs' sums in
 // CTA order, so results do not depend on timing.  Statistics and sums are fp32.
 //
-// Rows that the ring has no room for (over 8192 elements; in the backward float32
-// rows of all four tensors from about 6900) have one CTA each and are walked in a
-// loop, again from cache for each pass.  There the columns' sums are taken in a
+// Rows that the ring has no room for (over 8192 elements; in the backward, whose
+// weights take up to 64 KB of shared memory beside it, float32 rows over 5152 where
+// dh, out, dout and y are all there, and over 6868 of three of them) have one CTA
+// each and are walked in a loop, again from cache for each pass.  There the columns' sums are taken in a
 // pass of their own before anything is written (dx and dy may be dh or dout).
 #include <algorithm>
 #include <atomic>
