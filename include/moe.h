@@ -460,7 +460,9 @@ moe_status moe_clip_workspace_size(int32_t count, size_t* bytes);
  * float32) clips nothing either: dst = src, and the caller sees *norm.  Where
  * nothing is clipped a tensor whose dst is its src is not written.  Squares are summed
  * without overflow or underflow whatever the values, in an order fixed by the
- * sizes and the device; subnormal float32 gradients count.  A dst must not
+ * sizes, each src's place modulo 16 bytes and the device (elsewhere modulo 16 the
+ * same values may give a norm whose last bit differs); subnormal float32 gradients
+ * count.  A dst must not
  * overlap another tensor's src or dst, or its own src but for being the same
  * (MOE_ERR_INVALID_ARG). */
 moe_status moe_clip_grads(const moe_grad* grads, int32_t count, float max_norm, float* norm, void* ws, size_t ws_bytes,
