@@ -204,11 +204,28 @@ __device__ __forceinline__ void scale_chunk(const void* src, void* dst_, int64_t
   }
 }
 
+// The same by a scale that is no normal float32 or near to it, an element at a
+// time in 64 bits.
+constexpr float SMALL_SCALE = 0x1p-100f;
+template <typename T>
+__device__ __noinline__ void scale_chunk64(const void* src, void* dst_, int64_t n, int64_t chunk, double scale) {
+  constexpr int VN = Vec<T>::N;
+  const Part<T> p(src, n, chunk);
+  T* dst = static_cast<T*>(dst_);
+#pragma unroll 1
+  for (int j = 0; j < VECS; ++j)
+#pragma unroll 1
+    for (int i = 0; i < VN; ++i) {
+      const int64_t at = p.at(j) + i;
+      if (at >= 0 && at < n) dst[at] = from_f32<T>((float)((double)to_f32(p.src[at]) * scale));
+    }
+}
+
 // One CTA an SM: each makes the norm for itself.
 template <int N>
 __global__ void __launch_bounds__(CLIP_NT* GROUPS, 1) grad_clip_kernel(const __grid_constant__ ClipList<N> l, const ClipScale s) {
   pdl_enter();
-  __shared__ float by;
+  __shared__ double by;
   __shared__ bool clip;
   if (threadIdx.x < 32) {
     double sum = 0.0;
@@ -220,17 +237,22 @@ __global__ void __launch_bounds__(CLIP_NT* GROUPS, 1) grad_clip_kernel(const __g
       const float as_float = (float)norm;
       if (s.norm != nullptr && blockIdx.x == 0) *s.norm = as_float;
       clip = isfinite(as_float) && as_float > s.max_norm;
-      by = clip ? (float)((double)s.max_norm / norm) : 1.f;
+      by = clip ? (double)s.max_norm / norm : 1.0;
     }
   }
   __syncthreads();
   const bool clips = clip;
-  const float scale = by;
+  const float scale = (float)by;
   const int64_t total = l.first(l.count);
 #pragma unroll 1
   for (int64_t c = total - 1 - blockIdx.x - (int64_t)(threadIdx.x / CLIP_NT) * gridDim.x; c >= 0; c -= GROUPS * gridDim.x) {
     const ClipEntry& e = l.t[tensor_of(l, c)];
     if (e.dst == nullptr || (!clips && e.dst == e.src)) continue;
+    if (scale < SMALL_SCALE) {
+      if (e.first_bf16 & 1) scale_chunk64<__nv_bfloat16>(e.src, e.dst, e.n, c - (e.first_bf16 >> 1), by);
+      else scale_chunk64<float>(e.src, e.dst, e.n, c - (e.first_bf16 >> 1), by);
+      continue;
+    }
     if (e.first_bf16 & 1) scale_chunk<__nv_bfloat16>(e.src, e.dst, e.n, c - (e.first_bf16 >> 1), scale);
     else scale_chunk<float>(e.src, e.dst, e.n, c - (e.first_bf16 >> 1), scale);
   }

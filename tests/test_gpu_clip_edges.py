@@ -47,3 +47,24 @@ def test_clip_repeats_itself_at_the_same_place_modulo_16_bytes(dtype):
         for r in results[1:]:
             assert all(torch.equal(a, b) for a, b in zip(results[0], r)), first
     check_no_device_error()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("top,most", [(2.0 ** 100, 2.0 ** -15), (2.0 ** 115, 2.0 ** -20), (2.0 ** 118, 2.0 ** -100), (2.0 ** 118, 2.0 ** -124),
+                                      (2.0 ** 118, 2.0 ** -140), (2.0 ** 20, 2.0 ** -100), (2.0 ** 20, 2.0 ** -145), (2.0 ** -20, 2.0 ** -149)])
+def test_clip_by_a_scale_that_is_no_normal_float32(dtype, top, most):
+    """max_norm / norm is below 2^-126, or next to it: the clipped gradients have that norm all the same."""
+    t = ops.TYPES[dtype]
+    src = [(ops.rand(n, seed=n).double() * top).to(t) for n in (70001, 9)]
+    src[0][5], src[1][3] = 0, -0.0
+    total = ops.norm64(src)
+    for dst in ([torch.full_like(v, float("nan")) for v in src], [v.clone() for v in src]):
+        before = dst if dst[0].isnan().any() else None
+        norm = clipped(src if before is not None else dst, dst, most)
+        assert abs(float(norm) - total) <= ops.NORM * total
+        for s, d in zip(src, dst):
+            e = s.double() * (most / total)
+            # the result's own rounding: half a step of the type, or of its smallest values; a bf16 one by way of float32
+            room = (ops.NORM + 2 * ops.U + ops.HALF[t]) * e.abs() + (2.0 ** -134 if t == torch.bfloat16 else 0) + 2.0 ** -150
+            assert ((d.double() - e).abs() <= room).all(), f"off by {float(((d.double() - e).abs() / room).max())} of the room"
+    check_no_device_error()
