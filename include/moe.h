@@ -477,7 +477,9 @@ moe_status moe_clip_grads(const moe_grad* grads, int32_t count, float max_norm, 
  * of the losses and the number of labelled tokens.  0 <= T <= 2^24,
  * 1 <= V <= 2^24, T V <= 2^44, 1 <= d <= 65536, d a multiple of 8 for MOE_BF16
  * and of 4 for MOE_F32.  Infinities in a float32 W count as the largest bf16 of
- * their sign.  Deterministic. */
+ * their sign, and a float32 x with an infinity has no finite loss.  A logit of -inf adds
+ * nothing; with one of +inf (or past float32) lse is inf and the loss inf, or NaN
+ * where it is the label's.  Deterministic. */
 moe_status moe_vocab_loss_fwd(int32_t T, int32_t d, int32_t V, int32_t dtype, const void* x, const void* W,
                               const int32_t* labels, float* loss, float* lse, float* total, void* ws, size_t ws_bytes,
                               moe_stream_t stream);

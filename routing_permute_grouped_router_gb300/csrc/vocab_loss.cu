@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(1024) loss_combine_kernel(const LossWork w, in
 #pragma unroll 4
     for (int i = strip; i < parts; i += 32) {
       const float2 p = w.partial[(int64_t)i * w.Tp + r];
-      const float best = fmaxf(top, p.x), at = best == -INFINITY ? 0.f : best;
+      const float best = fmaxf(top, p.x), at = base_of(best);
       sum = sum * expf(top - at) + p.y * expf(p.x - at);
       top = best;
     }
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(1024) loss_combine_kernel(const LossWork w, in
     float best = top;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-    const float at = best == -INFINITY ? 0.f : best;
+    const float at = base_of(best);
     sum = warp_sum(sums[lane][strip] * expf(top - at));
     if (lane == 0 && r0 + strip < n) {
       const int t = w.list[r0 + strip];

@@ -13,6 +13,11 @@ constexpr int LOSS_TILE = 256;   // rows and columns of a product's tile
 constexpr int LOSS_PART = 128;   // columns of a partial sum of the forward
 constexpr int MAX_PARTS = 3;     // bf16 parts of a float32 value
 
+// What logits are measured from in a sum of exponentials: their maximum, or the
+// finite value next to it.  So an infinite logit adds infinity (measured from
+// itself it would be a NaN), and -inf adds 0 among nothing but -inf too.
+__device__ __forceinline__ float base_of(float best) { return fminf(fmaxf(best, -3.402823466e38f), 3.402823466e38f); }
+
 // ---- vocab_loss_few.cu: the forward of at most LOSS_FEW tokens, in the workspace's first bytes ----
 constexpr int LOSS_FEW = 64;
 bool loss_is_few(int T, int d, bool bf16);  // float32: fewer

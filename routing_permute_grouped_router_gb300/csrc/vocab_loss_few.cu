@@ -70,8 +70,7 @@ __device__ __forceinline__ float exp_of(float x) {  // of a difference, <= 0
 // One more logit: a token's maximum and the sum of exp of the distances to it.
 __device__ __forceinline__ void add_logit(float& top, float& sum, float z) {
   const float best = fmaxf(top, z);
-  if (best == -INFINITY && z == z) return;  // nothing but -inf so far
-  const float e = exp_of(fminf(top, z) - best);  // 0 for a first one; NaN stays
+  const float e = exp_of(fminf(top, z) - base_of(best));  // 0 for a first one, and of -inf; NaN stays
   sum = z > top ? fmaf(sum, e, 1.f) : sum + (z == z ? e : z);
   top = best;
 }
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_few_kernel(const __grid_const
       float best = -INFINITY, s = 0.f;
 #pragma unroll 8
       for (int k = 0; k < n; ++k) best = fmaxf(best, p[k].x);
-      const float at = best == -INFINITY ? 0.f : best;
+      const float at = base_of(best);
 #pragma unroll 8
       for (int k = 0; k < n; ++k) s += p[k].y * exp_of(p[k].x - at);
       return make_float2(best, s);
@@ -404,7 +403,7 @@ __global__ void __launch_bounds__(F32_NT, 1) loss_few_f32_kernel(const FewArgs a
     }
   }
   auto join = [](float& t, float& s, float t2, float s2) {
-    const float best = fmaxf(t, t2), from = best == -INFINITY ? 0.f : best;
+    const float best = fmaxf(t, t2), from = base_of(best);
     s = s * exp_of(t - from) + s2 * exp_of(t2 - from);
     t = best;
   };
@@ -435,7 +434,7 @@ __global__ void __launch_bounds__(1024) loss_few_join_kernel(const FewArgs a, in
     for (int c = lane; c < ctas; c += 32) best = fmaxf(best, a.partial[t * ctas + c].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
-    const float at = best == -INFINITY ? 0.f : best;
+    const float at = base_of(best);
 #pragma unroll 4
     for (int c = lane; c < ctas; c += 32) {
       const float2 p = a.partial[t * ctas + c];

@@ -261,7 +261,7 @@ __device__ __forceinline__ void logits_epilogue(const LossWork& w, int row, int 
 #pragma unroll
   for (int i = 4; i < HALF; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
   const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-  const float from = best == -INFINITY ? 0.f : best;  // nothing but -inf: their exponentials are 0
+  const float from = base_of(best);
   float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < HALF; ++i) s[i & 3] += exp_from(v[i], from);
