@@ -42,3 +42,26 @@ def test_join_on_either_side_of_the_ring(rows, d, dtype, dout):
         c = ops.run_bwd(i, r, given[0], given[1], 0.8, 0.5, dx=given[dx], dy=given[dy])
         assert all(torch.equal(b[n], c[n]) for n in b)
     check_no_device_error()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [96, 512, 1021, 8192, 9000, 9001])
+def test_join_rows_with_an_infinity(d, dtype):
+    """An infinite x stays in out and gives ro = 0, so h is 0 but for a NaN in its place; an infinite y gives ry = 0, a NaN
+    in its place of out and so a row of NaN in h.  The rows around them are as without them."""
+    t = ops.TYPES[dtype]
+    i = ops.join_inputs(20, d, t, seed=43)
+    clean = ops.run_fwd(i)
+    i["x"][6, 5], i["x"][7, d - 1], i["y"][11, 3] = float("inf"), float("-inf"), float("inf")
+    r = ops.run_fwd(i)
+    rest = [k for k in range(20) if k not in (6, 7, 11)]
+    assert all(torch.equal(r[n][rest], clean[n][rest]) for n in r)
+    for row, at, value in ((6, 5, float("inf")), (7, d - 1, float("-inf"))):
+        others = [c for c in range(d) if c != at]
+        assert r["out"][row, at] == value and torch.equal(r["out"][row, others], clean["out"][row, others])
+        assert torch.equal(r["ry"][row], clean["ry"][row]) and r["ro"][row] == 0
+        assert r["h"][row, at].isnan() and (r["h"][row, others] == 0).all()
+    others = [c for c in range(d) if c != 3]
+    assert r["ry"][11] == 0 and r["out"][11, 3].isnan() and torch.equal(r["out"][11, others], i["x"][11, others])
+    assert r["ro"][11].isnan() and r["h"][11].isnan().all()
+    check_no_device_error()
