@@ -19,8 +19,8 @@
 //
 // float32 operands come as three bf16 parts of 8 bits each, whose sum they are
 // exactly.  A product then runs over six pairs of parts, the smallest first (so
-// the sums that are rounded often are small); the pairs left out are 2^-24 of
-// the product and below.  dz likewise has one part for a result in bf16, two
+// the sums that are rounded often are small); the pairs left out are 2^-23 of
+// the product in the mean, 2^-21 at most.  dz likewise has one part for a result in bf16, two
 // (16 bits) for a float32 dW of bf16 inputs, three in float32.
 //
 // Every mbarrier wait is bounded (2 s); on expiry the kernel records
