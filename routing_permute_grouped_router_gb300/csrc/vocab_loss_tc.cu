@@ -719,9 +719,11 @@ cudaError_t logits(const LossWork& w, cudaStream_t st) {
   if (!ok) return cudaErrorInvalidValue;
   const int64_t cols = KIND == LOGITS ? (w.V + BN - 1) / BN : w.piece / BN;
   const int64_t tiles = (int64_t)(w.Tp / (2 * BM)) * cols;
-  if (KIND == LOGITS) return launch<KIND, false>(maps, a, tiles, KK_LOSS_LOGITS, st);
-  return (w.d + 127) / 128 * a.seg[0].n <= SHORT_K ? launch<KIND, true>(maps, a, tiles, KK_LOSS_DLOGITS, st)
-                                                  : launch<KIND, false>(maps, a, tiles, KK_LOSS_DLOGITS, st);
+  if constexpr (KIND == LOGITS)
+    return launch<KIND, false>(maps, a, tiles, KK_LOSS_LOGITS, st);
+  else
+    return (w.d + 127) / 128 * a.seg[0].n <= SHORT_K ? launch<KIND, true>(maps, a, tiles, KK_LOSS_DLOGITS, st)
+                                                    : launch<KIND, false>(maps, a, tiles, KK_LOSS_DLOGITS, st);
 }
 
 }  // namespace
