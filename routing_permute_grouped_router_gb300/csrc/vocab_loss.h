@@ -3,6 +3,7 @@
 // for few tokens.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "step.h"
@@ -25,6 +26,11 @@ size_t loss_few_bytes();
 cudaError_t launch_loss_few(const LossArgs& a, uint32_t* err, cudaStream_t st);
 
 // ---- vocab_loss_tc.cu ----
+// 2-D tensor map over a row-major [rows, cols] matrix, 128-byte swizzle; what a box
+// has past it reads as 0.  maps_ready: the driver's encoder was found.
+bool maps_ready();
+bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
+              bool fp32 = false);
 // Labelled tokens only, in token order, padded with zero rows to a whole tile.
 struct LossWork {
   int32_t* list;    // [T]: the labelled tokens

@@ -26,9 +26,6 @@
 // form 1983).  Two multiplications an instruction and 12 warps with the next
 // columns on their way instead of 16 without: 16 tokens 513 to 464.  16 tokens a
 // group, 64 sums a lane, is slower (2048 x 50257: 140 us, not 105).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <atomic>
 
@@ -464,27 +461,6 @@ __global__ void __launch_bounds__(1024) loss_few_join_kernel(const FewArgs a, in
 }
 
 // ------------------------------ host side ---------------------------------- //
-// Looked up once; a thread that comes meanwhile waits for it.
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-                        cudaSuccess &&
-                    q == cudaDriverEntryPointSuccess;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? fn : nullptr);
-  }();
-  return encode;
-}
-bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {KB, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 // Words of a CTA: an equal share each, whole copies of the last tile's where they are few.
 int words_of(int V) { return std::max(TAIL, ((V + sm_count() - 1) / sm_count() + 15) / 16 * 16); }
 
@@ -542,10 +518,11 @@ cudaError_t launch_loss_few(const LossArgs& l, uint32_t* err, cudaStream_t st) {
   int ctas = (l.V + a.words - 1) / a.words;
   cudaError_t e;
   if (l.bf16) {
-    if (encoder() == nullptr) return cudaErrorNotSupported;
+    if (!maps_ready()) return cudaErrorNotSupported;
     const int n = l.T <= 16 ? 16 : l.T <= 32 ? 32 : 64;
     FewMaps maps{};
-    if (!make_map(&maps.w, l.W, l.V, l.d, MW) || !make_map(&maps.tail, l.W, l.V, l.d, TAIL) || !make_map(&maps.x, l.x, l.T, l.d, n))
+    if (!make_map(&maps.w, l.W, l.V, l.d, KB, MW) || !make_map(&maps.tail, l.W, l.V, l.d, KB, TAIL) ||
+        !make_map(&maps.x, l.x, l.T, l.d, KB, n))
       return cudaErrorInvalidValue;
     e = n == 16 ? launch<16>(maps, a, ctas, st) : n == 32 ? launch<32>(maps, a, ctas, st) : launch<64>(maps, a, ctas, st);
   } else {

@@ -641,20 +641,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   }();
   return encode;
 }
-// 2-D tensor map over a row-major [rows, cols] matrix, 128-byte swizzle; what a box has past it reads as 0
-bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
-              bool fp32 = false) {
-  const uint64_t es = fp32 ? 4 : 2;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * es};
-  cuuint32_t box[2] = {box_cols, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return encoder()(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // The pairs of parts, smallest products first; la and lb are the parts' distances in the maps.
 Segs segs(int pa, int pb, int la, int lb) {
   Segs s{};
@@ -708,7 +694,7 @@ cudaError_t launch(const Maps& maps, const TcArgs& args, int64_t tiles, int kind
 
 template <int KIND>
 cudaError_t logits(const LossWork& w, cudaStream_t st) {
-  if (encoder() == nullptr) return cudaErrorNotSupported;
+  if (!maps_ready()) return cudaErrorNotSupported;
   Maps maps{};
   TcArgs a{};
   a.w = w;
@@ -728,11 +714,25 @@ cudaError_t logits(const LossWork& w, cudaStream_t st) {
 
 }  // namespace
 
+bool maps_ready() { return encoder() != nullptr; }
+bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
+              bool fp32) {
+  const uint64_t es = fp32 ? 4 : 2;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * es};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return encoder()(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t tc_loss_logits(const LossWork& w, cudaStream_t st) { return logits<LOGITS>(w, st); }
 cudaError_t tc_loss_dlogits(const LossWork& w, cudaStream_t st) { return logits<DLOGITS>(w, st); }
 
 cudaError_t tc_loss_grads(const LossWork& w, bool dx, void* dW, bool dw_bf16, bool accumulate, cudaStream_t st) {
-  if (encoder() == nullptr) return cudaErrorNotSupported;
+  if (!maps_ready()) return cudaErrorNotSupported;
   Maps maps{};
   TcArgs a{};
   a.w = w;
