@@ -68,3 +68,36 @@ def test_clip_by_a_scale_that_is_no_normal_float32(dtype, top, most):
             room = (ops.NORM + 2 * ops.U + ops.HALF[t]) * e.abs() + (2.0 ** -134 if t == torch.bfloat16 else 0) + 2.0 ** -150
             assert ((d.double() - e).abs() <= room).all(), f"off by {float(((d.double() - e).abs() / room).max())} of the room"
     check_no_device_error()
+
+
+def test_clip_of_long_lists_from_several_threads():
+    """Each list is found sound and clipped as it is alone."""
+    import threading
+
+    lists = [[ops.rand(50 + i % 7, seed=1000 * k + i) for i in range(n)] for k, n in enumerate((33, 100, 300, 1000))]
+    alone = []
+    for src in lists:
+        dst = [torch.empty_like(v) for v in src]
+        alone.append((clipped(src, dst, 0.5), dst))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(k):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    dst = [torch.empty_like(v) for v in lists[k]]
+                    norm = clipped(lists[k], dst, 0.5)
+                    stream.synchronize()
+                    assert torch.equal(norm, alone[k][0]) and all(torch.equal(a, b) for a, b in zip(dst, alone[k][1]))
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(k % 4,)) for k in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    check_no_device_error()

@@ -50,3 +50,36 @@ def test_row_workspaces_serve_fewer_rows(d):
 def test_clip_workspace_serves_fewer_tensors():
     sizes = [pkg.moe_clip_workspace_size(n) for n in (*range(0, 3000), 1 << 14, pkg.MOE_CLIP_MAX_TENSORS)]
     assert sizes == sorted(sizes)
+
+
+def test_clip_overlaps_are_found_by_several_threads_at_once():
+    """Lists of more tensors than the stack has room for share the library's: each call's answer is its own."""
+    import ctypes
+    import threading
+
+    lib = pkg.lib()
+
+    def entries(n, base, overlap):
+        e = [pkg.MoeGrad(base + 64 * i, base + (1 << 30) + 64 * i, 16, F) for i in range(n)]
+        if overlap is not None:
+            e[overlap].dst += 4
+        return (pkg.MoeGrad * n)(*e)
+
+    def status(e, n):
+        return pkg.STATUS[lib.moe_clip_grads(e, n, 1.0, ctypes.c_void_p(0x1000), 0x2000, 1 << 40, None)]
+
+    sizes = (33, 40, 300, 2000)
+    # what is refused here is refused before anything is launched; without a fault the call would go on, so none is made
+    lists = [(entries(n, 1 << 34, n // 2), n) for n in sizes] + [(entries(n, 1 << 35, n - 2), n) for n in sizes]
+    wrong = []
+
+    def work():
+        for _ in range(200):
+            wrong.extend(n for e, n in lists if status(e, n) != "MOE_ERR_INVALID_ARG")
+
+    threads = [threading.Thread(target=work) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
