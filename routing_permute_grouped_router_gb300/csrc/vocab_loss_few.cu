@@ -9,8 +9,12 @@
 // and sum of exponentials over its words in registers; the CTA's threads join
 // theirs at the end, and a second kernel the CTAs'.
 //
-// Sums over K of 1024 at a time are added up in TMEM and then, rounded, in
-// registers, as in the products of many tokens.
+// Sums over K of 256 at a time are added up in TMEM, where they are cut off, and
+// then, rounded, in registers.  Longer ones lean to 0: the loss of one token that has
+// learned its label, 4096 x 128000, is 8e-8 off (root mean square, 6e-8 of products
+// in fp32), 1.4e-7 with K of 512, 2.8e-7 with the 1024 of many tokens' products;
+// shorter ones cost more than they give (K of 128: 6e-8, 177 us for 173, 190 for 182
+// at 64 tokens; K of 1024: 171 and 180).
 //
 // Few float32 tokens take no tensor core: W's parts would have to be written and
 // read again, 12 bytes for each 4.  Groups of 8 tokens, or of fewer where more do
@@ -41,7 +45,7 @@ constexpr int W_BYTES = MW * KS * 2;
 constexpr int NST = 4;
 constexpr int STAGE = W_BYTES + LOSS_FEW * KS * 2;  // for the most tokens
 constexpr int BUFS = 4;                         // accumulators
-constexpr int CHAIN = 8;                        // stages added up in TMEM
+constexpr int CHAIN = 2;                        // stages added up in TMEM
 constexpr int TAIL = 32;                        // words a copy of the last tile
 constexpr int THREADS = 192, EPI = 128;
 constexpr int CTRL_OFF = NST * STAGE;

@@ -110,3 +110,20 @@ def test_dx_has_the_label_term_beyond_8_bits(T, d, V, dw):
     assert own + words < 0.5 * off, "the case does not tell the term"
     assert abs(along) <= own + words + 2.0 ** -20, f"{along:.2e} along dx, {own + words:.2e} at most"
     check_no_device_error()
+
+
+@pytest.mark.parametrize("T", [1, 16, 33, 64])
+@pytest.mark.parametrize("at", [0, 130, 1024, 2500, 4095])
+def test_logits_of_few_bf16_tokens_lose_little_beside_a_large_product(T, at):
+    """One word, so lse is its logit: a product of 2^24, at `at`, and 4095 of 1/32.
+
+    The tensor core cuts a sum off, so what 16 small products give, 1/2, is lost on top of the large one, whose steps are
+    2 (or 1, with a bit more).  That ends with the sum over K = 256 that has it: 16 halves at most.  The others are 8
+    each, exact, and so are their sums with it, but for one rounding by at most 1.  (32 would be lost of a K of 1024.)
+    """
+    x, W = torch.full((T, 4096), 1 / 32, device="cuda"), torch.ones(1, 4096, device="cuda")
+    x[:, at], W[:, at] = 4096, 4096
+    _, lse, _ = ops.run_loss(x.bfloat16(), W.bfloat16(), torch.zeros(T, dtype=torch.int32, device="cuda"))
+    lost = 2.0 ** 24 + 4095 / 32 - lse.double()
+    assert -1 <= float(lost.min()) and float(lost.max()) <= 9, f"{float(lost.max())} lost"
+    check_no_device_error()
