@@ -13,15 +13,17 @@
 //
 // The tensor core cuts a sum off to fp32 after each MMA (it does not round), so
 // a sum over K shrinks by some 2e-8 a step of 16: 1.6e-4 over a vocabulary of
-// 130000.  Eight stages (K of 1024) at a time are therefore added up in TMEM,
-// and their sums in the epilogue's registers, rounded; the two accumulators
-// alternate, so the MMAs do not wait.
+// 130000.  Eight stages (K of 1024) at a time are therefore added up in TMEM, four
+// of float32 operands, and their sums in the epilogue's registers, rounded; the two
+// accumulators alternate, so the MMAs do not wait.  (float32 gradients are 1.2e-6 off
+// with eight and 6.6e-7 with four, products in fp32 5e-7 to 3e-6; 777 x 1000 x 10007
+// forward 121 and 124 us, backward 307 and 326.  Two cost 20 %.)
 //
 // float32 operands come as three bf16 parts of 8 bits each, whose sum they are
 // exactly.  A product then runs over six pairs of parts, the smallest first (so
 // the sums that are rounded often are small); the pairs left out are 2^-23 of
-// the product in the mean, 2^-21 at most.  dz likewise has one part for a result in bf16, two
-// (16 bits) for a float32 dW of bf16 inputs, three in float32.
+// the product in the mean, 2^-21 at most.  dz likewise has one part for a result in
+// bf16, two (16 bits) for a float32 dW of bf16 inputs, three in float32.
 //
 // Every mbarrier wait is bounded (2 s); on expiry the kernel records
 // DEV_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
@@ -44,7 +46,7 @@ constexpr int KB = 2;                       // k-blocks of a stage
 constexpr int BLOCK_BYTES = BM * BK * 2;    // a loaded box
 constexpr int A_BYTES = KB * BLOCK_BYTES, STAGE = 2 * A_BYTES;
 static_assert(BM == BNH && KB == 2, "boxes of A and B are alike");
-constexpr int CHAIN = 8;                    // stages added up in TMEM
+constexpr int CHAIN = 8, CHAIN_F32 = 4;      // stages added up in TMEM
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int HALF = BN / 2;                // columns of a row that an epilogue thread holds
@@ -82,6 +84,7 @@ struct TcArgs {
   LossWork w;
   Segs seg[2];  // of the logits or of acc; of dW
   int with_dx, with_dw, dw_bf16, add_acc, add_dw;
+  int chain;    // stages added up in TMEM
 };
 
 __host__ __device__ constexpr uint32_t idesc(bool a_mn, bool b_mn) {
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
         const bool a_mn = KIND == GRADS && t.what == 1, b_mn = KIND == GRADS;
         const uint32_t id = a_mn ? idesc(true, true) : b_mn ? idesc(false, true) : idesc(false, false);
         const int total = t.blocks * a.seg[KIND == GRADS ? t.what : 0].n;
-        for (int b0 = 0; b0 < total && alive; b0 += CHAIN) {
+        for (int b0 = 0; b0 < total && alive; b0 += a.chain) {
           const uint32_t acc = uses & 1u;
           if (!mbar_wait(smem_addr(&tempty_bar[acc]), ((uses >> 1) & 1u) ^ 1u, abort_flag, a.w.err, 920 + KIND)) {
             alive = false;
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
           ++uses;
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * BN;
-          const int b1 = b0 + CHAIN < total ? b0 + CHAIN : total;
+          const int b1 = b0 + a.chain < total ? b0 + a.chain : total;
           for (int b = b0; b < b1; ++b) {
             if (!mbar_wait(smem_addr(&full_bar[stage]), phase, abort_flag, a.w.err, 930 + KIND)) {
               alive = false;
@@ -573,7 +576,7 @@ __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_consta
         for (int i = 0; i < HALF; ++i) v[i] = 0.f;
       }
       bool ok = true;
-      for (int b = 0; b < total; b += CHAIN) {
+      for (int b = 0; b < total; b += a.chain) {
         const uint32_t acc = uses & 1u;
         if (!mbar_wait(smem_addr(&tfull_bar[acc]), (uses >> 1) & 1u, abort_flag, a.w.err, 940 + KIND)) {
           ok = false;
@@ -698,6 +701,7 @@ cudaError_t logits(const LossWork& w, cudaStream_t st) {
   Maps maps{};
   TcArgs a{};
   a.w = w;
+  a.chain = w.parts == 1 ? CHAIN : CHAIN_F32;
   a.seg[0] = segs(w.parts, w.parts, w.ldx, w.ldw);
   bool ok = make_map(&maps.m[0], w.xp, w.Tp, (uint64_t)w.parts * w.ldx, BK, BM) &&
             make_map(&maps.m[1], w.wp, w.V, (uint64_t)w.parts * w.ldw, BK, BNH);
@@ -736,6 +740,7 @@ cudaError_t tc_loss_grads(const LossWork& w, bool dx, void* dW, bool dw_bf16, bo
   Maps maps{};
   TcArgs a{};
   a.w = w;
+  a.chain = w.parts == 1 ? CHAIN : CHAIN_F32;
   a.with_dx = dx;
   a.with_dw = dW != nullptr;
   a.dw_bf16 = dw_bf16;

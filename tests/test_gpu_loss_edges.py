@@ -127,3 +127,15 @@ def test_logits_of_few_bf16_tokens_lose_little_beside_a_large_product(T, at):
     lost = 2.0 ** 24 + 4095 / 32 - lse.double()
     assert -1 <= float(lost.min()) and float(lost.max()) <= 9, f"{float(lost.max())} lost"
     check_no_device_error()
+
+
+@pytest.mark.parametrize("T", [49, 300])
+@pytest.mark.parametrize("at", [0, 130, 1024, 2500, 4095])
+def test_logits_of_float32_tokens_lose_little_beside_a_large_product(T, at):
+    """The same in float32, on the tensor cores from 49 tokens on: 32 halves of the sum over K = 512 that has it."""
+    x, W = torch.full((T, 4096), 1 / 32, device="cuda"), torch.ones(1, 4096, device="cuda")
+    x[:, at], W[:, at] = 4096, 4096
+    _, lse, _ = ops.run_loss(x, W, torch.zeros(T, dtype=torch.int32, device="cuda"))
+    lost = 2.0 ** 24 + 4095 / 32 - lse.double()
+    assert -1 <= float(lost.min()) and float(lost.max()) <= 17, f"{float(lost.max())} lost"
+    check_no_device_error()
