@@ -481,14 +481,17 @@ moe_status moe_clip_grads(const moe_grad* grads, int32_t count, float max_norm, 
  * nothing; with one of +inf (or past float32) lse is inf and the loss inf, or NaN
  * where it is the label's.  Products are added up in fp32, but cut off and not
  * rounded over d of 1024 at a time (512 of MOE_F32; 256 of at most 64 MOE_BF16
- * tokens): 1e-6 of a logit and less.  Deterministic. */
+ * tokens): 1e-6 of the sum of magnitudes and less.  Deterministic. */
 moe_status moe_vocab_loss_fwd(int32_t T, int32_t d, int32_t V, int32_t dtype, const void* x, const void* W,
                               const int32_t* labels, float* loss, float* lse, float* total, void* ws, size_t ws_bytes,
                               moe_stream_t stream);
 
 /* Bytes of workspace of moe_vocab_loss_fwd (training = 0) or of both calls
  * (training = 1).  As many bytes do for any fewer tokens too, with the same d, V
- * and dtype.  Host only; device as above. */
+ * and dtype.  MOE_F32 calls hold W in bf16 parts there, 6 bytes an element (but for
+ * the forward of few tokens: up to 48; 24 and 12 of d past 13312 and 26624); the backward
+ * holds up to 2^28 values of dz, 2 bytes for each of its 1 to 3 parts.  Host only; device
+ * as above. */
 moe_status moe_vocab_loss_workspace_size(int32_t T, int32_t d, int32_t V, int32_t dtype, int training, size_t* bytes);
 
 /* Its gradient, the logits formed again:

@@ -221,7 +221,8 @@ __device__ __noinline__ void scale_chunk64(const void* src, void* dst_, int64_t 
     }
 }
 
-// One CTA an SM: each makes the norm for itself.
+// One CTA an SM: each makes the norm for itself.  (64 registers for 1024 threads: 54
+// bytes are spilled beside the eight vectors that a thread has in work.)
 template <int N>
 __global__ void __launch_bounds__(CLIP_NT* GROUPS, 1) grad_clip_kernel(const __grid_constant__ ClipList<N> l, const ClipScale s) {
   pdl_enter();

@@ -384,6 +384,9 @@ __device__ __forceinline__ bool grads_epilogue(const CUtensorMap* map, int row0,
 }
 
 // ------------------------------ the kernel --------------------------------- //
+// 168 registers a thread are all that ten warps can have (three share a quarter of
+// the SM's): next to its 128 columns an epilogue thread spills 600 bytes in GRADS, 100
+// to 140 in DLOGITS, 56 in LOGITS.
 template <int KIND, bool SHORT>
 __global__ void __launch_bounds__(THREADS, 1) loss_tc_kernel(const __grid_constant__ Maps maps,
                                                              const __grid_constant__ TcArgs a) {
