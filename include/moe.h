@@ -462,9 +462,8 @@ moe_status moe_clip_workspace_size(int32_t count, size_t* bytes);
  * without overflow or underflow whatever the values, in an order fixed by the
  * sizes, each src's place modulo 16 bytes and the device (elsewhere modulo 16 the
  * same values may give a norm whose last bit differs); subnormal float32 gradients
- * count.  A dst must not
- * overlap another tensor's src or dst, or its own src but for being the same
- * (MOE_ERR_INVALID_ARG). */
+ * count.  A dst must not overlap another tensor's src or dst, or its own src but for
+ * being the same (MOE_ERR_INVALID_ARG). */
 moe_status moe_clip_grads(const moe_grad* grads, int32_t count, float max_norm, float* norm, void* ws, size_t ws_bytes,
                           moe_stream_t stream);
 
@@ -481,7 +480,7 @@ moe_status moe_clip_grads(const moe_grad* grads, int32_t count, float max_norm, 
  * nothing; with one of +inf (or past float32) lse is inf and the loss inf, or NaN
  * where it is the label's.  Products are added up in fp32, but cut off and not
  * rounded over d of 1024 at a time (512 of MOE_F32; 256 of at most 64 MOE_BF16
- * tokens): 1e-6 of the sum of magnitudes and less.  Deterministic. */
+ * tokens): some 1e-6 of the sum of their magnitudes, 2^-17 at most.  Deterministic. */
 moe_status moe_vocab_loss_fwd(int32_t T, int32_t d, int32_t V, int32_t dtype, const void* x, const void* W,
                               const int32_t* labels, float* loss, float* lse, float* total, void* ws, size_t ws_bytes,
                               moe_stream_t stream);
@@ -489,9 +488,9 @@ moe_status moe_vocab_loss_fwd(int32_t T, int32_t d, int32_t V, int32_t dtype, co
 /* Bytes of workspace of moe_vocab_loss_fwd (training = 0) or of both calls
  * (training = 1).  As many bytes do for any fewer tokens too, with the same d, V
  * and dtype.  MOE_F32 calls hold W in bf16 parts there, 6 bytes an element (but for
- * the forward of few tokens: up to 48; 24 and 12 of d past 13312 and 26624); the backward
- * holds up to 2^28 values of dz, 2 bytes for each of its 1 to 3 parts.  Host only; device
- * as above. */
+ * the forward of few tokens: up to 48; 24, 12 and none of d past 13312, 26624 and
+ * 53248); the backward holds up to 2^28 values of dz, 2 bytes for each of its 1 to 3
+ * parts.  Host only; device as above. */
 moe_status moe_vocab_loss_workspace_size(int32_t T, int32_t d, int32_t V, int32_t dtype, int training, size_t* bytes);
 
 /* Its gradient, the logits formed again:
